@@ -23,6 +23,8 @@ ERR_PLAN = -7
 ERR_NOMEM = -8
 ERR_TIMEOUT = -9
 PLAN_DUP_RECORDS = 1
+SCORINGS = {"softmax": 0, "sigmoid": 1}
+SCOPES = {"rank": 0, "global": 1}
 
 #: every symbol include/moonep.h declares
 EXPORTS = (
@@ -33,7 +35,9 @@ EXPORTS = (
     "moonep_prefetch_weight", "moonep_prefetch_rows", "moonep_reduce_redundant_grad", "moonep_hidden_view",
     "moonep_weight_view", "moonep_get_status", "moonep_strerror", "moonep_num_sms",
     "moonep_plan_noalloc", "moonep_prepare", "moonep_plan_rank", "moonep_dispatch_rank",
-    "moonep_combine_rank",
+    "moonep_combine_rank", "moonep_route", "moonep_route_backward", "moonep_quantize_mx",
+    "moonep_dequantize_mx", "moonep_expert_product", "moonep_gated_act",
+    "moonep_gated_act_backward",
 )
 
 
@@ -78,6 +82,7 @@ def load(path: str = LIB_PATH):
     vp, ci, i64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64
     cfgp = ctypes.POINTER(MoonepConfig)
     planp = ctypes.POINTER(MoonepCommPlan)
+    i32p = ctypes.POINTER(ctypes.c_int32)
     sig = {
         "moonep_query_sizes": (ci, [cfgp, ctypes.POINTER(ci), ctypes.POINTER(ci),
                                     ctypes.POINTER(ctypes.c_size_t)]),
@@ -109,6 +114,13 @@ def load(path: str = LIB_PATH):
                                       ctypes.POINTER(vp), vp]),
         "moonep_combine_rank": (ci, [vp, planp, ci, ctypes.POINTER(vp), ctypes.POINTER(vp),
                                      vp, vp, vp]),
+        "moonep_route": (ci, [vp, vp, ci, ci, ctypes.c_float, ci, i32p, vp, vp, vp, vp, vp, vp]),
+        "moonep_route_backward": (ci, [vp, vp, ci, ci, i32p, vp, vp, vp, vp, vp, vp, vp]),
+        "moonep_quantize_mx": (ci, [vp, vp, ci, i64, i64, vp, vp, vp, vp]),
+        "moonep_dequantize_mx": (ci, [vp, vp, vp, ci, i64, i64, vp, vp]),
+        "moonep_expert_product": (ci, [vp, vp, vp, i64, vp, i64, vp, vp, ci, ci, ci, vp, vp]),
+        "moonep_gated_act": (ci, [vp] * 5 + [ci] + [vp] * 6),
+        "moonep_gated_act_backward": (ci, [vp] * 8 + [ci] + [vp] * 4),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)

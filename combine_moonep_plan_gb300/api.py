@@ -59,6 +59,35 @@ def _check_tensor(t, name, dtype, shape):
     return t.data_ptr()
 
 
+_FLOATS = (torch.float32, torch.bfloat16)
+
+
+def _one_of(t, name, dtypes):
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: expected one of {dtypes}, got {t.dtype}")
+    return t.dtype
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _check_rows(t, name, rows, cols):
+    """A uint8 [rows, cols] tensor whose rows may lie apart: (address, row
+    distance in bytes)."""
+    if t.dtype != torch.uint8:
+        raise TypeError(f"{name}: expected torch.uint8, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a CUDA tensor")
+    if tuple(t.shape) != (rows, cols):
+        raise ValueError(f"{name}: expected shape {(rows, cols)}, got {tuple(t.shape)}")
+    if cols == 0:
+        return None, 0
+    if cols > 1 and t.stride(1) != 1 or rows > 1 and t.stride(0) < cols:
+        raise ValueError(f"{name}: rows must be contiguous and not overlap")
+    return t.data_ptr(), max(t.stride(0), cols) if rows > 1 else cols
+
+
 class CommPlan:
     """A communication plan [MoonEPCommPlan]: device arrays owned by libmoonep."""
 
@@ -103,6 +132,18 @@ class CommPlan:
             self.destroy()
         except Exception:
             pass
+
+
+class Route:
+    """What Buffer.route returns and Buffer.route_backward reads: topk
+    [R, S, K] int32, weights [R, S, K] fp32, tokens_per_expert [R, E] int32,
+    and with a balance loss loss [1] fp32 and coef [R, E] fp32."""
+
+    __slots__ = ("topk", "weights", "tokens_per_expert", "loss", "coef", "scoring", "num_tokens")
+
+    def __init__(self, topk, weights, tokens_per_expert, loss, coef, scoring, num_tokens):
+        self.topk, self.weights, self.tokens_per_expert = topk, weights, tokens_per_expert
+        self.loss, self.coef, self.scoring, self.num_tokens = loss, coef, scoring, num_tokens
 
 
 class Buffer:
@@ -310,6 +351,16 @@ class Buffer:
                                                 _lib.ptr_array(ptrs), arr, _stream()),
               "moonep_prefetch_rows")
 
+    def _token_counts(self, num_tokens):
+        """Per-rank token counts as a host array for the C ABI (None: None)."""
+        if num_tokens is None:
+            return None
+        vals = [int(v) for v in (num_tokens.tolist() if torch.is_tensor(num_tokens)
+                                 else num_tokens)]
+        if len(vals) != self.R:
+            raise ValueError(f"num_tokens: expected {self.R} values")
+        return (ctypes.c_int32 * self.R)(*vals)
+
     def prepare(self, hidden: torch.Tensor | None, topk: torch.Tensor,
                 weights: torch.Tensor | None = None, num_tokens=None,
                 tokens_per_expert: bool = True) -> torch.Tensor | None:
@@ -323,13 +374,7 @@ class Buffer:
         hp = _check_tensor(hidden, "hidden", torch.bfloat16, (R, S, H)) if hidden is not None else None
         tp = _check_tensor(topk, "topk", torch.int32, (R, S, K))
         wp = _check_tensor(weights, "weights", torch.float32, (R, S, K)) if weights is not None else None
-        nt = None
-        if num_tokens is not None:
-            vals = [int(v) for v in (num_tokens.tolist() if torch.is_tensor(num_tokens)
-                                     else num_tokens)]
-            if len(vals) != R:
-                raise ValueError(f"num_tokens: expected {R} values")
-            nt = (ctypes.c_int32 * R)(*vals)
+        nt = self._token_counts(num_tokens)
         tpe = torch.empty((R, self.E), dtype=torch.int32, device="cuda") if tokens_per_expert else None
         check(_lib.load().moonep_prepare(self._ctx, nt, hp, tp, wp,
                                          tpe.data_ptr() if tpe is not None else None, _stream()),
@@ -354,6 +399,203 @@ class Buffer:
         check(_lib.load().moonep_reduce_redundant_grad(
             self._ctx, plan.struct, len(gp), _lib.ptr_array(gp), _lib.ptr_array(sp), HHp,
             _stream()), "moonep_reduce_redundant_grad")
+
+    # ------------------------------------------------------------ router
+    def route(self, logits: torch.Tensor, scoring: str = "softmax", balance: float = 0.0,
+              scope: str = "rank", num_tokens=None) -> Route:
+        """Top-K routing of logits [R, S, E] (fp32 or bf16): the picks (largest
+        logits, equal ones by lowest index), their weights (scores normalised
+        over the picks; scoring "softmax" or "sigmoid"), tokens_per_expert for
+        the planner, and with balance != 0 the balance loss with that factor,
+        per rank ("rank", averaged over the ranks that hold tokens) or over
+        all ranks' tokens ("global").  num_tokens: valid tokens of each rank
+        (host values); later rows get id 0 and weight 0 and stay out of the
+        loss."""
+        R, S, K, E = self.R, self.S, self.K, self.E
+        if scoring not in _lib.SCORINGS:
+            raise ValueError(f"scoring: expected one of {sorted(_lib.SCORINGS)}")
+        if scope not in _lib.SCOPES:
+            raise ValueError(f"scope: expected one of {sorted(_lib.SCOPES)}")
+        lp = _check_tensor(logits, "logits", _one_of(logits, "logits", _FLOATS), (R, S, E))
+        nt = self._token_counts(num_tokens)
+        dev = logits.device
+        topk = torch.empty((R, S, K), dtype=torch.int32, device=dev)
+        weights = torch.empty((R, S, K), dtype=torch.float32, device=dev)
+        tpe = torch.empty((R, E), dtype=torch.int32, device=dev)
+        loss = coef = None
+        if balance:
+            loss = torch.empty((1,), dtype=torch.float32, device=dev)
+            coef = torch.empty((R, E), dtype=torch.float32, device=dev)
+        check(_lib.load().moonep_route(
+            self._ctx, lp, logits.dtype == torch.bfloat16, _lib.SCORINGS[scoring], balance,
+            _lib.SCOPES[scope], nt, topk.data_ptr(), weights.data_ptr(), tpe.data_ptr(),
+            _ptr(coef), _ptr(loss), _stream()), "moonep_route")
+        return Route(topk, weights, tpe, loss, coef, scoring, nt)
+
+    def route_backward(self, route: Route, logits: torch.Tensor,
+                       d_weights: torch.Tensor | None = None,
+                       d_loss: torch.Tensor | None = None,
+                       out: torch.Tensor | None = None) -> torch.Tensor:
+        """Gradient of the logits that `route` was made from: d_weights
+        [R, S, K] fp32 (None: zero) and, when the route has a balance loss,
+        d_loss [1] fp32 (None: 1).  Returns d_logits in the logits' type."""
+        R, S, K, E = self.R, self.S, self.K, self.E
+        lp = _check_tensor(logits, "logits", _one_of(logits, "logits", _FLOATS), (R, S, E))
+        dw = dl = None
+        if d_weights is not None:
+            dw = _check_tensor(d_weights, "d_weights", torch.float32, (R, S, K))
+        if d_loss is not None:
+            dl = _check_tensor(d_loss, "d_loss", torch.float32, (1,))
+        tk = _check_tensor(route.topk, "topk", torch.int32, (R, S, K))
+        wp = _check_tensor(route.weights, "weights", torch.float32, (R, S, K))
+        if out is None:
+            out = torch.empty_like(logits)
+        op = _check_tensor(out, "d_logits", logits.dtype, (R, S, E))
+        check(_lib.load().moonep_route_backward(
+            self._ctx, lp, logits.dtype == torch.bfloat16, _lib.SCORINGS[route.scoring],
+            route.num_tokens, tk, wp, dw, _ptr(route.coef), dl, op, _stream()),
+            "moonep_route_backward")
+        return out
+
+    # ----------------------------------------------------------- experts
+    def _segments(self, cu_seqlens):
+        return _check_tensor(cu_seqlens, "cu_seqlens", torch.int32, (self.R, self.E + self.B))
+
+    def quantize_mx(self, x: torch.Tensor, cu_seqlens: torch.Tensor | None = None,
+                    out: tuple | None = None):
+        """Microscaled 4-bit form of x [..., cols] (bf16 or fp32, cols a
+        multiple of 32): (packed uint8 [..., cols/2], scales uint8
+        [..., cols/32]), as prefetch_weight and expert_product take them.
+        With cu_seqlens (dispatch's), x is [R*NvS, cols] and only the rows of
+        segments are read and written."""
+        xp = _check_tensor(x, "x", _one_of(x, "x", _FLOATS), x.shape)
+        if x.dim() < 1 or x.shape[-1] % 32:
+            raise ValueError("x: the last dimension must be a multiple of 32")
+        lead, cols = x.shape[:-1], x.shape[-1]
+        cu = None
+        if cu_seqlens is not None:
+            cu = self._segments(cu_seqlens)
+            if tuple(lead) != (self.R * self.NvS,):
+                raise ValueError(f"x: expected {self.R * self.NvS} rows with cu_seqlens")
+        if out is None:
+            out = (torch.empty((*lead, cols // 2), dtype=torch.uint8, device=x.device),
+                   torch.empty((*lead, cols // 32), dtype=torch.uint8, device=x.device))
+        packed, scales = out
+        pp = _check_tensor(packed, "packed", torch.uint8, (*lead, cols // 2))
+        sp = _check_tensor(scales, "scales", torch.uint8, (*lead, cols // 32))
+        rows = x.numel() // cols if cols else 0
+        check(_lib.load().moonep_quantize_mx(self._ctx, xp, x.dtype == torch.float32, rows, cols,
+                                              cu, pp, sp, _stream()), "moonep_quantize_mx")
+        return packed, scales
+
+    def dequantize_mx(self, packed: torch.Tensor, scales: torch.Tensor,
+                      dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None):
+        """The values (bf16 or fp32) that a microscaled 4-bit tensor stands for."""
+        if dtype not in _FLOATS:
+            raise TypeError(f"dtype: expected one of {_FLOATS}, got {dtype}")
+        pp = _check_tensor(packed, "packed", torch.uint8, packed.shape)
+        if packed.dim() < 1 or packed.shape[-1] % 16:
+            raise ValueError("packed: the last dimension must be a multiple of 16")
+        lead, cols = packed.shape[:-1], packed.shape[-1] * 2
+        sp = _check_tensor(scales, "scales", torch.uint8, (*lead, cols // 32))
+        if out is None:
+            out = torch.empty((*lead, cols), dtype=dtype, device=packed.device)
+        op = _check_tensor(out, "out", dtype, (*lead, cols))
+        rows = packed.numel() * 2 // cols if cols else 0
+        check(_lib.load().moonep_dequantize_mx(self._ctx, pp, sp, dtype == torch.float32, rows,
+                                                cols, op, _stream()), "moonep_dequantize_mx")
+        return out
+
+    def expert_product(self, rows: tuple, weight: tuple, cu_seqlens: torch.Tensor,
+                       out: torch.Tensor | None = None,
+                       dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+        """Every segment's rows times its expert's weights, both microscaled
+        4-bit: rows (packed [R*NvS, Kd/2], scales [R*NvS, Kd/32]; their rows
+        may lie apart, the packed ones by a multiple of 16 bytes), weight
+        (packed [E + R*B, N, Kd/2], scales [E + R*B, N, Kd/32], slots as
+        prefetch_weight fills them).  Returns out [R*NvS, N] bf16 or fp32;
+        rows outside every segment are not written."""
+        (a, sa), (w, sw) = rows, weight
+        G, n_rows = self.E + self.R * self.B, self.R * self.NvS
+        wp = _check_tensor(w, "weight", torch.uint8, (G, *w.shape[1:]))
+        if w.dim() != 3 or w.shape[2] % 16 or w.shape[1] % 8:
+            raise ValueError("weight: expected [E + R*B, N, Kd/2] with N a multiple of 8 and "
+                             "Kd of 32")
+        N, Kd = w.shape[1], 2 * w.shape[2]
+        swp = _check_tensor(sw, "weight scales", torch.uint8, (G, N, Kd // 32))
+        ap, lda = _check_rows(a, "rows", n_rows, Kd // 2)
+        sap, lds = _check_rows(sa, "row scales", n_rows, Kd // 32)
+        if out is None:
+            if dtype not in _FLOATS:
+                raise TypeError(f"dtype: expected one of {_FLOATS}, got {dtype}")
+            out = torch.empty((n_rows, N), dtype=dtype, device=a.device)
+        op = _check_tensor(out, "out", _one_of(out, "out", _FLOATS), (n_rows, N))
+        check(_lib.load().moonep_expert_product(
+            self._ctx, self._segments(cu_seqlens), ap, lda, sap, lds, wp, swp, N, Kd,
+            out.dtype == torch.float32, op, _stream()), "moonep_expert_product")
+        return out
+
+    def gated_act(self, gate: torch.Tensor, up: torch.Tensor, cu_seqlens: torch.Tensor,
+                  route_weights_nvs: torch.Tensor | None = None, checkpoint: bool = False,
+                  out: torch.Tensor | None = None):
+        """act = w * gate * sigmoid(gate) * up over the rows of segments, gate
+        and up [R*NvS, F] bf16 (F a multiple of 32), w the dispatched route
+        weights [R*NvS] fp32 (None: 1).  Returns (act, checkpoint): with
+        checkpoint=True the 8-bit form of gate and up (two E4M3 code tensors
+        [R*NvS, F] and two E8M0 scale tensors [R*NvS, F/32], uint8) that
+        gated_act_backward reads, so gate and up need not be kept."""
+        n, F = self.R * self.NvS, gate.shape[-1]
+        gp = _check_tensor(gate, "gate", torch.bfloat16, (n, F))
+        up_p = _check_tensor(up, "up", torch.bfloat16, (n, F))
+        if F % 32:
+            raise ValueError("gate: the last dimension must be a multiple of 32")
+        wp = None
+        if route_weights_nvs is not None:
+            wp = _check_tensor(route_weights_nvs, "route_weights_nvs", torch.float32, (n,))
+        if out is None:
+            out = torch.empty_like(gate)
+        op = _check_tensor(out, "act", torch.bfloat16, (n, F))
+        ckpt = None
+        if checkpoint:
+            ckpt = tuple(torch.empty((n, c), dtype=torch.uint8, device=gate.device)
+                         for c in (F, F, F // 32, F // 32))
+        check(_lib.load().moonep_gated_act(
+            self._ctx, self._segments(cu_seqlens), gp, up_p, wp, F, op,
+            *((t.data_ptr() for t in ckpt) if checkpoint else (None,) * 4), _stream()),
+            "moonep_gated_act")
+        return out, ckpt
+
+    def gated_act_backward(self, checkpoint: tuple, d_act: torch.Tensor,
+                           cu_seqlens: torch.Tensor,
+                           route_weights_nvs: torch.Tensor | None = None,
+                           out: tuple | None = None):
+        """Gradients of gated_act from its checkpoint and d_act [R*NvS, F]
+        bf16: (d_gate, d_up) [R*NvS, F] bf16 and, with route weights, their
+        gradient [R*NvS] fp32 (None without), which combine gathers back to
+        [R, S, K].  out: the three tensors to write."""
+        n, F = self.R * self.NvS, d_act.shape[-1]
+        dp = _check_tensor(d_act, "d_act", torch.bfloat16, (n, F))
+        if F % 32:
+            raise ValueError("d_act: the last dimension must be a multiple of 32")
+        if len(checkpoint) != 4:
+            raise ValueError("checkpoint: expected gated_act's four tensors")
+        cp = [_check_tensor(t, f"checkpoint[{i}]", torch.uint8, (n, F if i < 2 else F // 32))
+              for i, t in enumerate(checkpoint)]
+        wp = dwp = None
+        if out is None:
+            out = (torch.empty_like(d_act), torch.empty_like(d_act),
+                   None if route_weights_nvs is None else torch.empty_like(route_weights_nvs))
+        d_gate, d_up, d_w = out
+        gp = _check_tensor(d_gate, "d_gate", torch.bfloat16, (n, F))
+        up_p = _check_tensor(d_up, "d_up", torch.bfloat16, (n, F))
+        if route_weights_nvs is not None:
+            wp = _check_tensor(route_weights_nvs, "route_weights_nvs", torch.float32, (n,))
+        if d_w is not None:
+            dwp = _check_tensor(d_w, "d_weights", torch.float32, (n,))
+        check(_lib.load().moonep_gated_act_backward(
+            self._ctx, self._segments(cu_seqlens), *cp, dp, wp, F, gp, up_p, dwp, _stream()),
+            "moonep_gated_act_backward")
+        return d_gate, d_up, d_w
 
     # ------------------------------------------------- rank-local forms
     # The per-rank shape of the path when each EP rank is its own GPU: one

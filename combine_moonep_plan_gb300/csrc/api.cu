@@ -124,6 +124,9 @@ int moonep_ctx_create(const moonep_config *cfg, int alloc_views, moonep_ctx **ou
   if (e == cudaSuccess && hist) e = cudaMalloc(&ctx->d_hist, hist);
   if (e == cudaSuccess && hist) e = cudaMemset(ctx->d_hist, 0, hist);
   if (e == cudaSuccess && ord) e = cudaMalloc(&ctx->d_ord, ord);
+  if (e == cudaSuccess)
+    e = cudaMalloc(&ctx->d_route,
+                   (size_t)route_scratch_words(c.R, c.E, ctx->sms) * sizeof(int32_t));
   if (e == cudaSuccess && alloc_views) {
     const size_t rows = (size_t)c.R * ctx->NvS;
     e = cudaMalloc(&ctx->d_hidden_view, rows * c.H * sizeof(uint16_t) + 16);
@@ -140,6 +143,7 @@ int moonep_ctx_create(const moonep_config *cfg, int alloc_views, moonep_ctx **ou
     cudaFree(ctx->d_sync);
     cudaFree(ctx->d_hist);
     cudaFree(ctx->d_ord);
+    cudaFree(ctx->d_route);
     cudaFree(ctx->d_hidden_view);
     cudaFree(ctx->d_weight_view);
     free(ctx);
@@ -158,10 +162,11 @@ int moonep_ctx_destroy(moonep_ctx *ctx) {
   ctx->d_sync = nullptr;
   cudaFree(ctx->d_hist);
   cudaFree(ctx->d_ord);
+  cudaFree(ctx->d_route);
   cudaFree(ctx->d_hidden_view);
   cudaFree(ctx->d_weight_view);
   ctx->d_status = nullptr;
-  ctx->d_hist = ctx->d_ord = nullptr;
+  ctx->d_hist = ctx->d_ord = ctx->d_route = nullptr;
   ctx->d_hidden_view = nullptr;
   ctx->d_weight_view = nullptr;
   ctx->destroyed = 1;
@@ -441,6 +446,143 @@ int moonep_reduce_redundant_grad(moonep_ctx *ctx, const moonep_comm_plan *plan, 
   for (int p = 0; p < n_proj; p++)
     if (!Gh[p] || !Gs[p] || !aligned16(Gh[p]) || !aligned16(Gs[p])) return MOONEP_ERR_INVALID_ARG;
   return launch_reduce(ctx, plan, n_proj, Gh, Gs, HHp, (cudaStream_t)stream);
+}
+
+// Host-side token counts: each in [0, S].
+static bool tokens_ok(const moonep_config &c, const int32_t *num_tokens) {
+  if (num_tokens)
+    for (int r = 0; r < c.R; r++)
+      if (num_tokens[r] < 0 || num_tokens[r] > c.S) return false;
+  return true;
+}
+
+static bool aligned4(const void *p) { return ((uintptr_t)p & 3u) == 0; }
+
+int moonep_route(moonep_ctx *ctx, const void *logits, int logits_bf16, int scoring, float balance,
+                 int scope, const int32_t *num_tokens, int32_t *topk, float *w_sk,
+                 int32_t *tokens_per_expert, float *coef, float *loss, void *stream) {
+  int st = check_ctx(ctx);
+  if (st) return st;
+  const moonep_config &c = ctx->cfg;
+  if ((scoring != MOONEP_SCORE_SOFTMAX && scoring != MOONEP_SCORE_SIGMOID) ||
+      (scope != MOONEP_SCOPE_RANK && scope != MOONEP_SCOPE_GLOBAL) || c.K > c.E)
+    return MOONEP_ERR_INVALID_ARG;
+  if (!tokens_per_expert || (c.S > 0 && (!logits || !topk || !w_sk)) ||
+      (coef == nullptr) != (loss == nullptr) || !tokens_ok(c, num_tokens))
+    return MOONEP_ERR_INVALID_ARG;
+  if (!aligned16(logits) || !aligned4(topk) || !aligned4(w_sk) || !aligned4(tokens_per_expert) ||
+      !aligned4(coef) || !aligned4(loss))
+    return MOONEP_ERR_INVALID_ARG;
+  return launch_route(ctx, logits, logits_bf16 != 0, scoring, balance, scope, num_tokens, topk,
+                      w_sk, tokens_per_expert, coef, loss, (cudaStream_t)stream);
+}
+
+int moonep_route_backward(moonep_ctx *ctx, const void *logits, int logits_bf16, int scoring,
+                          const int32_t *num_tokens, const int32_t *topk, const float *w_sk,
+                          const float *d_w_sk, const float *coef, const float *d_loss,
+                          void *d_logits, void *stream) {
+  int st = check_ctx(ctx);
+  if (st) return st;
+  const moonep_config &c = ctx->cfg;
+  if ((scoring != MOONEP_SCORE_SOFTMAX && scoring != MOONEP_SCORE_SIGMOID) || c.K > c.E ||
+      !tokens_ok(c, num_tokens))
+    return MOONEP_ERR_INVALID_ARG;
+  if (c.S == 0) return MOONEP_OK;
+  if (!logits || !topk || !w_sk || !d_logits) return MOONEP_ERR_INVALID_ARG;
+  if (!aligned16(logits) || !aligned16(d_logits) || !aligned4(topk) || !aligned4(w_sk) ||
+      !aligned4(d_w_sk) || !aligned4(coef) || !aligned4(d_loss))
+    return MOONEP_ERR_INVALID_ARG;
+  return launch_route_backward(ctx, logits, logits_bf16 != 0, scoring, num_tokens, topk, w_sk,
+                               d_w_sk, coef, d_loss, d_logits, (cudaStream_t)stream);
+}
+
+// Sizes of a microscaled tensor: whole blocks, and offsets that fit.
+static bool mx_sizes_ok(int64_t rows, int64_t cols) {
+  return rows >= 0 && cols >= 0 && cols % 32 == 0 && cols <= INT32_MAX &&
+         (cols == 0 || rows <= INT64_MAX / 8 / cols);
+}
+
+int moonep_quantize_mx(moonep_ctx *ctx, const void *x, int x_fp32, int64_t rows, int64_t cols,
+                       const int32_t *cu_seqlens, uint8_t *packed, uint8_t *scales,
+                       void *stream) {
+  int st = check_ctx(ctx);
+  if (st) return st;
+  if (!mx_sizes_ok(rows, cols)) return MOONEP_ERR_INVALID_ARG;
+  if (cu_seqlens && (rows != (int64_t)ctx->cfg.R * ctx->NvS || !aligned4(cu_seqlens)))
+    return MOONEP_ERR_INVALID_ARG;
+  if (rows == 0 || cols == 0) return MOONEP_OK;
+  if (!x || !packed || !scales || !aligned16(x) || !aligned16(packed))
+    return MOONEP_ERR_INVALID_ARG;
+  return launch_quantize_mx(ctx, x, x_fp32 != 0, rows, cols, cu_seqlens, packed, scales,
+                            (cudaStream_t)stream);
+}
+
+int moonep_dequantize_mx(moonep_ctx *ctx, const uint8_t *packed, const uint8_t *scales, int y_fp32,
+                         int64_t rows, int64_t cols, void *y, void *stream) {
+  int st = check_ctx(ctx);
+  if (st) return st;
+  if (!mx_sizes_ok(rows, cols)) return MOONEP_ERR_INVALID_ARG;
+  if (rows == 0 || cols == 0) return MOONEP_OK;
+  if (!y || !packed || !scales || !aligned16(y) || !aligned16(packed))
+    return MOONEP_ERR_INVALID_ARG;
+  return launch_dequantize_mx(ctx, packed, scales, y_fp32 != 0, rows, cols, y,
+                              (cudaStream_t)stream);
+}
+
+int moonep_expert_product(moonep_ctx *ctx, const int32_t *cu_seqlens, const uint8_t *a,
+                          int64_t row_bytes, const uint8_t *a_scales, int64_t scale_row_bytes,
+                          const uint8_t *w, const uint8_t *w_scales, int N, int Kd, int out_fp32,
+                          void *out, void *stream) {
+  int st = check_ctx(ctx);
+  if (st) return st;
+  const int64_t groups = (int64_t)ctx->cfg.E + (int64_t)ctx->cfg.R * ctx->cfg.B;
+  if (N < 0 || N % 8 != 0 || Kd < 0 || Kd % 32 != 0 || groups * N > INT32_MAX)
+    return MOONEP_ERR_INVALID_ARG;
+  if (row_bytes < Kd / 2 || row_bytes % 16 != 0 || scale_row_bytes < Kd / 32)
+    return MOONEP_ERR_INVALID_ARG;
+  if (N == 0 || ctx->NvS == 0) return MOONEP_OK;
+  if (!cu_seqlens || !aligned4(cu_seqlens) || !out || !aligned16(out))
+    return MOONEP_ERR_INVALID_ARG;
+  if (Kd > 0 && (!a || !a_scales || !w || !w_scales || !aligned16(a) || !aligned16(w)))
+    return MOONEP_ERR_INVALID_ARG;
+  return launch_product(ctx, cu_seqlens, a, row_bytes, a_scales, scale_row_bytes, w, w_scales, N,
+                        Kd, out, out_fp32 != 0, (cudaStream_t)stream);
+}
+
+int moonep_gated_act(moonep_ctx *ctx, const int32_t *cu_seqlens, const uint16_t *gate,
+                     const uint16_t *up, const float *w_nvs, int F, uint16_t *act, uint8_t *gate8,
+                     uint8_t *up8, uint8_t *gate_scales, uint8_t *up_scales, void *stream) {
+  int st = check_ctx(ctx);
+  if (st) return st;
+  const int given = (gate8 != nullptr) + (up8 != nullptr) + (gate_scales != nullptr) +
+                    (up_scales != nullptr);
+  if (F < 0 || F % 32 != 0 || (given != 0 && given != 4)) return MOONEP_ERR_INVALID_ARG;
+  if (F == 0 || ctx->NvS == 0) return MOONEP_OK;
+  if (!cu_seqlens || !gate || !up || !act || !aligned4(cu_seqlens) || !aligned16(gate) ||
+      !aligned16(up) || !aligned16(act) || !aligned4(w_nvs) || !aligned16(gate8) ||
+      !aligned16(up8))
+    return MOONEP_ERR_INVALID_ARG;
+  return launch_gated(ctx, cu_seqlens, gate, up, w_nvs, F, act, gate8, up8, gate_scales, up_scales,
+                      (cudaStream_t)stream);
+}
+
+int moonep_gated_act_backward(moonep_ctx *ctx, const int32_t *cu_seqlens, const uint8_t *gate8,
+                              const uint8_t *up8, const uint8_t *gate_scales,
+                              const uint8_t *up_scales, const uint16_t *d_act, const float *w_nvs,
+                              int F, uint16_t *d_gate, uint16_t *d_up, float *d_w_nvs,
+                              void *stream) {
+  int st = check_ctx(ctx);
+  if (st) return st;
+  if (F < 0 || F % 32 != 0) return MOONEP_ERR_INVALID_ARG;
+  if (ctx->NvS == 0 || (F == 0 && !d_w_nvs)) return MOONEP_OK;
+  if (!cu_seqlens || !aligned4(cu_seqlens) || !aligned4(d_w_nvs) || !aligned4(w_nvs))
+    return MOONEP_ERR_INVALID_ARG;
+  if (F > 0 && (!gate8 || !up8 || !gate_scales || !up_scales || !d_act || !d_gate || !d_up ||
+                !aligned16(gate8) || !aligned16(up8) || !aligned16(d_act) || !aligned16(d_gate) ||
+                !aligned16(d_up)))
+    return MOONEP_ERR_INVALID_ARG;
+  return launch_gated_backward(ctx, cu_seqlens, gate8, up8, gate_scales, up_scales, d_act, w_nvs,
+                               F, d_gate, d_up, d_w_nvs, (cudaStream_t)stream);
 }
 
 void *moonep_hidden_view(moonep_ctx *ctx, int rank) {

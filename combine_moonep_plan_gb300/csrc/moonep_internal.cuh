@@ -106,6 +106,7 @@ struct moonep_ctx {
   int32_t *d_ord;      // [R*C] ordinal of a route among its tile's routes to the same expert
   uint16_t *d_hidden_view;  // optional [R*NvS, H] bf16
   float *d_weight_view;     // optional [R*NvS] fp32
+  int32_t *d_route;         // moonep_route's per-block sums (route_scratch_words)
   unsigned long long *d_sync;  // [kSyncWords] the planner's counters (kSync*)
   int test_planner_timeout;    // test hook: the planner's arrival wait never completes
   int plan_cluster;            // blocks of the whole-problem planner launched as one
@@ -155,6 +156,31 @@ int launch_prepare(moonep_ctx *ctx, const int32_t *num_tokens, uint16_t *hidden,
                    int32_t *topk, float *w, int32_t *tpe, cudaStream_t st);
 int launch_reduce(moonep_ctx *ctx, const moonep_comm_plan *plan, int n_proj, float *const *Gh,
                   float *const *Gs, int64_t HHp, cudaStream_t st);
+// The router: words of its per-block sums, forward, backward.
+int64_t route_scratch_words(int R, int E, int sms);
+int launch_route(moonep_ctx *ctx, const void *logits, int bf16, int scoring, float alpha, int global,
+                 const int32_t *num_tokens, int32_t *topk, float *w, int32_t *tpe, float *coef,
+                 float *loss, cudaStream_t st);
+int launch_route_backward(moonep_ctx *ctx, const void *logits, int bf16, int scoring,
+                          const int32_t *num_tokens, const int32_t *topk, const float *w,
+                          const float *dw, const float *coef, const float *dloss, void *dz,
+                          cudaStream_t st);
+// Microscaled 4-bit tensors and the experts' product of two of them.
+int launch_quantize_mx(moonep_ctx *ctx, const void *x, int fp32, int64_t rows, int64_t cols,
+                       const int32_t *cu, uint8_t *packed, uint8_t *scales, cudaStream_t st);
+int launch_dequantize_mx(moonep_ctx *ctx, const uint8_t *packed, const uint8_t *scales, int fp32,
+                         int64_t rows, int64_t cols, void *y, cudaStream_t st);
+int launch_product(moonep_ctx *ctx, const int32_t *cu, const uint8_t *rows, int64_t lda,
+                   const uint8_t *row_scales, int64_t lds, const uint8_t *w,
+                   const uint8_t *w_scales, int N, int Kd, void *out, int fp32, cudaStream_t st);
+// The experts' gated activation.
+int launch_gated(moonep_ctx *ctx, const int32_t *cu, const uint16_t *gate, const uint16_t *up,
+                 const float *w, int F, uint16_t *act, uint8_t *g8, uint8_t *u8, uint8_t *gs,
+                 uint8_t *us, cudaStream_t st);
+int launch_gated_backward(moonep_ctx *ctx, const int32_t *cu, const uint8_t *g8, const uint8_t *u8,
+                          const uint8_t *gs, const uint8_t *us, const uint16_t *d_act,
+                          const float *w, int F, uint16_t *d_gate, uint16_t *d_up, float *d_w,
+                          cudaStream_t st);
 // Opt the planner kernels into the dynamic shared memory E experts need.
 cudaError_t plan_configure(int R, int E, int B);
 // Blocks of the single-launch planner when they can run as one thread-block

@@ -38,7 +38,8 @@
  *     scratch and status word, the plan's arrays and the optional zero-copy
  *     buffers behind moonep_hidden_view / moonep_weight_view.
  *   - One context plans one batch at a time: its planner scratch (counters,
- *     per-rank totals) is shared by its moonep_plan calls, so two of them
+ *     per-rank totals) is shared by its moonep_plan calls, and moonep_route's
+ *     scratch by its moonep_route calls, so two of either
  *     must not overlap on the GPU (issue them on one stream, or order the
  *     streams); use one context per concurrent stream.  The copy entry points
  *     keep no state between calls and may overlap freely.
@@ -371,6 +372,112 @@ int moonep_prepare(moonep_ctx *ctx, const int32_t *num_tokens, uint16_t *hidden,
 int moonep_reduce_redundant_grad(moonep_ctx *ctx, const moonep_comm_plan *plan,
                                  int n_proj, float *const *Gh,
                                  float *const *Gs, int64_t HHp, void *stream);
+
+/* The router.  logits [R, S, E] (fp32, or bf16 when logits_bf16) -> for every
+ * valid token (s < num_tokens[r]; num_tokens is a HOST array [R], NULL = S):
+ *   scores  softmax: s_e = exp(z_e - max z), sigmoid: s_e = 1/(1+exp(-z_e));
+ *           p_e = s_e / sum s
+ *   topk [R, S, K]  the K largest logits, largest first, equal ones by lowest
+ *           index (a NaN logit ranks first)
+ *   w_sk [R, S, K]  p of the picks over their sum (0 when every score is 0)
+ * Rows past num_tokens get id 0 and weight 0, as moonep_prepare leaves them.
+ *   tokens_per_expert [R, E]  counts of the written ids (moonep_plan's)
+ * and, when loss is given, the balance loss over the valid tokens' picks
+ * c[r, e] and probability sums P[r, e]:
+ *   MOONEP_SCOPE_RANK    a/R' sum_r sum_e (E c[r,e]/(K n_r)) (P[r,e]/n_r), R'
+ *                        the ranks that hold a token
+ *   MOONEP_SCOPE_GLOBAL  a sum_e (E c[e]/(K T)) (P[e]/T), summed over ranks
+ *   loss [1] fp32, coef [R, E] fp32: the factor of P[r, e] in the loss, which
+ *           moonep_route_backward reads (both given, or both NULL)
+ * Needs K <= E.  Uses the context's scratch: the rule of one batch at a time
+ * covers moonep_route and moonep_plan together.  Results do not depend on
+ * scheduling (sums in a fixed order). */
+#define MOONEP_SCORE_SOFTMAX 0
+#define MOONEP_SCORE_SIGMOID 1
+#define MOONEP_SCOPE_RANK 0
+#define MOONEP_SCOPE_GLOBAL 1
+int moonep_route(moonep_ctx *ctx, const void *logits, int logits_bf16,
+                 int scoring, float balance, int scope,
+                 const int32_t *num_tokens, int32_t *topk, float *w_sk,
+                 int32_t *tokens_per_expert, float *coef, float *loss,
+                 void *stream);
+
+/* Gradient of the logits, in their type, from moonep_route's topk, w_sk and
+ * coef (NULL: no balance loss), d_w_sk [R, S, K] fp32 (NULL: zero) and d_loss
+ * [1] fp32 in device memory (NULL: 1).  The counts are constants of the loss.
+ *   g_e = d_loss p_e (coef_e - sum_j p_j coef_j)
+ *         + [e picked] w_e (d_w_e - sum_k w_k d_w_k)
+ *   d_logits_e = g_e (softmax), g_e (1 - s_e) (sigmoid)
+ * Rows past num_tokens get 0. */
+int moonep_route_backward(moonep_ctx *ctx, const void *logits, int logits_bf16,
+                          int scoring, const int32_t *num_tokens,
+                          const int32_t *topk, const float *w_sk,
+                          const float *d_w_sk, const float *coef,
+                          const float *d_loss, void *d_logits, void *stream);
+
+/* Microscaled 4-bit quantisation (OCP MX v1.0, MXFP4) of x [rows, cols] (bf16,
+ * or fp32 when x_fp32), cols % 32 == 0: every 32 values of a row share the
+ * scale 2^(s - 127), s = floor(log2(largest magnitude)) - 2 + 127 (at least
+ * 0), and become E2M1 codes, rounded to nearest even, saturating at 6.
+ *   packed [rows, cols/2] uint8, value 2i in the low four bits of byte i
+ *   scales [rows, cols/32] uint8 (E8M0)
+ * A block with a NaN or an infinity gets scale 255 (NaN).  With cu_seqlens
+ * (device [R, E+B]), rows must be R*NvS, and only rows that belong to a
+ * segment are read and written. */
+int moonep_quantize_mx(moonep_ctx *ctx, const void *x, int x_fp32, int64_t rows,
+                       int64_t cols, const int32_t *cu_seqlens,
+                       uint8_t *packed, uint8_t *scales, void *stream);
+
+/* The values that codes and scales stand for, y [rows, cols] bf16 (fp32 when
+ * y_fp32). */
+int moonep_dequantize_mx(moonep_ctx *ctx, const uint8_t *packed,
+                         const uint8_t *scales, int y_fp32, int64_t rows,
+                         int64_t cols, void *y, void *stream);
+
+/* The experts' product over the dispatched layout, both sides MXFP4:
+ *   out[row, n] = sum_k A[row, k] W[g, n, k]
+ * for every row of every segment, g the weight row of its segment (home
+ * expert e: e; slot b of rank j: E + j*B + b, as moonep_prefetch_rows fills
+ * them); fp32 accumulation, one rounding to bf16 (none when out_fp32).
+ *   cu_seqlens   device [R, E+B]: the plan's; segments outside [0, NvS) are
+ *                skipped and latch MOONEP_ERR_PLAN
+ *   a            R*NvS rows of Kd/2 packed bytes, row_bytes apart (a multiple
+ *                of 16, at least Kd/2), 16-byte aligned
+ *   a_scales     R*NvS rows of Kd/32 bytes, scale_row_bytes apart
+ *   w, w_scales  dense [E + R*B, N, Kd/2] (16-byte aligned), [E + R*B, N, Kd/32]
+ *   out          [R*NvS, N], 16-byte aligned; other rows are not written
+ * N % 8 == 0, Kd % 32 == 0. */
+int moonep_expert_product(moonep_ctx *ctx, const int32_t *cu_seqlens,
+                          const uint8_t *a, int64_t row_bytes,
+                          const uint8_t *a_scales, int64_t scale_row_bytes,
+                          const uint8_t *w, const uint8_t *w_scales, int N,
+                          int Kd, int out_fp32, void *out, void *stream);
+
+/* The experts' gated activation over the dispatched layout, times the route
+ * weight (combine sums unweighted):
+ *   act[row, f] = w[row] * gate * sigmoid(gate) * up
+ * gate, up, act [R*NvS, F] bf16, F % 32 == 0, w_nvs [R*NvS] fp32 or NULL (1);
+ * fp32 inside, one rounding.  With a checkpoint (all four given, or all
+ * NULL): gate and up as E4M3 codes [R*NvS, F] uint8 with E8M0 scales
+ * [R*NvS, F/32] (largest exponent 8, saturating at 448; otherwise as
+ * moonep_quantize_mx).  Only rows that belong to a segment are read and
+ * written. */
+int moonep_gated_act(moonep_ctx *ctx, const int32_t *cu_seqlens,
+                     const uint16_t *gate, const uint16_t *up,
+                     const float *w_nvs, int F, uint16_t *act, uint8_t *gate8,
+                     uint8_t *up8, uint8_t *gate_scales, uint8_t *up_scales,
+                     void *stream);
+
+/* Backward pass from the checkpoint: the formula's gradient at the gate and
+ * up values that the checkpoint stands for.  d_act [R*NvS, F] bf16 ->
+ * d_gate, d_up [R*NvS, F] bf16 and, when given, d_w_nvs [R*NvS] fp32 (sum
+ * over f in a fixed order), which moonep_combine gathers back to [R, S, K]. */
+int moonep_gated_act_backward(moonep_ctx *ctx, const int32_t *cu_seqlens,
+                              const uint8_t *gate8, const uint8_t *up8,
+                              const uint8_t *gate_scales,
+                              const uint8_t *up_scales, const uint16_t *d_act,
+                              const float *w_nvs, int F, uint16_t *d_gate,
+                              uint16_t *d_up, float *d_w_nvs, void *stream);
 
 /* Zero-copy aliases [API, Buffer.hidden_nvsh_buffer_view and
  * router_weight_buffer_view]: device address of rank `rank`'s [NvS, H] bf16
