@@ -114,6 +114,7 @@ int moonep_ctx_create(const moonep_config *cfg, int alloc_views, moonep_ctx **ou
   ctx->blocks_reduce = occupancy_reduce();
   ctx->blocks_expand = occupancy_dedup(false);
   ctx->blocks_fold = occupancy_dedup(true);
+  ctx->product_clusters = product_clusters(ctx->sms);
   const size_t hist =
       (size_t)plan_scratch_words(c.R, c.E, ctx->C, c.K, ctx->sms_device) * sizeof(int32_t);
   const size_t ord = (size_t)c.R * ctx->C * sizeof(int32_t);
@@ -536,7 +537,7 @@ int moonep_expert_product(moonep_ctx *ctx, const int32_t *cu_seqlens, const uint
   int st = check_ctx(ctx);
   if (st) return st;
   const int64_t groups = (int64_t)ctx->cfg.E + (int64_t)ctx->cfg.R * ctx->cfg.B;
-  if (N < 0 || N % 8 != 0 || Kd < 0 || Kd % 32 != 0 || groups * N > INT32_MAX)
+  if (N < 0 || N % 8 != 0 || Kd < 0 || Kd % 32 != 0 || groups * N > INT32_MAX - 256)
     return MOONEP_ERR_INVALID_ARG;
   if (row_bytes < Kd / 2 || row_bytes % 16 != 0 || scale_row_bytes < Kd / 32)
     return MOONEP_ERR_INVALID_ARG;

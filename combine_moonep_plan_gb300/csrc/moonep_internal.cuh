@@ -108,6 +108,7 @@ struct moonep_ctx {
   float *d_weight_view;     // optional [R*NvS] fp32
   int32_t *d_route;         // moonep_route's per-block sums (route_scratch_words)
   unsigned long long *d_sync;  // [kSyncWords] the planner's counters (kSync*)
+  int product_clusters;        // CTA pairs of the experts' product resident at once
   int test_planner_timeout;    // test hook: the planner's arrival wait never completes
   int plan_cluster;            // blocks of the whole-problem planner launched as one
                                // cluster (0: a cooperative launch)
@@ -170,6 +171,7 @@ int launch_quantize_mx(moonep_ctx *ctx, const void *x, int fp32, int64_t rows, i
                        const int32_t *cu, uint8_t *packed, uint8_t *scales, cudaStream_t st);
 int launch_dequantize_mx(moonep_ctx *ctx, const uint8_t *packed, const uint8_t *scales, int fp32,
                          int64_t rows, int64_t cols, void *y, cudaStream_t st);
+int product_clusters(int sms);  // CTA pairs resident at once on that many SMs (0: none)
 int launch_product(moonep_ctx *ctx, const int32_t *cu, const uint8_t *rows, int64_t lda,
                    const uint8_t *row_scales, int64_t lds, const uint8_t *w,
                    const uint8_t *w_scales, int N, int Kd, void *out, int fp32, cudaStream_t st);

@@ -1,106 +1,694 @@
 // The experts' grouped product: every segment's rows times its expert's
-// weights, both microscaled 4-bit.
+// weights, both microscaled 4-bit, on the block-scaled tensor cores.
 //
-//   out[row, n] = sum_k A[row, k] * W[g, n, k]
+//   out[row, n] = sum_k A[row, k] W[g, n, k]
 // Group g is a weight row of the [E + R*B, N, Kd] tensor: home expert e holds
 // segment e of rank e / (E/R), slot (j, b) is row E + j*B + b and segment E+b
 // of rank j, so groups and segments that can hold rows pair up one to one.
+//
+// The weights are the tensor cores' M side (256 of the N outputs per tile, a
+// pair of SMs with 128 each) and the segment's rows the N side, which comes in
+// steps of 16: segments are ragged and often short (a decode step has a few
+// rows per expert), so the side with the fine step wastes the least.  A
+// segment is cut into equal pieces of at most 192 rows.
+//
+// One persistent pair of CTAs (cluster of two) per pair of SMs; warps:
+//   0      TMA: 256 values of k per stage, 128 weight rows and half the
+//          piece's rows per CTA
+//   1-3    scales: plain [rows, Kd/32] tensors (as prefetch and dispatch move
+//          them) rearranged to the tensor cores' 128 x 4 blocks on the way to
+//          shared memory; each lane loads 16 scales of four rows 32 apart and
+//          so holds whole 16-byte lines of four such blocks
+//   4-7    epilogue: accumulator (lane = output column, TMEM column = row) to
+//          global memory, two neighbouring columns per store
+//   8      MMA, one thread of the pair's first CTA: scales to TMEM, then four
+//          64-deep products per stage
+// Accumulators are double-buffered in TMEM (2 x 192 columns); each of the five
+// shared-memory stages has its own 24 columns of scales, so a stage's scales
+// are only overwritten once its products are done (the stage's barrier).
+// Every wait has a limit of one second, after which the kernel latches
+// MOONEP_ERR_TIMEOUT, drains and returns.
+#include <cuda.h>
+
 #include "moonep_internal.cuh"
 #include "mx_common.cuh"
 
 namespace moonep {
 namespace {
 
-constexpr int kTileRows = 64, kTileCols = 64, kStep = 32;
+constexpr int kThreads = 288;
+constexpr int kStages = 5;
+constexpr int kMaxCols = 192;             // rows of a piece (MMA N)
+constexpr int kTileN = 256;               // outputs per tile (MMA M of the pair)
+constexpr int kStageK = 256;              // values of k per stage (128 bytes)
+constexpr int kBoxRows = 32;              // rows per TMA box of the row side
+constexpr int kABytes = 128 * 128;
+constexpr int kBBytes = 96 * 128;         // half a piece
+constexpr int kSfBytes = 2 * 512 + 4 * 512;  // two weight blocks, four row blocks
+constexpr int kStageBytes = kABytes + kBBytes + kSfBytes;
+constexpr int kSfCols = 24;               // TMEM columns of one stage's scales
+constexpr int kSfBase = 2 * kMaxCols;
+constexpr int kEntries = 1024;            // tile table entries
+constexpr long long kLimitNs = 1000000000LL;
+static_assert(kSfBase + kStages * kSfCols <= 512, "TMEM columns");
+static_assert(kStageBytes % 1024 == 0, "operand tiles start on 1 KB");
+
+struct __align__(1024) Shared {
+  uint8_t stage[kStages][kStageBytes];
+  int32_t last[kEntries];   // tiles up to and including the entry's groups
+  int32_t start[kEntries];  // first row (rank-local) of the entry's one group
+  int32_t rows[kEntries];
+  int32_t wsum[8];
+  uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2];
+  uint32_t tmem;
+  int32_t dead;
+};
 
 struct ProductArgs {
-  const uint8_t *a, *as;  // rows: [.., Kd/2] pitch lda, scales pitch lds
-  const uint8_t *w, *ws;  // [G, N, Kd/2], [G, N, Kd/32]
-  const int32_t *cu;      // [R, EB]
-  void *out;              // [R*NvS, N]
-  int64_t lda, lds;
+  const uint8_t *as, *ws;  // scales: rows (pitch lds), weights [G, N, Kd/32]
+  const int32_t *cu;       // [R, EB]
+  void *out;               // [R*NvS, N]
+  int64_t lds;
   int R, E, B, L, EB, NvS, N, Kd;
+  int groups, per;  // groups, groups per table entry
+  int as16, ws16;   // scale rows are whole aligned 16-byte vectors
   int32_t *status;
 };
 
-// Rows [first, last) of group g in the whole buffer; an offset outside the
-// rank's window is reported and the segment treated as empty.
-__device__ __forceinline__ bool segment(const ProductArgs &a, int g, int64_t *first, int *rows) {
+__device__ __forceinline__ uint32_t smem_addr(const void *p) {
+  return (uint32_t)__cvta_generic_to_shared(p);
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// The same shared address in the pair's first CTA.
+__device__ __forceinline__ uint32_t in_leader(uint32_t a) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(a));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n"
+      " mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ long long now_ns() {
+  long long t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
+}
+// Waits for a phase, at most a second; false (and the CTA marked dead) after
+// that, or once another warp has given up.
+__device__ bool wait(Shared *sh, const void *bar, uint32_t parity, int32_t *status) {
+  const uint32_t b = smem_addr(bar);
+  if (try_wait(b, parity)) return true;
+  const long long t0 = now_ns();
+  while (!try_wait(b, parity)) {
+    if (*(volatile int32_t *)&sh->dead) return false;
+    if (now_ns() - t0 > kLimitNs) {
+      *(volatile int32_t *)&sh->dead = 1;
+      set_status(status, MOONEP_ERR_TIMEOUT);
+      return false;
+    }
+  }
+  return true;
+}
+// The same for a whole warp, with one answer for all its lanes.
+__device__ __forceinline__ bool wait_warp(Shared *sh, const void *bar, uint32_t parity,
+                                          int32_t *status) {
+  int ok = 1;
+  if ((threadIdx.x & 31) == 0) ok = wait(sh, bar, parity, status);
+  ok = __shfl_sync(0xffffffffu, ok, 0);
+  // the phase is over for every lane: it cannot end again before this warp's
+  // own next arrival
+  if (ok) try_wait(smem_addr(bar), parity);
+  return ok != 0;
+}
+__device__ __forceinline__ void arrive_leader(const void *bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                   in_leader(smem_addr(bar)))
+               : "memory");
+}
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, int x, int y,
+                                         uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void commit(const void *bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+      "[%0], %1;" ::"r"(smem_addr(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+// Operand descriptors: rows of 128 bytes, 128-byte swizzle, eight-row groups
+// 1 KB apart; scale blocks of 32 lines of 16 bytes, unswizzled, eight-line
+// groups 128 bytes apart.
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr) {
+  return (uint64_t)((addr >> 4) & 0x3fff) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+__device__ __forceinline__ uint64_t scale_desc(uint32_t addr) {
+  return (uint64_t)((addr >> 4) & 0x3fff) | ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46);
+}
+__device__ __forceinline__ void scales_to_tmem(uint32_t col, uint32_t addr) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(col), "l"(scale_desc(addr))
+               : "memory");
+}
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                    uint32_t sfa, uint32_t sfb, bool add) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %6, 0;\n"
+      " tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], "
+      "[%5], p;\n}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"((uint32_t)add)
+      : "memory");
+}
+
+// Rows [start, start + rows) of group g in its rank's window; offsets outside
+// the window are reported and the segment treated as empty.
+__device__ __forceinline__ bool segment(const ProductArgs &a, int g, int *start, int *rows) {
   const int j = g < a.E ? g / a.L : (g - a.E) / a.B;
   const int x = g < a.E ? g : a.E + (g - a.E) % a.B;
   const int32_t *cu = a.cu + (int64_t)j * a.EB;
   const int lo = x ? cu[x - 1] : 0, hi = cu[x];
   const bool bad = lo < 0 || hi < lo || hi > a.NvS;
-  *first = (int64_t)j * a.NvS + lo;
+  *start = bad ? 0 : lo;
   *rows = bad ? 0 : hi - lo;
   return !bad;
 }
 
-__device__ __forceinline__ void put(float *p, float v) { *p = v; }
-__device__ __forceinline__ void put(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
+__device__ __forceinline__ int pieces(int rows) { return (rows + kMaxCols - 1) / kMaxCols; }
 
-// One block per (64 columns, group): 64-row tiles, fp32 accumulation.
+struct Tile {
+  int g, n0;      // group, first output
+  int64_t row;    // first row in the whole buffer
+  int rows, cols; // valid rows, rows rounded up to 16
+};
+
+// Tile t: the piece of a segment and 256 outputs, outputs fastest.
+__device__ Tile tile_of(const ProductArgs &a, const Shared *sh, int t) {
+  const int nb = (a.N + kTileN - 1) / kTileN;
+  int lo = 0, hi = (a.groups + a.per - 1) / a.per - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (sh->last[mid] > t) hi = mid; else lo = mid + 1;
+  }
+  int rest = t - (lo ? sh->last[lo - 1] : 0);
+  int g = lo * a.per, start = sh->start[lo], rows = sh->rows[lo];
+  if (a.per > 1)
+    for (;; g++) {
+      segment(a, g, &start, &rows);
+      const int n = pieces(rows) * nb;
+      if (rest < n) break;
+      rest -= n;
+    }
+  const int p = pieces(rows), m = rest / nb;
+  const int each = ((rows + p - 1) / p + 15) & ~15;
+  const int j = g < a.E ? g / a.L : (g - a.E) / a.B;
+  Tile o;
+  o.g = g;
+  o.n0 = (rest - m * nb) * kTileN;
+  o.row = (int64_t)j * a.NvS + start + m * each;
+  o.rows = min(each, rows - m * each);
+  o.cols = (o.rows + 15) & ~15;
+  return o;
+}
+
+// The table of tiles; every thread of the CTA takes part.  Returns the count.
+__device__ int build_table(const ProductArgs &a, Shared *sh) {
+  const int nb = (a.N + kTileN - 1) / kTileN;
+  const int entries = (a.groups + a.per - 1) / a.per;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  for (int i = tid; i < kEntries; i += kThreads) {
+    int n = 0, start = 0, rows = 0;
+    if (i < entries)
+      for (int g = i * a.per; g < min(a.groups, (i + 1) * a.per); g++) {
+        if (!segment(a, g, &start, &rows) && blockIdx.x == 0)
+          set_status(a.status, MOONEP_ERR_PLAN);
+        n += pieces(rows) * nb;
+      }
+    sh->last[i] = n;
+    sh->start[i] = start;
+    sh->rows[i] = rows;
+  }
+  __syncthreads();
+  // eight warps scan 128 entries each, four per lane
+  int4 v = make_int4(0, 0, 0, 0);
+  int sum = 0;
+  if (warp < 8) {
+    v = ((const int4 *)sh->last)[tid];
+    v.y += v.x;
+    v.z += v.y;
+    v.w += v.z;
+    sum = v.w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += u;
+    }
+    if (lane == 31) sh->wsum[warp] = sum;
+  }
+  __syncthreads();
+  if (warp < 8) {
+    int base = sum - v.w;
+    for (int i = 0; i < warp; i++) base += sh->wsum[i];
+    ((int4 *)sh->last)[tid] = make_int4(v.x + base, v.y + base, v.z + base, v.w + base);
+  }
+  __syncthreads();
+  return sh->last[kEntries - 1];
+}
+
+// Sixteen scales of one row from column c on, 1.0 past the row's end or for a
+// row that is not there.  Rows of whole aligned vectors load directly; other
+// rows from the aligned words around them, bytes that would lie outside the
+// tensor never touched.
+__device__ __forceinline__ uint4 load_scales(const uint8_t *base, int64_t total, int64_t row,
+                                             int64_t pitch, int c, int n, bool vec, bool there) {
+  const uint32_t one = 0x7f7f7f7fu;
+  uint4 r = make_uint4(one, one, one, one);
+  if (!there || c >= n) return r;
+  const uint8_t *p = base + row * pitch + c;
+  if (vec) return __ldg((const uint4 *)p);
+  const uint32_t shift = (uint32_t)((uintptr_t)p & 3) * 8;
+  const uint8_t *w0 = p - ((uintptr_t)p & 3), *end = base + total;
+  const int need = min(16, n - c);
+  uint32_t w[5];
+#pragma unroll
+  for (int i = 0; i < 5; i++) {
+    const uint8_t *q = w0 + 4 * i;
+    w[i] = 0;
+    if (q >= p + need) continue;
+    if (q >= base && q + 4 <= end) {
+      w[i] = __ldg((const uint32_t *)q);
+    } else {
+#pragma unroll
+      for (int b = 0; b < 4; b++)
+        if (q + b >= base && q + b < end) w[i] |= (uint32_t)__ldg(q + b) << (8 * b);
+    }
+  }
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    const int have = need - 4 * i;
+    const uint32_t keep = have >= 4 ? 0xffffffffu : have <= 0 ? 0u : (1u << (8 * have)) - 1;
+    o[i] = (__funnelshift_r(w[i], w[i + 1], shift) & keep) | (one & ~keep);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+__device__ __forceinline__ uint32_t word(const uint4 &v, int i) {
+  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
+
+// A scale warp: walks (tile, 512 values of k) chunks, two chunks' loads in
+// flight; each chunk fills two stages.
+struct ScaleWalk {
+  int t, c;       // next chunk to load
+  Tile tile;
+};
+
 template <typename T>
-__global__ void __launch_bounds__(256) product_kernel(ProductArgs a) {
+__device__ __forceinline__ void store_pair(T *out, int64_t row, int64_t N, int n, float lo,
+                                           float hi);
+template <>
+__device__ __forceinline__ void store_pair(float *out, int64_t row, int64_t N, int n, float lo,
+                                           float hi) {
+  *(float2 *)(out + row * N + n) = make_float2(lo, hi);
+}
+template <>
+__device__ __forceinline__ void store_pair(__nv_bfloat16 *out, int64_t row, int64_t N, int n,
+                                           float lo, float hi) {
+  *(__nv_bfloat162 *)(out + row * N + n) = __floats2bfloat162_rn(lo, hi);
+}
+
+template <typename T>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    product_kernel(const __grid_constant__ CUtensorMap map_w,
+                   const __grid_constant__ CUtensorMap map_a, const ProductArgs a) {
+  extern __shared__ uint8_t raw[];
+  Shared *sh = (Shared *)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = cluster_rank();
+  const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
+  if (tid == 0) {
+    sh->dead = 0;
+    for (int s = 0; s < kStages; s++) {
+      // full: the leader's expect_tx and three scale warps of each CTA
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], 7;" ::"r"(smem_addr(&sh->full[s])));
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_addr(&sh->empty[s])));
+    }
+    for (int b = 0; b < 2; b++) {
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_addr(&sh->acc_full[b])));
+      // four epilogue warps of each CTA
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], 8;" ::"r"(smem_addr(&sh->acc_empty[b])));
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 8) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                     smem_addr(&sh->tmem))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+  }
   pdl_wait();
   pdl_launch_dependents();
-  __shared__ float sa[kStep][kTileRows + 4], sb[kStep][kTileCols + 4];
-  const int g = blockIdx.y, n0 = blockIdx.x * kTileCols, tid = threadIdx.x;
-  int64_t first;
-  int rows;
-  if (!segment(a, g, &first, &rows)) {
-    if (blockIdx.x == 0 && tid == 0) set_status(a.status, MOONEP_ERR_PLAN);
-    return;
-  }
-  const int tx = tid & 15, ty = tid >> 4;
-  for (int m0 = 0; m0 < rows; m0 += kTileRows) {
-    float acc[4][4] = {};
-    for (int k0 = 0; k0 < a.Kd; k0 += kStep) {
-      // one block of 32 values per row: four threads take eight values each
-      const int r = tid >> 2, c = (tid & 3) * 8;
-      const bool va = m0 + r < rows, vb = n0 + r < a.N;
-      const int64_t ra = first + m0 + r, rb = (int64_t)g * a.N + n0 + r;
-      const uint32_t pa = va ? *(const uint32_t *)(a.a + ra * a.lda + (k0 + c) / 2) : 0u;
-      const uint32_t pb = vb ? *(const uint32_t *)(a.w + (rb * a.Kd + k0 + c) / 2) : 0u;
-      const float fa = va ? mx_value(a.as[ra * a.lds + k0 / 32]) : 0.0f;
-      const float fb = vb ? mx_value(a.ws[(rb * a.Kd + k0) / 32]) : 0.0f;
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < 8; i++) {
-        sa[c + i][r] = mx_e2m1((pa >> (4 * i)) & 15u) * fa;
-        sb[c + i][r] = mx_e2m1((pb >> (4 * i)) & 15u) * fb;
+  const int tiles = build_table(a, sh);
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  cluster_sync();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  const uint32_t tmem = *(volatile uint32_t *)&sh->tmem;
+  const int stages = (a.Kd + kStageK - 1) / kStageK;  // per tile
+
+  if (warp == 0) {
+    if (lane == 0) {
+      uint32_t s = 0, phase = 0, pending = 0;
+      bool ok = true;
+      for (int t = first; t < tiles && ok; t += step) {
+        const Tile tl = tile_of(a, sh, t);
+        const int half = tl.cols >> 1, boxes = (half + kBoxRows - 1) / kBoxRows;
+        const uint32_t bytes = 2u * (kABytes + boxes * (kBoxRows * 128));
+        const int wrow = tl.g * a.N + tl.n0 + (int)rank * 128;
+        const int arow = (int)tl.row + (int)rank * half;
+        for (int k = 0; k < stages; k++) {
+          if (!(ok = wait(sh, &sh->empty[s], phase ^ 1, a.status))) break;
+          const uint32_t base = smem_addr(sh->stage[s]);
+          const uint32_t bar = in_leader(smem_addr(&sh->full[s]));
+          if (rank == 0)
+            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(
+                             smem_addr(&sh->full[s])),
+                         "r"(bytes)
+                         : "memory");
+          tma_load(base, &map_w, k * 128, wrow, bar);
+          for (int b = 0; b < boxes; b++)
+            tma_load(base + kABytes + b * (kBoxRows * 128), &map_a, k * 128, arow + b * kBoxRows,
+                     bar);
+          pending |= 1u << s;
+          if (++s == kStages) {
+            s = 0;
+            phase ^= 1;
+          }
+        }
       }
-      __syncthreads();
+      // given up: the copies in flight end before the CTA does
+      if (!ok && rank == 0)
+        for (int q = 0; q < kStages; q++) {
+          const long long t0 = now_ns();
+          const uint32_t ph = (uint32_t)q < s ? phase : phase ^ 1;
+          if (pending & (1u << q))
+            while (!try_wait(smem_addr(&sh->full[q]), ph) && now_ns() - t0 < kLimitNs / 4) {
+            }
+        }
+    }
+  } else if (warp < 4) {
+    // scale warp 0: the CTA's 128 weight rows; 1, 2: rows 0-127, 128-191
+    const int role = warp - 1, nsc = a.Kd / 32, chunks = (a.Kd + 511) / 512;
+    const bool vec = role ? a.as16 : a.ws16;
+    const uint8_t *base = role ? a.as : a.ws;
+    const int64_t pitch = role ? a.lds : nsc;
+    const int64_t total = role ? ((int64_t)a.R * a.NvS - 1) * a.lds + nsc
+                               : (int64_t)a.groups * a.N * nsc;
+    const uint32_t at = kABytes + kBBytes + (role ? 1024 + (role - 1) * 512 : 0) + lane * 16;
+    uint32_t s = 0, phase = 0;
+    bool ok = true;
+    ScaleWalk w{first, 0, {}};
+    if (first < tiles) w.tile = tile_of(a, sh, first);
+    // loads the walk's chunk and moves on
+    auto load = [&](uint4 v[4]) {
+      if (w.t >= tiles) return;
+      const int lim = role ? w.tile.rows - (role - 1) * 128 : a.N - w.tile.n0 - (int)rank * 128;
+      const int64_t row0 = role ? w.tile.row + (role - 1) * 128
+                                : (int64_t)w.tile.g * a.N + w.tile.n0 + rank * 128;
 #pragma unroll
-      for (int k = 0; k < kStep; k++) {
-        const float4 x = *(const float4 *)&sa[k][ty * 4], y = *(const float4 *)&sb[k][tx * 4];
-        const float xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+      for (int i = 0; i < 4; i++)
+        v[i] = load_scales(base, total, row0 + lane + 32 * i, pitch, w.c * 16, nsc, vec,
+                           lane + 32 * i < lim);
+      if (++w.c == chunks) {
+        w.c = 0;
+        w.t += step;
+        if (w.t < tiles) w.tile = tile_of(a, sh, w.t);
+      }
+    };
+    // writes a chunk's scales into its one or two stages
+    auto fill = [&](const uint4 v[4], int c) {
+      for (int h = 0; h < 2 && c * 2 + h < stages; h++) {
+        if (!(ok = wait_warp(sh, &sh->empty[s], phase ^ 1, a.status))) return;
+        const uint32_t p = smem_addr(sh->stage[s]) + at;
 #pragma unroll
-        for (int i = 0; i < 4; i++)
-#pragma unroll
-          for (int q = 0; q < 4; q++) acc[i][q] += xs[i] * ys[q];
+        for (int i = 0; i < 2; i++) {
+          const uint32_t q = p + i * (role ? 1024 : 512);
+          const uint32_t x = h ? word(v[0], 2 + i) : word(v[0], i);
+          const uint32_t y = h ? word(v[1], 2 + i) : word(v[1], i);
+          const uint32_t z = h ? word(v[2], 2 + i) : word(v[2], i);
+          const uint32_t u = h ? word(v[3], 2 + i) : word(v[3], i);
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(q), "r"(x), "r"(y),
+                       "r"(z), "r"(u)
+                       : "memory");
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) arrive_leader(&sh->full[s]);
+        if (++s == kStages) {
+          s = 0;
+          phase ^= 1;
+        }
+      }
+    };
+    uint4 even[4], odd[4];
+    load(even);
+    load(odd);
+    int c = 0;
+    for (int t = first; t < tiles && ok;) {
+      fill(even, c);
+      load(even);
+      if (++c == chunks) {
+        c = 0;
+        t += step;
+      }
+      if (t >= tiles || !ok) break;
+      fill(odd, c);
+      load(odd);
+      if (++c == chunks) {
+        c = 0;
+        t += step;
       }
     }
+  } else if (warp == 8) {
+    if (lane == 0 && rank == 0) {
+      uint32_t s = 0, phase = 0, it = 0;
+      bool ok = true;
+      for (int t = first; t < tiles && ok; t += step, it++) {
+        const int cols = tile_of(a, sh, t).cols;
+        const uint32_t d = tmem + (it & 1) * kMaxCols;
+        if (!(ok = wait(sh, &sh->acc_empty[it & 1], ((it >> 1) & 1) ^ 1, a.status))) break;
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        // E2M1 both sides, E8M0 scales, M = 256, N = cols
+        const uint32_t idesc = (1u << 7) | (1u << 10) | (1u << 23) | ((uint32_t)(cols >> 3) << 17) |
+                               (16u << 24);
+        const int blocks = (cols + 127) >> 7;
+        for (int k = 0; k < stages; k++) {
+          if (!(ok = wait(sh, &sh->full[s], phase, a.status))) break;
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          const uint32_t base = smem_addr(sh->stage[s]);
+          const uint32_t sf = base + kABytes + kBBytes;
+          const uint32_t ca = tmem + kSfBase + s * kSfCols, cb = ca + 8;
+          const int deep = min(4, (a.Kd - k * kStageK + 63) >> 6);
 #pragma unroll
-    for (int i = 0; i < 4; i++)
+          for (int i = 0; i < 2; i++) {
+            scales_to_tmem(ca + i * 4, sf + i * 512);
+            for (int b = 0; b < blocks; b++)
+              scales_to_tmem(cb + i * 8 + b * 4, sf + 1024 + i * 1024 + b * 512);
+          }
+          const uint64_t da = operand_desc(base), db = operand_desc(base + kABytes);
+          for (int q = 0; q < deep; q++)
+            mma(d, da + 2 * q, db + 2 * q,
+                idesc | ((uint32_t)(q & 1) << 5) | ((uint32_t)(q & 1) << 30), ca + (q >> 1) * 4,
+                cb + (q >> 1) * 8, k + q > 0);
+          commit(&sh->empty[s]);
+          if (++s == kStages) {
+            s = 0;
+            phase ^= 1;
+          }
+        }
+        if (ok) commit(&sh->acc_full[it & 1]);
+      }
+    }
+  } else {
+    // epilogue: lane = output n, accumulator columns = rows
+    const int q = warp & 3;
+    uint32_t it = 0;
+    for (int t = first; t < tiles; t += step, it++) {
+      const Tile tl = tile_of(a, sh, t);
+      if (!wait_warp(sh, &sh->acc_full[it & 1], (it >> 1) & 1, a.status)) break;
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      const uint32_t d = tmem + (it & 1) * kMaxCols + ((uint32_t)(q * 32) << 16);
+      const int n = tl.n0 + (int)rank * 128 + q * 32 + (lane & ~1);
+      const bool odd = lane & 1;
+      for (int c = 0; c < tl.cols; c += 16) {
+        uint32_t v[16];
+        asm volatile(
+            "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, "
+            "%10, %11, %12, %13, %14, %15}, [%16];"
+            : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+              "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]),
+              "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+            : "r"(d + c));
+        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+        // neighbouring lanes swap so that each holds both columns of one row
 #pragma unroll
-      for (int q = 0; q < 4; q++)
-        if (m0 + ty * 4 + i < rows && n0 + tx * 4 + q < a.N)
-          put((T *)a.out + (first + m0 + ty * 4 + i) * a.N + n0 + tx * 4 + q, acc[i][q]);
+        for (int i = 0; i < 16; i += 2) {
+          const float mine = __uint_as_float(odd ? v[i + 1] : v[i]);
+          const float give = __uint_as_float(odd ? v[i] : v[i + 1]);
+          const float got = __shfl_xor_sync(0xffffffffu, give, 1);
+          const int r = c + i + odd;
+          if (n < a.N && r < tl.rows)
+            store_pair((T *)a.out, tl.row + r, a.N, n, odd ? got : mine, odd ? mine : got);
+        }
+      }
+      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) arrive_leader(&sh->acc_empty[it & 1]);
+    }
+  }
+  __syncwarp();
+  // both CTAs are done with each other's memory and with TMEM
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  cluster_sync();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  if (warp == 8)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+}
+
+// A product over no terms: zeros in every segment's rows.
+template <typename T>
+__global__ void __launch_bounds__(256) zero_rows_kernel(const int32_t *cu, T *out, int R, int EB,
+                                                        int NvS, int N) {
+  pdl_wait();
+  pdl_launch_dependents();
+  for (int64_t row = blockIdx.x; row < (int64_t)R * NvS; row += gridDim.x) {
+    const int j = (int)(row / NvS);
+    if (row - (int64_t)j * NvS >= used_rows(cu, j, EB, NvS)) continue;
+    for (int n = threadIdx.x; n < N; n += blockDim.x) out[row * N + n] = T(0.0f);
   }
 }
 
+constexpr size_t kSmem = sizeof(Shared) + 1024;
+
+typedef CUresult (*EncodeFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                             const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                             const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// The driver's tensor-map encoder, looked up once.
+EncodeFn encoder() {
+  static const EncodeFn fn = [] {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess) {
+      cudaGetLastError();
+      p = nullptr;
+    }
+    return (EncodeFn)p;
+  }();
+  return fn;
+}
+
+// Rows of `bytes` packed bytes, `pitch` apart, in boxes of `box` rows x 128
+// bytes.
+bool make_map(CUtensorMap *m, const void *p, int64_t bytes, int64_t rows, int64_t pitch, int box) {
+  const cuuint64_t dims[2] = {(cuuint64_t)bytes, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)pitch};
+  const cuuint32_t boxes[2] = {128, (cuuint32_t)box}, one[2] = {1, 1};
+  return encoder() &&
+         encoder()(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, (void *)p, dims, strides, boxes, one,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace
+
+int product_clusters(int sms) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * (sms / 2 > 0 ? sms / 2 : 1));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = 2;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  int n = 0;
+  for (auto fn : {(const void *)product_kernel<float>, (const void *)product_kernel<__nv_bfloat16>})
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem) !=
+            cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      return 0;
+    }
+  return n < sms / 2 ? n : (sms / 2 > 0 ? sms / 2 : 1);
+}
 
 int launch_product(moonep_ctx *ctx, const int32_t *cu, const uint8_t *rows, int64_t lda,
                    const uint8_t *row_scales, int64_t lds, const uint8_t *w,
                    const uint8_t *w_scales, int N, int Kd, void *out, int fp32, cudaStream_t st) {
   const moonep_config &c = ctx->cfg;
-  ProductArgs a{rows, row_scales, w, w_scales, cu, out, lda, lds, c.R, c.E, c.B, ctx->L,
-                ctx->EB, ctx->NvS, N, Kd, ctx->d_status};
-  const dim3 grid((N + kTileCols - 1) / kTileCols, c.E + c.R * c.B);
+  if (Kd == 0) {
+    if (fp32)
+      return cuda_status(launch_pdl(zero_rows_kernel<float>, dim3(ctx->sms * 4), dim3(256), 0, st,
+                                    false, cu, (float *)out, c.R, ctx->EB, ctx->NvS, N));
+    return cuda_status(launch_pdl(zero_rows_kernel<__nv_bfloat16>, dim3(ctx->sms * 4), dim3(256),
+                                  0, st, false, cu, (__nv_bfloat16 *)out, c.R, ctx->EB, ctx->NvS,
+                                  N));
+  }
+  if (ctx->product_clusters <= 0) return MOONEP_ERR_CUDA;
+  const int64_t groups = (int64_t)c.E + (int64_t)c.R * c.B;
+  CUtensorMap mw, ma;
+  if (!make_map(&mw, w, Kd / 2, groups * N, Kd / 2, 128) ||
+      !make_map(&ma, rows, Kd / 2, (int64_t)c.R * ctx->NvS, lda, kBoxRows))
+    return MOONEP_ERR_CUDA;
+  ProductArgs a{};
+  a.as = row_scales;
+  a.ws = w_scales;
+  a.cu = cu;
+  a.out = out;
+  a.lds = lds;
+  a.R = c.R;
+  a.E = c.E;
+  a.B = c.B;
+  a.L = ctx->L;
+  a.EB = ctx->EB;
+  a.NvS = ctx->NvS;
+  a.N = N;
+  a.Kd = Kd;
+  a.groups = (int)groups;
+  a.per = (int)((groups + kEntries - 1) / kEntries);
+  a.as16 = Kd % 512 == 0 && lds % 16 == 0 && aligned16(row_scales);
+  a.ws16 = Kd % 512 == 0 && aligned16(w_scales);
+  a.status = ctx->d_status;
   auto kern = fp32 ? product_kernel<float> : product_kernel<__nv_bfloat16>;
-  return cuda_status(launch_pdl(kern, grid, dim3(256), 0, st, false, a));
+  return cuda_status(launch_pdl(kern, dim3(2 * ctx->product_clusters), dim3(kThreads), kSmem, st,
+                                false, mw, ma, a));
 }
 
 }  // namespace moonep
