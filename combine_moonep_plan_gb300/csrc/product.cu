@@ -97,7 +97,7 @@ __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n .reg .pred p;\n"
-      " mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+      " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
       " selp.u32 %0, 1, 0, p;\n}"
       : "=r"(ok)
       : "r"(bar), "r"(parity)
@@ -109,35 +109,36 @@ __device__ __forceinline__ long long now_ns() {
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
   return t;
 }
-// Waits for a phase, at most a second; false (and the CTA marked dead) after
-// that, or once another warp has given up.
-__device__ bool wait(Shared *sh, const void *bar, uint32_t parity, int32_t *status) {
-  const uint32_t b = smem_addr(bar);
-  if (try_wait(b, parity)) return true;
+// A whole warp waits for a phase, at most a second; false for every lane (and
+// the CTA marked dead) after that, or once another warp has given up.
+__device__ __noinline__ bool wait_long(Shared *sh, uint32_t bar, uint32_t parity, int32_t *status) {
   const long long t0 = now_ns();
-  while (!try_wait(b, parity)) {
-    if (*(volatile int32_t *)&sh->dead) return false;
-    if (now_ns() - t0 > kLimitNs) {
+  while (!__all_sync(0xffffffffu, try_wait(bar, parity))) {
+    const bool late = now_ns() - t0 > kLimitNs;
+    if (late) {
       *(volatile int32_t *)&sh->dead = 1;
       set_status(status, MOONEP_ERR_TIMEOUT);
-      return false;
     }
+    if (__any_sync(0xffffffffu, late || *(volatile int32_t *)&sh->dead)) return false;
   }
   return true;
 }
-// The same for a whole warp, with one answer for all its lanes.
-__device__ __forceinline__ bool wait_warp(Shared *sh, const void *bar, uint32_t parity,
-                                          int32_t *status) {
-  int ok = 1;
-  if ((threadIdx.x & 31) == 0) ok = wait(sh, bar, parity, status);
-  ok = __shfl_sync(0xffffffffu, ok, 0);
-  // the phase is over for every lane: it cannot end again before this warp's
-  // own next arrival
-  if (ok) try_wait(smem_addr(bar), parity);
-  return ok != 0;
+__device__ __forceinline__ bool wait(Shared *sh, const void *bar, uint32_t parity,
+                                     int32_t *status) {
+  if (__all_sync(0xffffffffu, try_wait(smem_addr(bar), parity))) return true;
+  return wait_long(sh, smem_addr(bar), parity, status);
+}
+// One lane of the warp, the same each time.  The tensor-core and TMA
+// instructions take uniform operands: under this condition, in code that the
+// whole warp walks, they issue directly, where a test of the lane number made
+// the compiler move every operand for each of them (150 cycles per product).
+__device__ __forceinline__ bool elect() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}" : "=r"(p));
+  return p != 0;
 }
 __device__ __forceinline__ void arrive_leader(const void *bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(
                    in_leader(smem_addr(bar)))
                : "memory");
 }
@@ -343,7 +344,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                    const __grid_constant__ CUtensorMap map_a, const ProductArgs a) {
   extern __shared__ uint8_t raw[];
   Shared *sh = (Shared *)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const uint32_t rank = cluster_rank();
   const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
   if (tid == 0) {
@@ -377,45 +379,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int stages = (a.Kd + kStageK - 1) / kStageK;  // per tile
 
   if (warp == 0) {
-    if (lane == 0) {
-      uint32_t s = 0, phase = 0, pending = 0;
-      bool ok = true;
-      for (int t = first; t < tiles && ok; t += step) {
-        const Tile tl = tile_of(a, sh, t);
-        const int half = tl.cols >> 1, boxes = (half + kBoxRows - 1) / kBoxRows;
-        const uint32_t bytes = 2u * (kABytes + boxes * (kBoxRows * 128));
-        const int wrow = tl.g * a.N + tl.n0 + (int)rank * 128;
-        const int arow = (int)tl.row + (int)rank * half;
-        for (int k = 0; k < stages; k++) {
-          if (!(ok = wait(sh, &sh->empty[s], phase ^ 1, a.status))) break;
-          const uint32_t base = smem_addr(sh->stage[s]);
-          const uint32_t bar = in_leader(smem_addr(&sh->full[s]));
+    uint32_t s = 0, phase = 0, pending = 0;
+    bool ok = true;
+    for (int t = first; t < tiles && ok; t += step) {
+      const Tile tl = tile_of(a, sh, t);
+      const int half = tl.cols >> 1, boxes = (half + kBoxRows - 1) / kBoxRows;
+      const uint32_t bytes = 2u * (kABytes + boxes * (kBoxRows * 128));
+      const int wrow = tl.g * a.N + tl.n0 + (int)rank * 128;
+      const int arow = (int)tl.row + (int)rank * half;
+      for (int k = 0; k < stages; k++) {
+        if (!(ok = wait(sh, &sh->empty[s], phase ^ 1, a.status))) break;
+        const uint32_t base = smem_addr(sh->stage[s]);
+        const uint32_t full = smem_addr(&sh->full[s]), bar = in_leader(full);
+        if (elect()) {
           if (rank == 0)
-            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(
-                             smem_addr(&sh->full[s])),
+            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(full),
                          "r"(bytes)
                          : "memory");
           tma_load(base, &map_w, k * 128, wrow, bar);
-          for (int b = 0; b < boxes; b++)
-            tma_load(base + kABytes + b * (kBoxRows * 128), &map_a, k * 128, arow + b * kBoxRows,
-                     bar);
-          pending |= 1u << s;
-          if (++s == kStages) {
-            s = 0;
-            phase ^= 1;
-          }
+#pragma unroll
+          for (int b = 0; b < kMaxCols / 2 / kBoxRows; b++)
+            if (b < boxes)
+              tma_load(base + kABytes + b * (kBoxRows * 128), &map_a, k * 128,
+                       arow + b * kBoxRows, bar);
+        }
+        pending |= 1u << s;
+        if (++s == kStages) {
+          s = 0;
+          phase ^= 1;
         }
       }
-      // given up: the copies in flight end before the CTA does
-      if (!ok && rank == 0)
-        for (int q = 0; q < kStages; q++) {
-          const long long t0 = now_ns();
-          const uint32_t ph = (uint32_t)q < s ? phase : phase ^ 1;
-          if (pending & (1u << q))
-            while (!try_wait(smem_addr(&sh->full[q]), ph) && now_ns() - t0 < kLimitNs / 4) {
-            }
-        }
     }
+    // given up: the copies in flight end before the CTA does
+    if (!ok && rank == 0)
+      for (int q = 0; q < kStages; q++) {
+        const long long t0 = now_ns();
+        const uint32_t ph = (uint32_t)q < s ? phase : phase ^ 1;
+        if (pending & (1u << q))
+          while (!try_wait(smem_addr(&sh->full[q]), ph) && now_ns() - t0 < kLimitNs / 4) {
+          }
+      }
   } else if (warp < 4) {
     // scale warp 0: the CTA's 128 weight rows; 1, 2: rows 0-127, 128-191
     const int role = warp - 1, nsc = a.Kd / 32, chunks = (a.Kd + 511) / 512;
@@ -448,7 +451,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // writes a chunk's scales into its one or two stages
     auto fill = [&](const uint4 v[4], int c) {
       for (int h = 0; h < 2 && c * 2 + h < stages; h++) {
-        if (!(ok = wait_warp(sh, &sh->empty[s], phase ^ 1, a.status))) return;
+        if (!(ok = wait(sh, &sh->empty[s], phase ^ 1, a.status))) return;
         const uint32_t p = smem_addr(sh->stage[s]) + at;
 #pragma unroll
         for (int i = 0; i < 2; i++) {
@@ -490,43 +493,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == 8) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       uint32_t s = 0, phase = 0, it = 0;
       bool ok = true;
+      const uint32_t stage0 = smem_addr(sh->stage[0]);
       for (int t = first; t < tiles && ok; t += step, it++) {
         const int cols = tile_of(a, sh, t).cols;
         const uint32_t d = tmem + (it & 1) * kMaxCols;
         if (!(ok = wait(sh, &sh->acc_empty[it & 1], ((it >> 1) & 1) ^ 1, a.status))) break;
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         // E2M1 both sides, E8M0 scales, M = 256, N = cols
         const uint32_t idesc = (1u << 7) | (1u << 10) | (1u << 23) | ((uint32_t)(cols >> 3) << 17) |
                                (16u << 24);
-        const int blocks = (cols + 127) >> 7;
+        const bool wide = cols > 128;
         for (int k = 0; k < stages; k++) {
           if (!(ok = wait(sh, &sh->full[s], phase, a.status))) break;
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-          const uint32_t base = smem_addr(sh->stage[s]);
+          const uint32_t base = stage0 + s * kStageBytes;
           const uint32_t sf = base + kABytes + kBBytes;
           const uint32_t ca = tmem + kSfBase + s * kSfCols, cb = ca + 8;
-          const int deep = min(4, (a.Kd - k * kStageK + 63) >> 6);
-#pragma unroll
-          for (int i = 0; i < 2; i++) {
-            scales_to_tmem(ca + i * 4, sf + i * 512);
-            for (int b = 0; b < blocks; b++)
-              scales_to_tmem(cb + i * 8 + b * 4, sf + 1024 + i * 1024 + b * 512);
-          }
+          const int deep = (a.Kd - k * kStageK + 63) >> 6;
           const uint64_t da = operand_desc(base), db = operand_desc(base + kABytes);
-          for (int q = 0; q < deep; q++)
-            mma(d, da + 2 * q, db + 2 * q,
-                idesc | ((uint32_t)(q & 1) << 5) | ((uint32_t)(q & 1) << 30), ca + (q >> 1) * 4,
-                cb + (q >> 1) * 8, k + q > 0);
-          commit(&sh->empty[s]);
+          if (elect()) {
+#pragma unroll
+            for (int i = 0; i < 2; i++) {
+              scales_to_tmem(ca + i * 4, sf + i * 512);
+              scales_to_tmem(cb + i * 8, sf + 1024 + i * 1024);
+              if (wide) scales_to_tmem(cb + i * 8 + 4, sf + 1024 + i * 1024 + 512);
+            }
+#pragma unroll
+            for (int q = 0; q < 4; q++)
+              if (q < deep)
+                mma(d, da + 2 * q, db + 2 * q,
+                    idesc | ((uint32_t)(q & 1) << 5) | ((uint32_t)(q & 1) << 30),
+                    ca + (q >> 1) * 4, cb + (q >> 1) * 8, k + q > 0);
+            commit(&sh->empty[s]);
+            if (k == stages - 1) commit(&sh->acc_full[it & 1]);
+          }
           if (++s == kStages) {
             s = 0;
             phase ^= 1;
           }
         }
-        if (ok) commit(&sh->acc_full[it & 1]);
       }
     }
   } else {
@@ -535,7 +542,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint32_t it = 0;
     for (int t = first; t < tiles; t += step, it++) {
       const Tile tl = tile_of(a, sh, t);
-      if (!wait_warp(sh, &sh->acc_full[it & 1], (it >> 1) & 1, a.status)) break;
+      if (!wait(sh, &sh->acc_full[it & 1], (it >> 1) & 1, a.status)) break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       const uint32_t d = tmem + (it & 1) * kMaxCols + ((uint32_t)(q * 32) << 16);
       const int n = tl.n0 + (int)rank * 128 + q * 32 + (lane & ~1);
