@@ -15,14 +15,17 @@
 // One persistent pair of CTAs (cluster of two) per pair of SMs; warps:
 //   0      TMA: 256 values of k per stage, 128 weight rows and half the
 //          piece's rows per CTA
-//   1-3    scales: plain [rows, Kd/32] tensors (as prefetch and dispatch move
+//   1-6    scales: plain [rows, Kd/32] tensors (as prefetch and dispatch move
 //          them) rearranged to the tensor cores' 128 x 4 blocks on the way to
 //          shared memory; each lane loads 16 scales of four rows 32 apart and
-//          so holds whole 16-byte lines of four such blocks
-//   4-7    epilogue: accumulator (lane = output column, TMEM column = row) to
-//          global memory, two neighbouring columns per store
-//   8      MMA, one thread of the pair's first CTA: scales to TMEM, then four
+//          so holds whole 16-byte lines of four such blocks.  Two sets of
+//          three warps take turns: one set needed 600 cycles per stage, twice
+//          the products' time
+//   7      MMA, one thread of the pair's first CTA: scales to TMEM, then four
 //          64-deep products per stage
+//   8-15   epilogue: accumulator (lane = output column, TMEM column = row) to
+//          global memory, two neighbouring columns per store; the two groups
+//          of four warps take alternate 32 rows
 // Accumulators are double-buffered in TMEM (2 x 192 columns); each of the five
 // shared-memory stages has its own 24 columns of scales, so a stage's scales
 // are only overwritten once its products are done (the stage's barrier).
@@ -36,7 +39,7 @@
 namespace moonep {
 namespace {
 
-constexpr int kThreads = 288;
+constexpr int kThreads = 512;
 constexpr int kStages = 5;
 constexpr int kMaxCols = 192;             // rows of a piece (MMA N)
 constexpr int kTileN = 256;               // outputs per tile (MMA M of the pair)
@@ -317,25 +320,22 @@ __device__ __forceinline__ uint32_t word(const uint4 &v, int i) {
   return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
 
-// A scale warp: walks (tile, 512 values of k) chunks, two chunks' loads in
-// flight; each chunk fills two stages.
-struct ScaleWalk {
-  int t, c;       // next chunk to load
-  Tile tile;
-};
-
-template <typename T>
-__device__ __forceinline__ void store_pair(T *out, int64_t row, int64_t N, int n, float lo,
-                                           float hi);
-template <>
-__device__ __forceinline__ void store_pair(float *out, int64_t row, int64_t N, int n, float lo,
-                                           float hi) {
-  *(float2 *)(out + row * N + n) = make_float2(lo, hi);
+__device__ __forceinline__ void store_pair(float *p, float lo, float hi) {
+  *(float2 *)p = make_float2(lo, hi);
 }
-template <>
-__device__ __forceinline__ void store_pair(__nv_bfloat16 *out, int64_t row, int64_t N, int n,
-                                           float lo, float hi) {
-  *(__nv_bfloat162 *)(out + row * N + n) = __floats2bfloat162_rn(lo, hi);
+__device__ __forceinline__ void store_pair(__nv_bfloat16 *p, float lo, float hi) {
+  *(__nv_bfloat162 *)p = __floats2bfloat162_rn(lo, hi);
+}
+
+// 16 accumulator columns of this warp's 32 lanes.
+__device__ __forceinline__ void tmem_load(uint32_t *v, uint32_t addr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, "
+      "%10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+        "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
+        "=r"(v[14]), "=r"(v[15])
+      : "r"(addr));
 }
 
 template <typename T>
@@ -351,18 +351,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     sh->dead = 0;
     for (int s = 0; s < kStages; s++) {
-      // full: the leader's expect_tx and three scale warps of each CTA
+      // full: the leader's expect_tx and one set of scale warps of each CTA
       asm volatile("mbarrier.init.shared::cta.b64 [%0], 7;" ::"r"(smem_addr(&sh->full[s])));
       asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_addr(&sh->empty[s])));
     }
     for (int b = 0; b < 2; b++) {
       asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_addr(&sh->acc_full[b])));
-      // four epilogue warps of each CTA
-      asm volatile("mbarrier.init.shared::cta.b64 [%0], 8;" ::"r"(smem_addr(&sh->acc_empty[b])));
+      // eight epilogue warps of each CTA
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], 16;" ::"r"(smem_addr(&sh->acc_empty[b])));
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 8) {
+  if (warp == 7) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
                      smem_addr(&sh->tmem))
                  : "memory");
@@ -419,9 +419,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           while (!try_wait(smem_addr(&sh->full[q]), ph) && now_ns() - t0 < kLimitNs / 4) {
           }
       }
-  } else if (warp < 4) {
-    // scale warp 0: the CTA's 128 weight rows; 1, 2: rows 0-127, 128-191
-    const int role = warp - 1, nsc = a.Kd / 32, chunks = (a.Kd + 511) / 512;
+  } else if (warp < 7) {
+    // role 0: the CTA's 128 weight rows; 1, 2: the piece's rows 0-127, 128-191.
+    // A warp takes every second chunk (512 values of k, two stages) of the
+    // CTA's sequence of tiles, two of its chunks' loads in flight.
+    const int role = (warp - 1) % 3, turn = (warp - 1) / 3;
+    const int nsc = a.Kd / 32, chunks = (a.Kd + 511) / 512;
     const bool vec = role ? a.as16 : a.ws16;
     const uint8_t *base = role ? a.as : a.ws;
     const int64_t pitch = role ? a.lds : nsc;
@@ -429,70 +432,83 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                : (int64_t)a.groups * a.N * nsc;
     const uint32_t at = kABytes + kBBytes + (role ? 1024 + (role - 1) * 512 : 0) + lane * 16;
     uint32_t s = 0, phase = 0;
-    bool ok = true;
-    ScaleWalk w{first, 0, {}};
-    if (first < tiles) w.tile = tile_of(a, sh, first);
-    // loads the walk's chunk and moves on
+    // moves (tile, chunk) on by n chunks
+    auto move = [&](int &t, int &c, int n) {
+      for (c += n; c >= chunks && t < tiles; c -= chunks) t += step;
+    };
+    int lt = first, lc = 0;  // next chunk to load
+    move(lt, lc, turn);
+    int have = -1;           // tile that `tile` describes
+    Tile tile{};
     auto load = [&](uint4 v[4]) {
-      if (w.t >= tiles) return;
-      const int lim = role ? w.tile.rows - (role - 1) * 128 : a.N - w.tile.n0 - (int)rank * 128;
-      const int64_t row0 = role ? w.tile.row + (role - 1) * 128
-                                : (int64_t)w.tile.g * a.N + w.tile.n0 + rank * 128;
+      if (lt >= tiles) return;
+      if (have != lt) {
+        tile = tile_of(a, sh, lt);
+        have = lt;
+      }
+      const int lim = role ? tile.rows - (role - 1) * 128 : a.N - tile.n0 - (int)rank * 128;
+      const int64_t row0 = role ? tile.row + (role - 1) * 128
+                                : (int64_t)tile.g * a.N + tile.n0 + rank * 128;
 #pragma unroll
       for (int i = 0; i < 4; i++)
-        v[i] = load_scales(base, total, row0 + lane + 32 * i, pitch, w.c * 16, nsc, vec,
+        v[i] = load_scales(base, total, row0 + lane + 32 * i, pitch, lc * 16, nsc, vec,
                            lane + 32 * i < lim);
-      if (++w.c == chunks) {
-        w.c = 0;
-        w.t += step;
-        if (w.t < tiles) w.tile = tile_of(a, sh, w.t);
+      move(lt, lc, 2);
+    };
+    // moves the stage on by n, at most kStages
+    auto skip = [&](int n) {
+      s += n;
+      if (s >= kStages) {
+        s -= kStages;
+        phase ^= 1;
       }
     };
     // writes a chunk's scales into its one or two stages
     auto fill = [&](const uint4 v[4], int c) {
-      for (int h = 0; h < 2 && c * 2 + h < stages; h++) {
-        if (!(ok = wait(sh, &sh->empty[s], phase ^ 1, a.status))) return;
+#pragma unroll
+      for (int h = 0; h < 2; h++) {
+        if (c * 2 + h >= stages) break;
+        if (!wait(sh, &sh->empty[s], phase ^ 1, a.status)) return false;
         const uint32_t p = smem_addr(sh->stage[s]) + at;
 #pragma unroll
-        for (int i = 0; i < 2; i++) {
-          const uint32_t q = p + i * (role ? 1024 : 512);
-          const uint32_t x = h ? word(v[0], 2 + i) : word(v[0], i);
-          const uint32_t y = h ? word(v[1], 2 + i) : word(v[1], i);
-          const uint32_t z = h ? word(v[2], 2 + i) : word(v[2], i);
-          const uint32_t u = h ? word(v[3], 2 + i) : word(v[3], i);
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(q), "r"(x), "r"(y),
-                       "r"(z), "r"(u)
+        for (int i = 0; i < 2; i++)
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                           p + i * (role ? 1024 : 512)),
+                       "r"(word(v[0], 2 * h + i)), "r"(word(v[1], 2 * h + i)),
+                       "r"(word(v[2], 2 * h + i)), "r"(word(v[3], 2 * h + i))
                        : "memory");
-        }
+        // the tensor cores read these lines through the async proxy
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) arrive_leader(&sh->full[s]);
-        if (++s == kStages) {
-          s = 0;
-          phase ^= 1;
-        }
+        skip(1);
+      }
+      return true;
+    };
+    uint4 buf[2][4];
+    load(buf[0]);
+    load(buf[1]);
+    int t = first, c = 0;
+    bool ok = true;
+    // the stages of the chunks before this warp's next one
+    auto pass = [&](int n) {
+      for (int i = 0; i < n && t < tiles; i++) {
+        skip(min(2, stages - 2 * c));
+        move(t, c, 1);
       }
     };
-    uint4 even[4], odd[4];
-    load(even);
-    load(odd);
-    int c = 0;
-    for (int t = first; t < tiles && ok;) {
-      fill(even, c);
-      load(even);
-      if (++c == chunks) {
-        c = 0;
-        t += step;
-      }
-      if (t >= tiles || !ok) break;
-      fill(odd, c);
-      load(odd);
-      if (++c == chunks) {
-        c = 0;
-        t += step;
+    pass(turn);
+    while (t < tiles && ok) {
+#pragma unroll
+      for (int i = 0; i < 2; i++) {
+        if (t >= tiles || !ok) break;
+        ok = fill(buf[i], c);
+        load(buf[i]);
+        move(t, c, 1);
+        pass(1);
       }
     }
-  } else if (warp == 8) {
+  } else if (warp == 7) {
     if (rank == 0) {
       uint32_t s = 0, phase = 0, it = 0;
       bool ok = true;
@@ -538,7 +554,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else {
     // epilogue: lane = output n, accumulator columns = rows
-    const int q = warp & 3;
+    const int q = warp & 3, group = (warp >> 2) & 1;
+    const bool odd = lane & 1;
     uint32_t it = 0;
     for (int t = first; t < tiles; t += step, it++) {
       const Tile tl = tile_of(a, sh, t);
@@ -546,26 +563,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       const uint32_t d = tmem + (it & 1) * kMaxCols + ((uint32_t)(q * 32) << 16);
       const int n = tl.n0 + (int)rank * 128 + q * 32 + (lane & ~1);
-      const bool odd = lane & 1;
-      for (int c = 0; c < tl.cols; c += 16) {
-        uint32_t v[16];
-        asm volatile(
-            "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, "
-            "%10, %11, %12, %13, %14, %15}, [%16];"
-            : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
-              "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]),
-              "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-            : "r"(d + c));
+      const int rows = n < a.N ? tl.rows - odd : 0;
+      T *out = (T *)a.out + (tl.row + odd) * a.N + n;
+      for (int c = group * 32; c < tl.cols; c += 64) {
+        // the last 16 columns of a piece may be another accumulator's: read,
+        // not stored
+        uint32_t v[32];
+        tmem_load(v, d + c);
+        tmem_load(v + 16, d + c + 16);
         asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
         // neighbouring lanes swap so that each holds both columns of one row
 #pragma unroll
-        for (int i = 0; i < 16; i += 2) {
+        for (int i = 0; i < 32; i += 2) {
           const float mine = __uint_as_float(odd ? v[i + 1] : v[i]);
           const float give = __uint_as_float(odd ? v[i] : v[i + 1]);
           const float got = __shfl_xor_sync(0xffffffffu, give, 1);
-          const int r = c + i + odd;
-          if (n < a.N && r < tl.rows)
-            store_pair((T *)a.out, tl.row + r, a.N, n, odd ? got : mine, odd ? mine : got);
+          if (c + i < rows)
+            store_pair(out + (int64_t)(c + i) * a.N, odd ? got : mine, odd ? mine : got);
         }
       }
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -579,7 +593,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   __syncthreads();
   cluster_sync();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-  if (warp == 8)
+  if (warp == 7)
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
