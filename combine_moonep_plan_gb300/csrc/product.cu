@@ -26,6 +26,9 @@
 //   8-15   epilogue: accumulator (lane = output column, TMEM column = row) to
 //          global memory, two neighbouring columns per store; the two groups
 //          of four warps take alternate 32 rows
+//   16     schedule: the CTA's next 32 tiles at a time, one per lane, to shared
+//          memory (every warp working its tiles out itself cost 4000 cycles
+//          per tile)
 // Accumulators are double-buffered in TMEM (2 x 192 columns); each of the five
 // shared-memory stages has its own 24 columns of scales, so a stage's scales
 // are only overwritten once its products are done (the stage's barrier).
@@ -39,12 +42,13 @@
 namespace moonep {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 544;
 constexpr int kStages = 5;
 constexpr int kMaxCols = 192;             // rows of a piece (MMA N)
 constexpr int kTileN = 256;               // outputs per tile (MMA M of the pair)
 constexpr int kStageK = 256;              // values of k per stage (128 bytes)
-constexpr int kBoxRows = 32;              // rows per TMA box of the row side
+constexpr int kBoxRows = 32;              // rows per TMA box of the row side,
+constexpr int kWideRows = kMaxCols / 2;   // or all of half a piece in one
 constexpr int kABytes = 128 * 128;
 constexpr int kBBytes = 96 * 128;         // half a piece
 constexpr int kSfBytes = 2 * 512 + 4 * 512;  // two weight blocks, four row blocks
@@ -62,7 +66,9 @@ struct __align__(1024) Shared {
   int32_t start[kEntries];  // first row (rank-local) of the entry's one group
   int32_t rows[kEntries];
   int32_t wsum[8];
+  int4 tile[2][32];  // the CTA's tiles: group, first output, first row, rows
   uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2];
+  uint64_t tile_full[2], tile_empty[2];
   uint32_t tmem;
   int32_t dead;
 };
@@ -145,6 +151,9 @@ __device__ __forceinline__ void arrive_leader(const void *bar) {
                    in_leader(smem_addr(bar)))
                : "memory");
 }
+__device__ __forceinline__ void arrive(const void *bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
 __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, int x, int y,
                                          uint32_t bar) {
   asm volatile(
@@ -199,14 +208,8 @@ __device__ __forceinline__ bool segment(const ProductArgs &a, int g, int *start,
 
 __device__ __forceinline__ int pieces(int rows) { return (rows + kMaxCols - 1) / kMaxCols; }
 
-struct Tile {
-  int g, n0;      // group, first output
-  int64_t row;    // first row in the whole buffer
-  int rows, cols; // valid rows, rows rounded up to 16
-};
-
 // Tile t: the piece of a segment and 256 outputs, outputs fastest.
-__device__ Tile tile_of(const ProductArgs &a, const Shared *sh, int t) {
+__device__ int4 tile_of(const ProductArgs &a, const Shared *sh, int t) {
   const int nb = (a.N + kTileN - 1) / kTileN;
   int lo = 0, hi = (a.groups + a.per - 1) / a.per - 1;
   while (lo < hi) {
@@ -225,17 +228,12 @@ __device__ Tile tile_of(const ProductArgs &a, const Shared *sh, int t) {
   const int p = pieces(rows), m = rest / nb;
   const int each = ((rows + p - 1) / p + 15) & ~15;
   const int j = g < a.E ? g / a.L : (g - a.E) / a.B;
-  Tile o;
-  o.g = g;
-  o.n0 = (rest - m * nb) * kTileN;
-  o.row = (int64_t)j * a.NvS + start + m * each;
-  o.rows = min(each, rows - m * each);
-  o.cols = (o.rows + 15) & ~15;
-  return o;
+  return make_int4(g, (rest - m * nb) * kTileN, j * a.NvS + start + m * each,
+                   min(each, rows - m * each));
 }
 
 // The table of tiles; every thread of the CTA takes part.  Returns the count.
-__device__ int build_table(const ProductArgs &a, Shared *sh) {
+__device__ __noinline__ int build_table(const ProductArgs &a, Shared *sh) {
   const int nb = (a.N + kTileN - 1) / kTileN;
   const int entries = (a.groups + a.per - 1) / a.per;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -278,32 +276,31 @@ __device__ int build_table(const ProductArgs &a, Shared *sh) {
   return sh->last[kEntries - 1];
 }
 
-// Sixteen scales of one row from column c on, 1.0 past the row's end or for a
-// row that is not there.  Rows of whole aligned vectors load directly; other
-// rows from the aligned words around them, bytes that would lie outside the
-// tensor never touched.
-__device__ __forceinline__ uint4 load_scales(const uint8_t *base, int64_t total, int64_t row,
-                                             int64_t pitch, int c, int n, bool vec, bool there) {
-  const uint32_t one = 0x7f7f7f7fu;
-  uint4 r = make_uint4(one, one, one, one);
-  if (!there || c >= n) return r;
-  const uint8_t *p = base + row * pitch + c;
-  if (vec) return __ldg((const uint4 *)p);
+// Sixteen scale bytes at p, the first `need` of them wanted and 1.0 in place of
+// the others, from the aligned words around them; bytes outside [base, end)
+// are never touched.  Out of line: inlined for every row of every scale warp
+// it made the kernel 150 KB of code, which no instruction cache holds.
+__device__ __noinline__ uint4 load_bytes(const uint8_t *base, const uint8_t *end, const uint8_t *p,
+                                         int need) {
   const uint32_t shift = (uint32_t)((uintptr_t)p & 3) * 8;
-  const uint8_t *w0 = p - ((uintptr_t)p & 3), *end = base + total;
-  const int need = min(16, n - c);
+  const uint8_t *w0 = p - ((uintptr_t)p & 3);
   uint32_t w[5];
 #pragma unroll
   for (int i = 0; i < 5; i++) {
     const uint8_t *q = w0 + 4 * i;
     w[i] = 0;
-    if (q >= p + need) continue;
-    if (q >= base && q + 4 <= end) {
-      w[i] = __ldg((const uint32_t *)q);
-    } else {
+    if (q < p + need && q >= base && q + 4 <= end) w[i] = __ldg((const uint32_t *)q);
+  }
+  if (w0 < base || w0 + 20 > end) {
+    // the tensor's first or last word: what of it lies inside
+    for (int i = 0; i < 20; i++) {
+      const uint8_t *q = w0 + i, *v = w0 + (i & ~3);
+      if (q >= base && q < end && !(v >= base && v + 4 <= end)) {
+        const uint32_t x = (uint32_t)__ldg(q) << (8 * (i & 3));
 #pragma unroll
-      for (int b = 0; b < 4; b++)
-        if (q + b >= base && q + b < end) w[i] |= (uint32_t)__ldg(q + b) << (8 * b);
+        for (int j = 0; j < 5; j++)
+          if (j == i >> 2) w[j] |= x;
+      }
     }
   }
   uint32_t o[4];
@@ -311,9 +308,20 @@ __device__ __forceinline__ uint4 load_scales(const uint8_t *base, int64_t total,
   for (int i = 0; i < 4; i++) {
     const int have = need - 4 * i;
     const uint32_t keep = have >= 4 ? 0xffffffffu : have <= 0 ? 0u : (1u << (8 * have)) - 1;
-    o[i] = (__funnelshift_r(w[i], w[i + 1], shift) & keep) | (one & ~keep);
+    o[i] = (__funnelshift_r(w[i], w[i + 1], shift) & keep) | (0x7f7f7f7fu & ~keep);
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// Sixteen scales of one row from column c on, 1.0 past the row's end or for a
+// row that is not there.  `vec`: rows of whole aligned vectors.
+__device__ __forceinline__ uint4 load_scales(const uint8_t *base, int64_t total, int64_t row,
+                                             int64_t pitch, int c, int n, bool vec, bool there) {
+  const uint32_t one = 0x7f7f7f7fu;
+  if (!there || c >= n) return make_uint4(one, one, one, one);
+  const uint8_t *p = base + row * pitch + c;
+  if (vec) return __ldg((const uint4 *)p);
+  return load_bytes(base, base + total, p, min(16, n - c));
 }
 
 __device__ __forceinline__ uint32_t word(const uint4 &v, int i) {
@@ -325,6 +333,17 @@ __device__ __forceinline__ void store_pair(float *p, float lo, float hi) {
 }
 __device__ __forceinline__ void store_pair(__nv_bfloat16 *p, float lo, float hi) {
   *(__nv_bfloat162 *)p = __floats2bfloat162_rn(lo, hi);
+}
+
+// The i-th tile of this CTA, for a whole warp that reads them in order.
+__device__ __forceinline__ bool next_tile(Shared *sh, int i, int32_t *status, int4 *tile) {
+  if ((i & 31) == 0 && !wait(sh, &sh->tile_full[(i >> 5) & 1], (i >> 6) & 1, status)) return false;
+  *tile = sh->tile[(i >> 5) & 1][i & 31];
+  if ((i & 31) == 31) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) arrive(&sh->tile_empty[(i >> 5) & 1]);
+  }
+  return true;
 }
 
 // 16 accumulator columns of this warp's 32 lanes.
@@ -341,7 +360,8 @@ __device__ __forceinline__ void tmem_load(uint32_t *v, uint32_t addr) {
 template <typename T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     product_kernel(const __grid_constant__ CUtensorMap map_w,
-                   const __grid_constant__ CUtensorMap map_a, const ProductArgs a) {
+                   const __grid_constant__ CUtensorMap map_a,
+                   const __grid_constant__ CUtensorMap map_wide, const ProductArgs a) {
   extern __shared__ uint8_t raw[];
   Shared *sh = (Shared *)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
   const int tid = threadIdx.x, lane = tid & 31;
@@ -356,6 +376,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_addr(&sh->empty[s])));
     }
     for (int b = 0; b < 2; b++) {
+      // read by the TMA, scale and epilogue warps, and the leader's MMA warp
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_addr(&sh->tile_full[b])));
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(&sh->tile_empty[b])),
+                   "r"(rank == 0 ? 16 : 15));
       asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_addr(&sh->acc_full[b])));
       // eight epilogue warps of each CTA
       asm volatile("mbarrier.init.shared::cta.b64 [%0], 16;" ::"r"(smem_addr(&sh->acc_empty[b])));
@@ -377,31 +401,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = *(volatile uint32_t *)&sh->tmem;
   const int stages = (a.Kd + kStageK - 1) / kStageK;  // per tile
+  const int mine = tiles > first ? (tiles - first + step - 1) / step : 0;  // tiles of this pair
 
   if (warp == 0) {
     uint32_t s = 0, phase = 0, pending = 0;
     bool ok = true;
-    for (int t = first; t < tiles && ok; t += step) {
-      const Tile tl = tile_of(a, sh, t);
-      const int half = tl.cols >> 1, boxes = (half + kBoxRows - 1) / kBoxRows;
-      const uint32_t bytes = 2u * (kABytes + boxes * (kBoxRows * 128));
-      const int wrow = tl.g * a.N + tl.n0 + (int)rank * 128;
-      const int arow = (int)tl.row + (int)rank * half;
+    const uint32_t to_leader = in_leader(smem_addr(sh)) - smem_addr(sh);
+    for (int i = 0; i < mine && ok; i++) {
+      int4 tile;
+      if (!(ok = next_tile(sh, i, a.status, &tile))) break;
+      const int half = ((tile.w + 15) & ~15) >> 1;
+      const bool wide = half > 2 * kBoxRows;
+      const int boxes = (half + kBoxRows - 1) / kBoxRows;
+      const uint32_t bytes = 2u * (kABytes + (wide ? kWideRows : boxes * kBoxRows) * 128);
+      const int wrow = tile.x * a.N + tile.y + (int)rank * 128;
+      const int arow = tile.z + (int)rank * half;
       for (int k = 0; k < stages; k++) {
         if (!(ok = wait(sh, &sh->empty[s], phase ^ 1, a.status))) break;
         const uint32_t base = smem_addr(sh->stage[s]);
-        const uint32_t full = smem_addr(&sh->full[s]), bar = in_leader(full);
+        const uint32_t full = smem_addr(&sh->full[s]), bar = full + to_leader;
         if (elect()) {
           if (rank == 0)
             asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(full),
                          "r"(bytes)
                          : "memory");
           tma_load(base, &map_w, k * 128, wrow, bar);
-#pragma unroll
-          for (int b = 0; b < kMaxCols / 2 / kBoxRows; b++)
-            if (b < boxes)
-              tma_load(base + kABytes + b * (kBoxRows * 128), &map_a, k * 128,
-                       arow + b * kBoxRows, bar);
+          if (wide) {
+            tma_load(base + kABytes, &map_wide, k * 128, arow, bar);
+          } else {
+            tma_load(base + kABytes, &map_a, k * 128, arow, bar);
+            if (boxes > 1)
+              tma_load(base + kABytes + kBoxRows * 128, &map_a, k * 128, arow + kBoxRows, bar);
+          }
         }
         pending |= 1u << s;
         if (++s == kStages) {
@@ -432,28 +463,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                : (int64_t)a.groups * a.N * nsc;
     const uint32_t at = kABytes + kBBytes + (role ? 1024 + (role - 1) * 512 : 0) + lane * 16;
     uint32_t s = 0, phase = 0;
-    // moves (tile, chunk) on by n chunks
-    auto move = [&](int &t, int &c, int n) {
-      for (c += n; c >= chunks && t < tiles; c -= chunks) t += step;
-    };
-    int lt = first, lc = 0;  // next chunk to load
-    move(lt, lc, turn);
-    int have = -1;           // tile that `tile` describes
-    Tile tile{};
+    bool ok = true;
+    int li = 0, lc = turn, have = -1;  // tile and chunk to load next; tile in `tile`
+    int4 tile = make_int4(0, 0, 0, 0);
     auto load = [&](uint4 v[4]) {
-      if (lt >= tiles) return;
-      if (have != lt) {
-        tile = tile_of(a, sh, lt);
-        have = lt;
-      }
-      const int lim = role ? tile.rows - (role - 1) * 128 : a.N - tile.n0 - (int)rank * 128;
-      const int64_t row0 = role ? tile.row + (role - 1) * 128
-                                : (int64_t)tile.g * a.N + tile.n0 + rank * 128;
+      for (; lc >= chunks; lc -= chunks) li++;
+      if (!ok) return;
+      for (; have < li && have < mine - 1; have++)
+        if (!(ok = next_tile(sh, have + 1, a.status, &tile))) return;
+      if (li >= mine) return;
+      const int lim = role ? tile.w - (role - 1) * 128 : a.N - tile.y - (int)rank * 128;
+      const int64_t row0 = role ? (int64_t)tile.z + (role - 1) * 128
+                                : (int64_t)tile.x * a.N + tile.y + rank * 128;
 #pragma unroll
       for (int i = 0; i < 4; i++)
         v[i] = load_scales(base, total, row0 + lane + 32 * i, pitch, lc * 16, nsc, vec,
                            lane + 32 * i < lim);
-      move(lt, lc, 2);
+      lc += 2;
     };
     // moves the stage on by n, at most kStages
     auto skip = [&](int n) {
@@ -488,33 +514,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint4 buf[2][4];
     load(buf[0]);
     load(buf[1]);
-    int t = first, c = 0;
-    bool ok = true;
-    // the stages of the chunks before this warp's next one
-    auto pass = [&](int n) {
-      for (int i = 0; i < n && t < tiles; i++) {
-        skip(min(2, stages - 2 * c));
-        move(t, c, 1);
+    int t = 0, c = 0;  // tile and chunk to fill next
+    auto move = [&] {
+      if (++c == chunks) {
+        c = 0;
+        t++;
       }
     };
-    pass(turn);
-    while (t < tiles && ok) {
+    // past the other set's chunk
+    auto pass = [&] {
+      skip(min(2, stages - 2 * c));
+      move();
+    };
+    if (turn) pass();
+    while (t < mine && ok) {
 #pragma unroll
       for (int i = 0; i < 2; i++) {
-        if (t >= tiles || !ok) break;
-        ok = fill(buf[i], c);
+        if (t >= mine || !ok) break;
+        if (!(ok = fill(buf[i], c))) break;
         load(buf[i]);
-        move(t, c, 1);
-        pass(1);
+        move();
+        if (t < mine) pass();
       }
     }
   } else if (warp == 7) {
     if (rank == 0) {
-      uint32_t s = 0, phase = 0, it = 0;
+      uint32_t s = 0, phase = 0;
+      int it = 0;
       bool ok = true;
       const uint32_t stage0 = smem_addr(sh->stage[0]);
-      for (int t = first; t < tiles && ok; t += step, it++) {
-        const int cols = tile_of(a, sh, t).cols;
+      for (; it < mine && ok; it++) {
+        int4 tile;
+        if (!(ok = next_tile(sh, it, a.status, &tile))) break;
+        const int cols = (tile.w + 15) & ~15;
         const uint32_t d = tmem + (it & 1) * kMaxCols;
         if (!(ok = wait(sh, &sh->acc_empty[it & 1], ((it >> 1) & 1) ^ 1, a.status))) break;
         // E2M1 both sides, E8M0 scales, M = 256, N = cols
@@ -552,20 +584,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
     }
-  } else {
+  } else if (warp < 16) {
     // epilogue: lane = output n, accumulator columns = rows
     const int q = warp & 3, group = (warp >> 2) & 1;
     const bool odd = lane & 1;
-    uint32_t it = 0;
-    for (int t = first; t < tiles; t += step, it++) {
-      const Tile tl = tile_of(a, sh, t);
+    for (int it = 0; it < mine; it++) {
+      int4 tile;
+      if (!next_tile(sh, it, a.status, &tile)) break;
       if (!wait(sh, &sh->acc_full[it & 1], (it >> 1) & 1, a.status)) break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       const uint32_t d = tmem + (it & 1) * kMaxCols + ((uint32_t)(q * 32) << 16);
-      const int n = tl.n0 + (int)rank * 128 + q * 32 + (lane & ~1);
-      const int rows = n < a.N ? tl.rows - odd : 0;
-      T *out = (T *)a.out + (tl.row + odd) * a.N + n;
-      for (int c = group * 32; c < tl.cols; c += 64) {
+      const int n = tile.y + (int)rank * 128 + q * 32 + (lane & ~1);
+      const int rows = n < a.N ? tile.w - odd : 0;
+      T *out = (T *)a.out + ((int64_t)tile.z + odd) * a.N + n;
+      for (int c = group * 32; c < tile.w; c += 64) {
         // the last 16 columns of a piece may be another accumulator's: read,
         // not stored
         uint32_t v[32];
@@ -585,6 +617,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
       __syncwarp();
       if (lane == 0) arrive_leader(&sh->acc_empty[it & 1]);
+    }
+  } else {
+    // 32 tiles at a time, two such batches
+    for (int i = 0; i < mine; i += 32) {
+      const int b = (i >> 5) & 1;
+      if (!wait(sh, &sh->tile_empty[b], ((i >> 6) & 1) ^ 1, a.status)) break;
+      if (i + lane < mine) sh->tile[b][lane] = tile_of(a, sh, first + (i + lane) * step);
+      __syncwarp();
+      if (lane == 0) arrive(&sh->tile_full[b]);
     }
   }
   __syncwarp();
@@ -684,9 +725,10 @@ int launch_product(moonep_ctx *ctx, const int32_t *cu, const uint8_t *rows, int6
   }
   if (ctx->product_clusters <= 0) return MOONEP_ERR_CUDA;
   const int64_t groups = (int64_t)c.E + (int64_t)c.R * c.B;
-  CUtensorMap mw, ma;
+  CUtensorMap mw, ma, mwide;
   if (!make_map(&mw, w, Kd / 2, groups * N, Kd / 2, 128) ||
-      !make_map(&ma, rows, Kd / 2, (int64_t)c.R * ctx->NvS, lda, kBoxRows))
+      !make_map(&ma, rows, Kd / 2, (int64_t)c.R * ctx->NvS, lda, kBoxRows) ||
+      !make_map(&mwide, rows, Kd / 2, (int64_t)c.R * ctx->NvS, lda, kWideRows))
     return MOONEP_ERR_CUDA;
   ProductArgs a{};
   a.as = row_scales;
@@ -709,7 +751,7 @@ int launch_product(moonep_ctx *ctx, const int32_t *cu, const uint8_t *rows, int6
   a.status = ctx->d_status;
   auto kern = fp32 ? product_kernel<float> : product_kernel<__nv_bfloat16>;
   return cuda_status(launch_pdl(kern, dim3(2 * ctx->product_clusters), dim3(kThreads), kSmem, st,
-                                false, mw, ma, a));
+                                false, mw, ma, mwide, a));
 }
 
 }  // namespace moonep
