@@ -53,43 +53,54 @@ __device__ __forceinline__ void checkpoint8(const float f[8], uint8_t *codes, ui
   if ((u & 3) == 0) scales[u >> 2] = (uint8_t)s;
 }
 
-// One warp per row.
-template <bool CKPT>
+// Rows of rank blockIdx.y, WPR warps to a row, two units (eight columns) per
+// lane at a time with their loads in flight together.
+template <bool CKPT, int WPR>
 __global__ void __launch_bounds__(kThreads) gated_kernel(GatedArgs a) {
   pdl_wait();
   pdl_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const int64_t rows = (int64_t)a.R * a.NvS;
-  for (int64_t row = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); row < rows;
-       row += (int64_t)gridDim.x * (kThreads / 32)) {
-    const int j = (int)(row / a.NvS);
-    if (row - (int64_t)j * a.NvS >= used_rows(a.cu, j, a.EB, a.NvS)) continue;
-    const float w = a.w ? a.w[row] : 1.0f;
-    for (int c0 = 0; c0 < a.F8; c0 += 32) {
-      const int c = c0 + lane;
-      const bool on = c < a.F8;
-      const int64_t u = row * a.F8 + c;
-      float g[8] = {0, 0, 0, 0, 0, 0, 0, 0}, v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-      if (on) {
-        bf16x8(ld_stream((const uint4 *)a.gate + u), g);
-        bf16x8(ld_stream((const uint4 *)a.up + u), v);
-        float o[8];
+  constexpr int kRows = kThreads / 32 / WPR, kLanes = WPR * 32;
+  const int lane = threadIdx.x % kLanes, sub = threadIdx.x / kLanes;
+  const int used = used_rows(a.cu, blockIdx.y, a.EB, a.NvS);
+  for (int64_t r = (int64_t)blockIdx.x * kRows + sub; r < used; r += (int64_t)gridDim.x * kRows) {
+    const int64_t row = (int64_t)blockIdx.y * a.NvS + r;
+    const float w = a.w ? __ldg(a.w + row) : 1.0f;
+    for (int c0 = 0; c0 < a.F8; c0 += kLanes * 2) {
+      uint4 gv[2] = {}, uv[2] = {};
 #pragma unroll
-        for (int i = 0; i < 8; i++) o[i] = w * (g[i] * sigmoid(g[i]) * v[i]);
-        st_global((uint4 *)a.act + u, to_bf16x8(o));
+      for (int b = 0; b < 2; b++) {
+        const int c = c0 + b * kLanes + lane;
+        if (c < a.F8) {
+          gv[b] = ld_stream((const uint4 *)a.gate + row * a.F8 + c);
+          uv[b] = ld_stream((const uint4 *)a.up + row * a.F8 + c);
+        }
       }
-      if (CKPT) {
-        checkpoint8(g, a.g8, a.gs, u, on);
-        checkpoint8(v, a.u8, a.us, u, on);
+#pragma unroll
+      for (int b = 0; b < 2; b++) {
+        const int c = c0 + b * kLanes + lane;
+        const bool on = c < a.F8;
+        const int64_t u = row * a.F8 + c;
+        float g[8], v[8];
+        bf16x8(gv[b], g);
+        bf16x8(uv[b], v);
+        if (on) {
+          float o[8];
+#pragma unroll
+          for (int i = 0; i < 8; i++) o[i] = w * (g[i] * sigmoid(g[i]) * v[i]);
+          st_global((uint4 *)a.act + u, to_bf16x8(o));
+        }
+        if (CKPT) {
+          checkpoint8(g, a.g8, a.gs, u, on);
+          checkpoint8(v, a.u8, a.us, u, on);
+        }
       }
     }
   }
 }
 
-__device__ __forceinline__ void read8(const uint8_t *codes, const uint8_t *scales, int64_t u,
-                                      float f[8]) {
-  const uint2 c = ((const uint2 *)codes)[u];
-  const float s = mx_value(scales[u >> 2]);
+// Eight checkpointed values from their codes and scale byte.
+__device__ __forceinline__ void read8(uint2 c, uint32_t scale, float f[8]) {
+  const float s = mx_value(scale);
   const uint32_t w[2] = {c.x, c.y};
 #pragma unroll
   for (int i = 0; i < 4; i++) {
@@ -99,36 +110,64 @@ __device__ __forceinline__ void read8(const uint8_t *codes, const uint8_t *scale
   }
 }
 
+template <int WPR>
 __global__ void __launch_bounds__(kThreads) gated_backward_kernel(GatedArgs a) {
   pdl_wait();
   pdl_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const int64_t rows = (int64_t)a.R * a.NvS;
-  for (int64_t row = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); row < rows;
-       row += (int64_t)gridDim.x * (kThreads / 32)) {
-    const int j = (int)(row / a.NvS);
-    if (row - (int64_t)j * a.NvS >= used_rows(a.cu, j, a.EB, a.NvS)) continue;
-    const float w = a.w ? a.w[row] : 1.0f;
+  constexpr int kRows = kThreads / 32 / WPR, kLanes = WPR * 32;
+  __shared__ float part[WPR];
+  const int lane = threadIdx.x % kLanes, sub = threadIdx.x / kLanes;
+  const int used = used_rows(a.cu, blockIdx.y, a.EB, a.NvS);
+  for (int64_t r = (int64_t)blockIdx.x * kRows + sub; r < used; r += (int64_t)gridDim.x * kRows) {
+    const int64_t row = (int64_t)blockIdx.y * a.NvS + r;
+    const float w = a.w ? __ldg(a.w + row) : 1.0f;
     float sum = 0.0f;
-    for (int c = lane; c < a.F8; c += 32) {
-      const int64_t u = row * a.F8 + c;
-      float d[8], g[8], v[8], dg[8], du[8];
-      bf16x8(ld_stream((const uint4 *)a.d_act + u), d);
-      read8(a.g8, a.gs, u, g);
-      read8(a.u8, a.us, u, v);
+    for (int c0 = 0; c0 < a.F8; c0 += kLanes * 2) {
+      uint4 dv[2];
+      uint2 gv[2], uv[2];
+      uint32_t gs[2], us[2];
 #pragma unroll
-      for (int i = 0; i < 8; i++) {
-        const float s = sigmoid(g[i]), gsd = d[i] * (g[i] * s);
-        sum += gsd * v[i];
-        du[i] = w * gsd;
-        dg[i] = w * (d[i] * v[i] * (s * (1.0f + g[i] * (1.0f - s))));
+      for (int b = 0; b < 2; b++) {
+        const int c = c0 + b * kLanes + lane;
+        if (c < a.F8) {
+          const int64_t u = row * a.F8 + c;
+          dv[b] = ld_stream((const uint4 *)a.d_act + u);
+          gv[b] = __ldg((const uint2 *)a.g8 + u);
+          uv[b] = __ldg((const uint2 *)a.u8 + u);
+          gs[b] = __ldg(a.gs + (u >> 2));
+          us[b] = __ldg(a.us + (u >> 2));
+        }
       }
-      st_global((uint4 *)a.d_gate + u, to_bf16x8(dg));
-      st_global((uint4 *)a.d_up + u, to_bf16x8(du));
+#pragma unroll
+      for (int b = 0; b < 2; b++) {
+        const int c = c0 + b * kLanes + lane;
+        if (c >= a.F8) break;
+        const int64_t u = row * a.F8 + c;
+        float d[8], g[8], v[8], dg[8], du[8];
+        bf16x8(dv[b], d);
+        read8(gv[b], gs[b], g);
+        read8(uv[b], us[b], v);
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+          const float s = sigmoid(g[i]), gsd = d[i] * (g[i] * s);
+          sum += gsd * v[i];
+          du[i] = w * gsd;
+          dg[i] = w * (d[i] * v[i] * (s * (1.0f + g[i] * (1.0f - s))));
+        }
+        st_global((uint4 *)a.d_gate + u, to_bf16x8(dg));
+        st_global((uint4 *)a.d_up + u, to_bf16x8(du));
+      }
     }
     if (a.d_w) {
 #pragma unroll
       for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (WPR > 1) {
+        __syncthreads();
+        if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = sum;
+        __syncthreads();
+        sum = 0.0f;
+        for (int i = 0; i < WPR; i++) sum += part[i];
+      }
       if (lane == 0) a.d_w[row] = sum;
     }
   }
@@ -144,10 +183,16 @@ GatedArgs args_of(const moonep_ctx *ctx, const int32_t *cu, int F) {
   return a;
 }
 
-dim3 grid_for(const moonep_ctx *ctx) {
-  const int64_t need = ((int64_t)ctx->cfg.R * ctx->NvS + kThreads / 32 - 1) / (kThreads / 32);
-  const int64_t cap = (int64_t)ctx->sms * 8;
-  return dim3((unsigned)(need < cap ? need : cap));
+// A whole block to a row where one warp to a row would leave SMs without
+// work; otherwise a warp.
+bool few_rows(const moonep_ctx *ctx) {
+  return (int64_t)ctx->cfg.R * ctx->NvS <= (int64_t)ctx->sms * 4;
+}
+
+dim3 grid_for(const moonep_ctx *ctx, int rows_per_block) {
+  const int64_t need = ((int64_t)ctx->NvS + rows_per_block - 1) / rows_per_block;
+  const int64_t cap = ((int64_t)ctx->sms * 8 + ctx->cfg.R - 1) / ctx->cfg.R;
+  return dim3((unsigned)(need < cap ? need : cap), ctx->cfg.R);
 }
 
 }  // namespace
@@ -164,8 +209,11 @@ int launch_gated(moonep_ctx *ctx, const int32_t *cu, const uint16_t *gate, const
   a.u8 = u8;
   a.gs = gs;
   a.us = us;
-  auto kern = g8 ? gated_kernel<true> : gated_kernel<false>;
-  return cuda_status(launch_pdl(kern, grid_for(ctx), dim3(kThreads), 0, st, false, a));
+  const bool few = few_rows(ctx);
+  auto kern = few ? (g8 ? gated_kernel<true, 8> : gated_kernel<false, 8>)
+                  : (g8 ? gated_kernel<true, 1> : gated_kernel<false, 1>);
+  return cuda_status(
+      launch_pdl(kern, grid_for(ctx, few ? 1 : 8), dim3(kThreads), 0, st, false, a));
 }
 
 int launch_gated_backward(moonep_ctx *ctx, const int32_t *cu, const uint8_t *g8, const uint8_t *u8,
@@ -182,8 +230,9 @@ int launch_gated_backward(moonep_ctx *ctx, const int32_t *cu, const uint8_t *g8,
   a.d_gate = d_gate;
   a.d_up = d_up;
   a.d_w = d_w;
-  return cuda_status(
-      launch_pdl(gated_backward_kernel, grid_for(ctx), dim3(kThreads), 0, st, false, a));
+  const bool few = few_rows(ctx);
+  return cuda_status(launch_pdl(few ? gated_backward_kernel<8> : gated_backward_kernel<1>,
+                                grid_for(ctx, few ? 1 : 8), dim3(kThreads), 0, st, false, a));
 }
 
 }  // namespace moonep

@@ -3,7 +3,8 @@
 //
 // Four lanes hold a block, eight values each: one or two 16-byte loads, the
 // block's largest magnitude by two exchanges, one 4-byte store of eight
-// codes, and one lane's scale byte.
+// codes, and one lane's scale byte.  Each thread has four such loads in
+// flight.
 #include "copy_common.cuh"
 #include "moonep_internal.cuh"
 #include "mx_common.cuh"
@@ -13,49 +14,66 @@ namespace {
 
 constexpr int kThreads = 256;
 
+constexpr int kBatch = 4;  // units (eight values) per thread, loads in flight together
+
 struct MxArgs {
   const void *x;        // [rows, cols] bf16 or fp32
   uint8_t *packed;      // [rows, cols / 2]
   uint8_t *scales;      // [rows, cols / 32]
   const int32_t *cu;    // [R, EB] or null: every row
-  int64_t units;        // rows * cols / 8
+  int64_t units;        // all units (no cu), or of one rank's window
   int cols8, EB, NvS;
 };
 
-__device__ __forceinline__ void load8(const __nv_bfloat16 *x, int64_t u, float f[8]) {
-  bf16x8(ld_stream((const uint4 *)x + u), f);
+__device__ __forceinline__ void load8(const __nv_bfloat16 *x, int64_t u, uint4 v[1]) {
+  v[0] = ld_stream((const uint4 *)x + u);
 }
-__device__ __forceinline__ void load8(const float *x, int64_t u, float f[8]) {
-  const uint4 a = ld_stream((const uint4 *)x + 2 * u), b = ld_stream((const uint4 *)x + 2 * u + 1);
-  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+__device__ __forceinline__ void load8(const float *x, int64_t u, uint4 v[2]) {
+  v[0] = ld_stream((const uint4 *)x + 2 * u);
+  v[1] = ld_stream((const uint4 *)x + 2 * u + 1);
+}
+__device__ __forceinline__ void values8(const __nv_bfloat16 *, const uint4 v[1], float f[8]) {
+  bf16x8(v[0], f);
+}
+__device__ __forceinline__ void values8(const float *, const uint4 v[2], float f[8]) {
+  const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
 #pragma unroll
   for (int i = 0; i < 8; i++) f[i] = __uint_as_float(w[i]);
 }
 
+// blockIdx.y: rank (0 without cu).  A rank's used rows are one span of memory
+// from its window's start, walked without regard to rows.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) quantize_kernel(MxArgs a) {
   pdl_wait();
   pdl_launch_dependents();
-  const int64_t step = (int64_t)gridDim.x * kThreads;
-  // the four lanes of a block enter and leave together: units is a multiple
-  // of 4 and so is the step; lanes past the end take part in the exchanges
-  for (int64_t u0 = (int64_t)blockIdx.x * kThreads; u0 < a.units; u0 += step) {
-    const int64_t u = u0 + threadIdx.x;
-    bool on = u < a.units;
-    if (on && a.cu) {
-      const int64_t row = u / a.cols8;
-      const int j = (int)(row / a.NvS);
-      on = row - (int64_t)j * a.NvS < used_rows(a.cu, j, a.EB, a.NvS);
-    }
-    float f[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (on) load8((const T *)a.x, u, f);
-    const uint32_t s = mx_scale<2>(mx_amax(f));
-    if (!on) continue;
-    const float inv = mx_inverse(s);
+  const int j = blockIdx.y;
+  const int64_t n = a.cu ? (int64_t)used_rows(a.cu, j, a.EB, a.NvS) * a.cols8 : a.units;
+  const int64_t first = j * a.units;
+  const T *x = (const T *)a.x + first * 8;
+  uint32_t *packed = (uint32_t *)a.packed + first;
+  uint8_t *scales = a.scales + first / 4;
+  // the four lanes of a block are inside or outside together (n is a multiple
+  // of 4); lanes outside take part in the exchanges
+  for (int64_t u0 = (int64_t)blockIdx.x * (kThreads * kBatch) + threadIdx.x;
+       u0 - threadIdx.x < n; u0 += (int64_t)gridDim.x * (kThreads * kBatch)) {
+    uint4 v[kBatch][sizeof(T) / 2] = {};
 #pragma unroll
-    for (int i = 0; i < 8; i++) f[i] = s == 255u ? 0.0f : f[i] * inv;
-    ((uint32_t *)a.packed)[u] = mx_pack_e2m1(f);
-    if ((threadIdx.x & 3) == 0) a.scales[u >> 2] = (uint8_t)s;
+    for (int b = 0; b < kBatch; b++)
+      if (u0 + b * kThreads < n) load8(x, u0 + b * kThreads, v[b]);
+#pragma unroll
+    for (int b = 0; b < kBatch; b++) {
+      const int64_t u = u0 + b * kThreads;
+      float f[8];
+      values8(x, v[b], f);
+      const uint32_t s = mx_scale<2>(mx_amax(f));
+      if (u >= n) continue;
+      const float inv = mx_inverse(s);
+#pragma unroll
+      for (int i = 0; i < 8; i++) f[i] *= inv;
+      packed[u] = s == 255u ? 0u : mx_pack_e2m1(f);
+      if ((threadIdx.x & 3) == 0) scales[u >> 2] = (uint8_t)s;
+    }
   }
 }
 
@@ -73,36 +91,50 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(const uint8_t *pac
                                                               int64_t units) {
   pdl_wait();
   pdl_launch_dependents();
-  for (int64_t u = (int64_t)blockIdx.x * kThreads + threadIdx.x; u < units;
-       u += (int64_t)gridDim.x * kThreads) {
-    const uint32_t w = ((const uint32_t *)packed)[u];
-    const float s = mx_value(scales[u >> 2]);
-    float f[8];
+  for (int64_t u0 = (int64_t)blockIdx.x * (kThreads * kBatch) + threadIdx.x; u0 < units;
+       u0 += (int64_t)gridDim.x * (kThreads * kBatch)) {
+    uint32_t w[kBatch] = {}, s[kBatch] = {};
 #pragma unroll
-    for (int i = 0; i < 8; i++) f[i] = mx_e2m1((w >> (4 * i)) & 15u) * s;
-    store8(y, u, f);
+    for (int b = 0; b < kBatch; b++)
+      if (u0 + b * kThreads < units) {
+        w[b] = __ldg((const uint32_t *)packed + u0 + b * kThreads);
+        s[b] = __ldg(scales + ((u0 + b * kThreads) >> 2));
+      }
+#pragma unroll
+    for (int b = 0; b < kBatch; b++) {
+      if (u0 + b * kThreads >= units) break;
+      const float v = mx_value(s[b]);
+      float f[8];
+      mx_e2m1x8(w[b], f);
+#pragma unroll
+      for (int i = 0; i < 8; i++) f[i] *= v;
+      store8(y, u0 + b * kThreads, f);
+    }
   }
 }
 
-unsigned grid_for(const moonep_ctx *ctx, int64_t units) {
-  const int64_t need = (units + kThreads - 1) / kThreads, cap = (int64_t)ctx->sms * 8;
-  return (unsigned)(need < cap ? need : cap);
+// Blocks for so many units in each of `spans` equal spans.
+dim3 grid_for(const moonep_ctx *ctx, int64_t units, int spans) {
+  const int64_t need = (units + kThreads * kBatch - 1) / (kThreads * kBatch);
+  const int64_t cap = ((int64_t)ctx->sms * 8 + spans - 1) / spans;
+  return dim3((unsigned)(need < cap ? need : cap), spans);
 }
 
 }  // namespace
 
 int launch_quantize_mx(moonep_ctx *ctx, const void *x, int fp32, int64_t rows, int64_t cols,
                        const int32_t *cu, uint8_t *packed, uint8_t *scales, cudaStream_t st) {
-  MxArgs a{x, packed, scales, cu, rows * (cols / 8), (int)(cols / 8), ctx->EB, ctx->NvS};
+  const int spans = cu ? ctx->cfg.R : 1;
+  MxArgs a{x, packed, scales, cu, rows / spans * (cols / 8), (int)(cols / 8), ctx->EB, ctx->NvS};
   auto kern = fp32 ? quantize_kernel<float> : quantize_kernel<__nv_bfloat16>;
   return cuda_status(
-      launch_pdl(kern, dim3(grid_for(ctx, a.units)), dim3(kThreads), 0, st, false, a));
+      launch_pdl(kern, grid_for(ctx, a.units, spans), dim3(kThreads), 0, st, false, a));
 }
 
 int launch_dequantize_mx(moonep_ctx *ctx, const uint8_t *packed, const uint8_t *scales, int fp32,
                          int64_t rows, int64_t cols, void *y, cudaStream_t st) {
   const int64_t units = rows * (cols / 8);
-  const dim3 grid(grid_for(ctx, units));
+  const dim3 grid = grid_for(ctx, units, 1);
   if (fp32)
     return cuda_status(launch_pdl(dequantize_kernel<float>, grid, dim3(kThreads), 0, st, false,
                                   packed, scales, (float *)y, units));

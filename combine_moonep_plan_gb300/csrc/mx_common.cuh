@@ -35,6 +35,13 @@ __device__ __forceinline__ float mx_value(uint32_t s) {
                    : (s ? __uint_as_float(s << 23) : __uint_as_float(0x00400000u));
 }
 
+// A pair of half-precision values as fp32.
+__device__ __forceinline__ void mx_half2(uint32_t h, float *lo, float *hi) {
+  asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.f32.f16 %0, a;\n cvt.f32.f16 %1, b;\n}"
+      : "=f"(*lo), "=f"(*hi)
+      : "r"(h));
+}
+
 // Eight values as packed E2M1 codes, value 0 in the lowest four bits.
 __device__ __forceinline__ uint32_t mx_pack_e2m1(const float v[8]) {
   uint32_t r;
@@ -49,12 +56,16 @@ __device__ __forceinline__ uint32_t mx_pack_e2m1(const float v[8]) {
   return r;
 }
 
-// E2M1 code (0..15) as fp32.
-__device__ __forceinline__ float mx_e2m1(uint32_t c) {
-  const uint32_t m = c & 7u;
-  // 0, 0.5 as they are; otherwise exponent m >> 1, mantissa m & 1
-  const float a = m < 2u ? 0.5f * (float)m : __uint_as_float(((126u + (m >> 1)) << 23) | ((m & 1u) << 22));
-  return (c & 8u) ? -a : a;
+// Eight packed E2M1 codes as fp32, through half precision.
+__device__ __forceinline__ void mx_e2m1x8(uint32_t w, float f[8]) {
+  uint32_t h[4];
+  asm("{\n .reg .b8 a, b, c, d;\n mov.b32 {a, b, c, d}, %4;\n"
+      " cvt.rn.f16x2.e2m1x2 %0, a;\n cvt.rn.f16x2.e2m1x2 %1, b;\n"
+      " cvt.rn.f16x2.e2m1x2 %2, c;\n cvt.rn.f16x2.e2m1x2 %3, d;\n}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+#pragma unroll
+  for (int i = 0; i < 4; i++) mx_half2(h[i], &f[2 * i], &f[2 * i + 1]);
 }
 
 // Four values as E4M3 codes, value 0 in the lowest byte.
@@ -74,11 +85,9 @@ __device__ __forceinline__ uint32_t mx_pack_e4m3(float v0, float v1, float v2, f
 __device__ __forceinline__ float2 mx_e4m3x2(uint32_t c) {
   uint32_t h;
   asm("{\n .reg .b16 a;\n cvt.u16.u32 a, %1;\n cvt.rn.f16x2.e4m3x2 %0, a;\n}" : "=r"(h) : "r"(c));
-  float lo, hi;
-  asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.f32.f16 %0, a;\n cvt.f32.f16 %1, b;\n}"
-      : "=f"(lo), "=f"(hi)
-      : "r"(h));
-  return make_float2(lo, hi);
+  float2 f;
+  mx_half2(h, &f.x, &f.y);
+  return f;
 }
 
 // Eight bf16 values of a 16-byte vector as fp32.

@@ -20,24 +20,24 @@
 #include <cuda_bf16.h>
 
 #include "moonep_internal.cuh"
+#include "mx_common.cuh"
 
 namespace moonep {
 namespace {
 
 constexpr int kWarps = 8;
+constexpr int kCluster = 8;  // blocks that add up their sums before they leave
 
 struct RouteArgs {
   const void *logits;  // [R, S, E] fp32 or bf16
   int32_t *topk;       // [R, S, K]
   float *w;            // [R, S, K]
-  float *part_p;       // [R, bpr, E] sums of p of one block's tokens, or null
-  int32_t *part_c;     // [R, bpr, E] picks of one block's tokens
-  int R, S, E, K, bpr, sigmoid;
+  float *part_p;       // [R, parts, E] sums of p of one cluster's tokens, or null
+  int32_t *part_c;     // [R, parts, E] picks of one cluster's tokens
+  int32_t *tpe;        // [R, E], written here when a rank has one cluster and no loss
+  int R, S, E, K, sigmoid, cluster;
   int32_t ntok[kMaxRanks];
 };
-
-__device__ __forceinline__ float to_f(float v) { return v; }
-__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
 
 // Order-preserving bits: a larger logit has a larger key, -0 equals +0, NaN
 // is largest; 0 is below every logit.
@@ -47,27 +47,297 @@ __device__ __forceinline__ uint32_t order_key(float v) {
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
+// The logit of a key (NaN for the NaN key).
+__device__ __forceinline__ float key_value(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? k & 0x7fffffffu : ~k);
+}
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
 
-// Score of one logit; m is the row's maximum (softmax).
-__device__ __forceinline__ float score(float z, float m, bool sigmoid) {
-  if (sigmoid) return 1.0f / (1.0f + expf(-z));
-  return m == -INFINITY ? 0.0f : expf(z - m);
+// Sum over the LP lanes that share a token.
+template <int LP>
+__device__ __forceinline__ float group_sum(float v) {
+#pragma unroll
+  for (int o = LP / 2; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
 }
 
-// One warp per token, any E: the row in shared memory.
+// Score of one logit; m is the row's maximum (softmax).
+__device__ __forceinline__ float score(float z, float m, bool sigmoid) {
+  if (sigmoid) return __fdividef(1.0f, 1.0f + __expf(-z));
+  return m == -INFINITY ? 0.0f : __expf(z - m);
+}
+
+__device__ __forceinline__ float to_f(float v) { return v; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
+
+// V logits of a row from column c on; -inf past the row's end.  `vec`: rows
+// are whole aligned vectors.
+template <int V>
+__device__ __forceinline__ void load_row(const float *z, int c, int E, bool vec, float f[V]) {
+  if (V % 4 == 0 && vec) {
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+      const float4 v = c + i < E ? __ldg((const float4 *)(z + c + i))
+                                 : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      f[i] = v.x;
+      f[i + 1] = v.y;
+      f[i + 2] = v.z;
+      f[i + 3] = v.w;
+    }
+    return;
+  }
+  if (V == 2 && vec) {
+    const float2 v = c < E ? __ldg((const float2 *)(z + c)) : make_float2(-INFINITY, -INFINITY);
+    f[0] = v.x;
+    f[V - 1] = v.y;
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < V; i++) f[i] = c + i < E ? __ldg(z + c + i) : -INFINITY;
+}
+template <int V>
+__device__ __forceinline__ void load_row(const __nv_bfloat16 *z, int c, int E, bool vec,
+                                         float f[V]) {
+  if (V % 8 == 0 && vec) {
+#pragma unroll
+    for (int i = 0; i < V; i += 8) {
+      if (c + i < E) {
+        bf16x8(__ldg((const uint4 *)(z + c + i)), f + i);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; j++) f[i + j] = -INFINITY;
+      }
+    }
+    return;
+  }
+  if (V < 8 && vec) {
+#pragma unroll
+    for (int i = 0; i < V; i += 2) {
+      const uint32_t v = c < E ? __ldg((const uint32_t *)(z + c + i)) : 0xff80ff80u;
+      f[i] = __uint_as_float(v << 16);
+      f[i + 1] = __uint_as_float(v & 0xffff0000u);
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < V; i++) f[i] = c + i < E ? to_f(z[c + i]) : -INFINITY;
+}
+
+template <int V>
+__device__ __forceinline__ void store_row(float *z, int c, int E, bool vec, const float f[V]) {
+  if (V % 4 == 0 && vec) {
+#pragma unroll
+    for (int i = 0; i < V; i += 4)
+      if (c + i < E) *(float4 *)(z + c + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
+    return;
+  }
+  if (V == 2 && vec) {
+    if (c < E) *(float2 *)(z + c) = make_float2(f[0], f[V - 1]);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < V; i++)
+    if (c + i < E) z[c + i] = f[i];
+}
+template <int V>
+__device__ __forceinline__ void store_row(__nv_bfloat16 *z, int c, int E, bool vec,
+                                          const float f[V]) {
+  if (V % 8 == 0 && vec) {
+#pragma unroll
+    for (int i = 0; i < V; i += 8)
+      if (c + i < E) *(uint4 *)(z + c + i) = to_bf16x8(f + i);
+    return;
+  }
+  if (V < 8 && vec) {
+    if (c < E)
+#pragma unroll
+      for (int i = 0; i < V; i += 2)
+        *(__nv_bfloat162 *)(z + c + i) = __floats2bfloat162_rn(f[i], f[i + 1]);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < V; i++)
+    if (c + i < E) z[c + i] = __float2bfloat16_rn(f[i]);
+}
+
+// Adds up the blocks' sums cnt[E] and acc[E] (acc: `warps` rows of E, one per
+// warp) over the cluster, in a fixed order, and writes them.
+__device__ void finish_block(const RouteArgs &a, int32_t *cnt, float *acc, int warps) {
+  const int r = blockIdx.y;
+  __syncthreads();
+  if (a.part_p) {
+    for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
+      float v = acc[e];
+      for (int i = 1; i < warps; i++) v += acc[(size_t)i * a.E + e];
+      acc[e] = v;
+    }
+  }
+  const int n = a.cluster, me = blockIdx.x % n, parts = gridDim.x / n;
+  const int64_t o = ((int64_t)r * parts + blockIdx.x / n) * a.E;
+  if (n > 1)
+    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;"
+                 ::: "memory");
+  else
+    __syncthreads();
+  const uint32_t c0 = (uint32_t)__cvta_generic_to_shared(cnt);
+  const uint32_t a0 = (uint32_t)__cvta_generic_to_shared(acc);
+  for (int e = me * blockDim.x + threadIdx.x; e < a.E; e += n * blockDim.x) {
+    int c = 0;
+    float p = 0.0f;
+    for (int b = 0; b < n; b++) {
+      uint32_t ca, pa;
+      int cv;
+      float pv;
+      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ca) : "r"(c0 + 4 * e), "r"(b));
+      asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(cv) : "r"(ca) : "memory");
+      c += cv;
+      if (!a.part_p) continue;
+      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(pa) : "r"(a0 + 4 * e), "r"(b));
+      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(pv) : "r"(pa) : "memory");
+      p += pv;
+    }
+    if (a.tpe) {
+      a.tpe[(int64_t)r * a.E + e] = c + (e == 0 ? (a.S - a.ntok[r]) * a.K : 0);
+    } else {
+      a.part_c[o + e] = c;
+      if (a.part_p) a.part_p[o + e] = p;
+    }
+  }
+  // no block leaves before the others have read its sums
+  if (n > 1)
+    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;"
+                 ::: "memory");
+}
+
+// Rows of at most LP * V logits in registers, LP lanes to a token, lane l
+// holding columns l*V .. l*V + V - 1 (so the lowest lane and the lowest of its
+// values is the lowest index).  A round finds the largest key that is left:
+// a warp to a token by one integer reduction and a vote, a few lanes by
+// exchanges of (key, index).
+template <typename T, int LP, int V>
+__global__ void __launch_bounds__(kWarps * 32) route_kernel(RouteArgs a, bool vec) {
+  pdl_wait();
+  pdl_launch_dependents();
+  constexpr int kTok = 32 / LP;  // tokens of a warp at a time
+  extern __shared__ float sh[];
+  float *acc = sh;                                             // [kWarps, E]
+  int32_t *cnt = (int32_t *)(sh + (size_t)kWarps * a.E);       // [E]
+  uint2 *stage = (uint2 *)(cnt + ((a.E + 1) & ~1));            // [tokens, K] (key, index)
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int sub = lane / LP, col = (lane % LP) * V;
+  const int r = blockIdx.y, n = a.ntok[r];
+  for (int e = threadIdx.x; e < a.E; e += blockDim.x) cnt[e] = 0;
+  __syncthreads();
+  float sum[V];
+#pragma unroll
+  for (int i = 0; i < V; i++) sum[i] = 0.0f;
+  stage += (size_t)(warp * kTok + sub) * a.K;
+  for (int s0 = (blockIdx.x * kWarps + warp) * kTok; s0 < a.S; s0 += gridDim.x * kWarps * kTok) {
+    const int s = s0 + sub;
+    const int64_t t = (int64_t)r * a.S + s;
+    const bool on = s < n;  // a token; else padding, or past the batch
+    float z[V];
+#pragma unroll
+    for (int i = 0; i < V; i++) z[i] = -INFINITY;
+    if (on) load_row<V>((const T *)a.logits + t * a.E, col, a.E, vec, z);
+    uint32_t key[V];
+#pragma unroll
+    for (int i = 0; i < V; i++) key[i] = col + i < a.E ? order_key(z[i]) : 0u;
+    float m = -INFINITY;
+    for (int k = 0; k < a.K; k++) {
+      uint32_t best = key[0];
+#pragma unroll
+      for (int i = 1; i < V; i++) best = max(best, key[i]);
+      uint32_t top;
+      int id = 0;
+      bool win;
+      if (LP == 32) {
+        top = __reduce_max_sync(0xffffffffu, best);
+        const int src = __ffs(__ballot_sync(0xffffffffu, best == top)) - 1;
+        win = lane == src;
+      } else {
+        // this lane's lowest index of its best value, then the group's
+#pragma unroll
+        for (int i = V - 1; i >= 0; i--)
+          if (key[i] == best) id = col + i;
+        top = best;
+        int tid = id;
+#pragma unroll
+        for (int o = LP / 2; o; o >>= 1) {
+          const uint32_t q = __shfl_xor_sync(0xffffffffu, top, o);
+          const int qi = __shfl_xor_sync(0xffffffffu, tid, o);
+          if (q > top || (q == top && qi < tid)) {
+            top = q;
+            tid = qi;
+          }
+        }
+        win = tid == id;
+      }
+      if (k == 0) m = key_value(top);
+      // the winner notes its pick and drops it
+      bool look = win;
+#pragma unroll
+      for (int i = 0; i < V; i++)
+        if (look && key[i] == top) {
+          key[i] = 0;
+          id = col + i;
+          look = false;
+        }
+      if (win) stage[k] = make_uint2(top, id);
+    }
+    __syncwarp();
+    // weights: the group's lanes share the picks
+    float Zk = 0.0f;
+    for (int k = lane % LP; k < a.K; k += LP) Zk += score(key_value(stage[k].x), m, a.sigmoid);
+    Zk = group_sum<LP>(Zk);
+    for (int k = lane % LP; k < a.K; k += LP) {
+      const uint2 q = stage[k];
+      const float v = score(key_value(q.x), m, a.sigmoid);
+      if (s < a.S) {
+        a.topk[t * a.K + k] = on ? (int)q.y : 0;
+        a.w[t * a.K + k] = !on || Zk == 0.0f ? 0.0f : v / Zk;
+      }
+      if (on) atomicAdd(&cnt[q.y], 1);
+    }
+    if (a.part_p) {
+      float Z = 0.0f;
+#pragma unroll
+      for (int i = 0; i < V; i++) {
+        z[i] = col + i < a.E ? score(z[i], m, a.sigmoid) : 0.0f;
+        Z += z[i];
+      }
+      Z = group_sum<LP>(Z);
+      const float inv = !on || Z == 0.0f ? 0.0f : 1.0f / Z;
+#pragma unroll
+      for (int i = 0; i < V; i++) sum[i] += on ? z[i] * inv : 0.0f;
+    }
+    __syncwarp();
+  }
+  if (a.part_p) {
+#pragma unroll
+    for (int i = 0; i < V; i++) {
+#pragma unroll
+      for (int o = LP; o < 32; o <<= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
+      if (sub == 0 && col + i < a.E) acc[(size_t)warp * a.E + col + i] = sum[i];
+    }
+  }
+  finish_block(a, cnt, acc, kWarps);
+}
+
+// Any E: one warp per token, the row in shared memory.
 template <typename T>
-__global__ void __launch_bounds__(kWarps * 32) route_kernel(RouteArgs a) {
+__global__ void __launch_bounds__(kWarps * 32) route_long_kernel(RouteArgs a) {
   pdl_wait();
   pdl_launch_dependents();
   extern __shared__ float sh[];
   const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  float *row = sh + (size_t)warp * a.E;                       // this token's logits
-  float *acc = sh + (size_t)(warps + warp) * a.E;             // this warp's sums of p
+  float *acc = sh + (size_t)warp * a.E;                       // this warp's sums of p
+  float *row = sh + (size_t)(warps + warp) * a.E;             // this token's logits
   int32_t *cnt = (int32_t *)(sh + (size_t)2 * warps * a.E);   // this block's picks
   const int r = blockIdx.y;
   const int n = a.ntok[r];
@@ -110,7 +380,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(RouteArgs a) {
       }
       if (lane == 0) atomicAdd(&cnt[at], 1);
     }
-    float sk = lane < a.K ? score(zk, m, a.sigmoid) : 0.0f;
+    const float sk = lane < a.K ? score(zk, m, a.sigmoid) : 0.0f;
     const float Zk = warp_sum(sk);
     if (lane < a.K) {
       a.topk[t * a.K + lane] = my;
@@ -125,16 +395,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(RouteArgs a) {
     }
     __syncwarp();
   }
-  __syncthreads();
-  const int64_t o = ((int64_t)r * gridDim.x + blockIdx.x) * a.E;
-  for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
-    a.part_c[o + e] = cnt[e];
-    if (a.part_p) {
-      float v = 0.0f;
-      for (int i = 0; i < warps; i++) v += sh[(size_t)(warps + i) * a.E + e];
-      a.part_p[o + e] = v;
-    }
-  }
+  finish_block(a, cnt, sh, warps);
 }
 
 struct FinishArgs {
@@ -144,11 +405,13 @@ struct FinishArgs {
   float *coef;   // [R, E] or null
   float *loss;   // [1] or null
   float alpha;
-  int R, S, E, K, bpr, global;
+  int R, S, E, K, parts, global;
   int32_t ntok[kMaxRanks];
 };
 
-// Sums the blocks' partials in block order: counts, coefficients, loss.
+// Sums the clusters' partials in order: counts, coefficients, loss.  A warp
+// takes 32 experts of one rank (rank scope), so its loads are rows of 128
+// bytes; the loss is added up over (rank, expert) in a fixed order.
 __global__ void __launch_bounds__(1024) route_finish_kernel(FinishArgs a) {
   pdl_wait();
   pdl_launch_dependents();
@@ -160,31 +423,41 @@ __global__ void __launch_bounds__(1024) route_finish_kernel(FinishArgs a) {
     busy += a.ntok[r] > 0;
   }
   float loss = 0.0f;
-  for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
-    int64_t call = 0;
-    float pall = 0.0f;
-    for (int r = 0; r < a.R; r++) {
+  if (!a.global || !a.loss) {
+    for (int i = threadIdx.x; i < a.R * a.E; i += blockDim.x) {
+      const int r = i / a.E, e = i - r * a.E;
+      const int64_t o = (int64_t)r * a.parts * a.E + e;
       int c = 0;
       float p = 0.0f;
-      for (int b = 0; b < a.bpr; b++) {
-        const int64_t o = ((int64_t)r * a.bpr + b) * a.E + e;
-        c += a.part_c[o];
-        if (a.loss) p += a.part_p[o];
+#pragma unroll 4
+      for (int b = 0; b < a.parts; b++) {
+        c += __ldg(a.part_c + o + (int64_t)b * a.E);
+        if (a.loss) p += __ldg(a.part_p + o + (int64_t)b * a.E);
       }
       const int n = a.ntok[r];
-      a.tpe[(int64_t)r * a.E + e] = c + (e == 0 ? (a.S - n) * a.K : 0);
+      a.tpe[i] = c + (e == 0 ? (a.S - n) * a.K : 0);
       if (!a.loss) continue;
-      if (a.global) {
-        call += c;
-        pall += p;
-      } else {
-        const float t = (float)(n > 0 ? n : 1);
-        const float q = a.alpha * (float)a.E * (float)c / ((float)a.K * t * t * (float)(busy > 0 ? busy : 1));
-        a.coef[(int64_t)r * a.E + e] = q;
-        loss += q * p;
-      }
+      const float t = (float)(n > 0 ? n : 1);
+      const float q = a.alpha * (float)a.E * (float)c /
+                      ((float)a.K * t * t * (float)(busy > 0 ? busy : 1));
+      a.coef[i] = q;
+      loss += q * p;
     }
-    if (a.loss && a.global) {
+  } else {
+    for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
+      int64_t call = 0;
+      float pall = 0.0f;
+      for (int r = 0; r < a.R; r++) {
+        const int64_t o = (int64_t)r * a.parts * a.E + e;
+        int c = 0;
+#pragma unroll 4
+        for (int b = 0; b < a.parts; b++) {
+          c += __ldg(a.part_c + o + (int64_t)b * a.E);
+          pall += __ldg(a.part_p + o + (int64_t)b * a.E);
+        }
+        a.tpe[(int64_t)r * a.E + e] = c + (e == 0 ? (a.S - a.ntok[r]) * a.K : 0);
+        call += c;
+      }
       const float t = (float)(total > 0 ? total : 1);
       const float q = a.alpha * (float)a.E * (float)call / ((float)a.K * t * t);
       for (int r = 0; r < a.R; r++) a.coef[(int64_t)r * a.E + e] = q;
@@ -214,22 +487,110 @@ struct RouteBwdArgs {
 };
 
 // 1 - sigmoid(z), without cancellation.
-__device__ __forceinline__ float one_minus_sigmoid(float z) { return 1.0f / (1.0f + expf(z)); }
+__device__ __forceinline__ float one_minus_sigmoid(float z) {
+  return __fdividef(1.0f, 1.0f + __expf(z));
+}
+
+// The same layout of rows in registers; blockIdx.y is the rank, whose
+// coefficients stay in registers too.  A pick's term reaches the lane of its
+// column through a zeroed row of shared memory.
+template <typename T, int LP, int V>
+__global__ void __launch_bounds__(kWarps * 32) route_backward_kernel(RouteBwdArgs a, bool vec) {
+  pdl_wait();
+  pdl_launch_dependents();
+  constexpr int kTok = 32 / LP, kRow = LP * V;
+  __shared__ __align__(16) float term[kWarps * kTok * kRow];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int sub = lane / LP, col = (lane % LP) * V;
+  const int r = blockIdx.y, n = a.ntok[r];
+  const float dl = a.dloss ? *a.dloss : 1.0f;
+  float *row = term + (warp * kTok + sub) * kRow;
+  float cf[V];
+#pragma unroll
+  for (int i = 0; i < V; i++) {
+    cf[i] = a.coef && col + i < a.E ? __ldg(a.coef + (int64_t)r * a.E + col + i) : 0.0f;
+    row[col + i] = 0.0f;
+  }
+  __syncwarp();
+  for (int s0 = (blockIdx.x * kWarps + warp) * kTok; s0 < a.S; s0 += gridDim.x * kWarps * kTok) {
+    const int s = s0 + sub;
+    const int64_t t = (int64_t)r * a.S + s;
+    const bool on = s < n;
+    float z[V], g[V];
+#pragma unroll
+    for (int i = 0; i < V; i++) z[i] = -INFINITY;
+    float wd = 0.0f;
+    if (on) {
+      load_row<V>((const T *)a.logits + t * a.E, col, a.E, vec, z);
+      if (a.dw)
+        for (int k = lane % LP; k < a.K; k += LP)
+          wd += __ldg(a.w + t * a.K + k) * __ldg(a.dw + t * a.K + k);
+    }
+    wd = group_sum<LP>(wd);
+    if (on && a.dw)
+      for (int k = lane % LP; k < a.K; k += LP) {
+        const int id = __ldg(a.topk + t * a.K + k);
+        if (id >= 0 && id < a.E)
+          row[id] = __ldg(a.w + t * a.K + k) * (__ldg(a.dw + t * a.K + k) - wd);
+      }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < V; i++) g[i] = row[col + i];
+    if (a.coef) {
+      float m = z[0];
+#pragma unroll
+      for (int i = 1; i < V; i++) m = fmaxf(m, z[i]);
+#pragma unroll
+      for (int o = LP / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      float p[V], Z = 0.0f, pc = 0.0f;
+#pragma unroll
+      for (int i = 0; i < V; i++) {
+        p[i] = col + i < a.E ? score(z[i], m, a.sigmoid) : 0.0f;
+        Z += p[i];
+        pc += p[i] * cf[i];
+      }
+      Z = group_sum<LP>(Z);
+      pc = group_sum<LP>(pc);
+      const float inv = Z == 0.0f ? 0.0f : 1.0f / Z;
+      pc *= inv;
+      const float f = dl * inv;
+#pragma unroll
+      for (int i = 0; i < V; i++) g[i] += f * p[i] * (cf[i] - pc);
+    }
+    if (a.sigmoid) {
+#pragma unroll
+      for (int i = 0; i < V; i++) g[i] *= one_minus_sigmoid(z[i]);
+    }
+    if (!on) {
+#pragma unroll
+      for (int i = 0; i < V; i++) g[i] = 0.0f;
+    }
+    if (s < a.S) store_row<V>((T *)a.dz + t * a.E, col, a.E, vec, g);
+    __syncwarp();
+    if (on && a.dw)
+      for (int k = lane % LP; k < a.K; k += LP) {
+        const int id = __ldg(a.topk + t * a.K + k);
+        if (id >= 0 && id < a.E) row[id] = 0.0f;
+      }
+    __syncwarp();
+  }
+}
 
 __device__ __forceinline__ void put(float *p, float v) { *p = v; }
 __device__ __forceinline__ void put(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
 
+// Any E: one warp per token, several passes over its row.
 template <typename T>
-__global__ void __launch_bounds__(kWarps * 32) route_backward_kernel(RouteBwdArgs a) {
+__global__ void __launch_bounds__(kWarps * 32) route_backward_long_kernel(RouteBwdArgs a) {
   pdl_wait();
   pdl_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t tokens = (int64_t)a.R * a.S;
+  const int r = blockIdx.y;
   const float dl = a.dloss ? *a.dloss : 1.0f;
-  for (int64_t t = (int64_t)blockIdx.x * kWarps + warp; t < tokens; t += (int64_t)gridDim.x * kWarps) {
-    const int r = (int)(t / a.S);
+  for (int s = blockIdx.x * kWarps + warp; s < a.S; s += gridDim.x * kWarps) {
+    const int64_t t = (int64_t)r * a.S + s;
     T *out = (T *)a.dz + t * a.E;
-    if (t - (int64_t)r * a.S >= a.ntok[r]) {
+    if (s >= a.ntok[r]) {
       for (int e = lane; e < a.E; e += 32) put(out + e, 0.0f);
       continue;
     }
@@ -242,9 +603,9 @@ __global__ void __launch_bounds__(kWarps * 32) route_backward_kernel(RouteBwdArg
     float Z = 0.0f, pc = 0.0f;
     if (cf) {
       for (int e = lane; e < a.E; e += 32) {
-        const float s = score(to_f(z[e]), m, a.sigmoid);
-        Z += s;
-        pc += s * cf[e];
+        const float s1 = score(to_f(z[e]), m, a.sigmoid);
+        Z += s1;
+        pc += s1 * cf[e];
       }
       Z = warp_sum(Z);
       pc = warp_sum(pc);
@@ -278,22 +639,89 @@ __global__ void __launch_bounds__(kWarps * 32) route_backward_kernel(RouteBwdArg
   }
 }
 
-// Blocks per rank of the forward pass: as many as fill the SMs once, no more
-// than the rank's tokens need.
-int blocks_per_rank(int R, int S, int sms) {
-  const int need = (S + kWarps - 1) / kWarps;
-  const int fill = (sms + R - 1) / R;
-  return need < fill ? (need > 0 ? need : 1) : fill;
+// How a row of E logits is held: lanes per token and values per lane.  A
+// thread to a token of up to 8 experts, four lanes up to 32, then a warp with
+// 2 to 16 values per lane; longer rows in shared memory.
+enum Form { kThread8, kFour8, kWarp2, kWarp4, kWarp8, kWarp16, kLong };
+Form form_of(int E) {
+  return E <= 8 ? kThread8 : E <= 32 ? kFour8 : E <= 64 ? kWarp2 : E <= 128 ? kWarp4
+         : E <= 256 ? kWarp8 : E <= 512 ? kWarp16 : kLong;
+}
+int tokens_per_warp(Form f) { return f == kThread8 ? 32 : f == kFour8 ? 8 : 1; }
+
+// Whether rows are whole 16-byte vectors.
+bool whole_vectors(int E, int bf16) { return E % (bf16 ? 8 : 4) == 0; }
+
+// Warps of a block of the shared-memory form: fewer where two rows of all
+// experts per warp would not fit.
+int warps_of(int E) { return E <= 1024 ? kWarps : 4; }
+
+// Blocks per rank of the forward pass: enough for the rank's tokens, at most
+// two per SM over all ranks; a power of two up to the cluster size, then a
+// multiple of it.
+int blocks_per_rank(int R, int S, int E, int sms) {
+  const Form f = form_of(E);
+  const int per = (f == kLong ? warps_of(E) : kWarps) * tokens_per_warp(f);
+  const int64_t need = ((int64_t)S + per - 1) / per;
+  const int64_t cap = (2 * sms + R - 1) / R;
+  int64_t b = need < cap ? need : cap;
+  if (b >= kCluster) return (int)(b / kCluster * kCluster);
+  int p = 1;
+  while (p < b) p <<= 1;
+  return p;
 }
 
-// Warps of a forward block: fewer where a row of all experts per warp would
-// not fit in shared memory.
-int warps_of(int E) { return E <= 1024 ? kWarps : 4; }
+template <typename T>
+cudaError_t launch_forward(const RouteArgs &a, int bpr, cudaStream_t st) {
+  const dim3 grid(bpr, a.R), block(kWarps * 32);
+  const Form f = form_of(a.E);
+  const bool vec = whole_vectors(a.E, sizeof(T) == 2);
+  size_t smem = ((size_t)kWarps * a.E + ((a.E + 1) & ~1)) * 4 +
+                (size_t)kWarps * tokens_per_warp(f) * a.K * sizeof(uint2);
+  switch (f) {
+    case kThread8: return launch_pdl_ex(route_kernel<T, 1, 8>, grid, block, smem, st, false, a.cluster, a, vec);
+    case kFour8: return launch_pdl_ex(route_kernel<T, 4, 8>, grid, block, smem, st, false, a.cluster, a, vec);
+    case kWarp2: return launch_pdl_ex(route_kernel<T, 32, 2>, grid, block, smem, st, false, a.cluster, a, vec);
+    case kWarp4: return launch_pdl_ex(route_kernel<T, 32, 4>, grid, block, smem, st, false, a.cluster, a, vec);
+    case kWarp8: return launch_pdl_ex(route_kernel<T, 32, 8>, grid, block, smem, st, false, a.cluster, a, vec);
+    case kWarp16: return launch_pdl_ex(route_kernel<T, 32, 16>, grid, block, smem, st, false, a.cluster, a, vec);
+    default: break;
+  }
+  const int warps = warps_of(a.E);
+  smem = (size_t)(2 * warps + 1) * a.E * sizeof(float);
+  cudaError_t e = cudaSuccess;
+  if (smem > 48 * 1024)
+    e = cudaFuncSetAttribute(route_long_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)smem);
+  return e != cudaSuccess ? e
+                          : launch_pdl_ex(route_long_kernel<T>, grid, dim3(warps * 32), smem, st,
+                                          false, a.cluster, a);
+}
+
+template <typename T>
+cudaError_t launch_backward(const RouteBwdArgs &a, int sms, cudaStream_t st) {
+  const Form f = form_of(a.E);
+  const bool vec = whole_vectors(a.E, sizeof(T) == 2);
+  const int per = kWarps * tokens_per_warp(f);
+  const int64_t need = ((int64_t)a.S + per - 1) / per, cap = ((int64_t)sms * 8 + a.R - 1) / a.R;
+  const dim3 grid((unsigned)(need < cap ? need : cap), a.R), block(kWarps * 32);
+  switch (f) {
+    case kThread8: return launch_pdl(route_backward_kernel<T, 1, 8>, grid, block, 0, st, false, a, vec);
+    case kFour8: return launch_pdl(route_backward_kernel<T, 4, 8>, grid, block, 0, st, false, a, vec);
+    case kWarp2: return launch_pdl(route_backward_kernel<T, 32, 2>, grid, block, 0, st, false, a, vec);
+    case kWarp4: return launch_pdl(route_backward_kernel<T, 32, 4>, grid, block, 0, st, false, a, vec);
+    case kWarp8: return launch_pdl(route_backward_kernel<T, 32, 8>, grid, block, 0, st, false, a, vec);
+    case kWarp16: return launch_pdl(route_backward_kernel<T, 32, 16>, grid, block, 0, st, false, a, vec);
+    default: break;
+  }
+  return launch_pdl(route_backward_long_kernel<T>, grid, block, 0, st, false, a);
+}
 
 }  // namespace
 
 int64_t route_scratch_words(int R, int E, int sms) {
-  return (int64_t)2 * R * ((sms + R - 1) / R) * E;
+  // at most 2 * sms / R + 1 blocks per rank
+  return (int64_t)2 * R * ((2 * sms + R - 1) / R / kCluster + 1) * E;
 }
 
 int launch_route(moonep_ctx *ctx, const void *logits, int bf16, int scoring, float alpha, int global,
@@ -302,18 +730,21 @@ int launch_route(moonep_ctx *ctx, const void *logits, int bf16, int scoring, flo
   const moonep_config &c = ctx->cfg;
   RouteArgs a{};
   FinishArgs f{};
+  const int bpr = blocks_per_rank(c.R, c.S, c.E, ctx->sms);
   a.R = f.R = c.R;
   a.S = f.S = c.S;
   a.E = f.E = c.E;
   a.K = f.K = c.K;
-  a.bpr = f.bpr = blocks_per_rank(c.R, c.S, ctx->sms);
+  a.cluster = bpr < kCluster ? bpr : kCluster;
+  f.parts = bpr / a.cluster;
   a.logits = logits;
   a.topk = topk;
   a.w = w;
   a.sigmoid = scoring;
-  const int64_t half = (int64_t)c.R * a.bpr * c.E;
+  const int64_t half = (int64_t)c.R * f.parts * c.E;
   a.part_c = ctx->d_route;
   a.part_p = loss ? (float *)(ctx->d_route + half) : nullptr;
+  a.tpe = !loss && f.parts == 1 ? tpe : nullptr;
   f.part_c = a.part_c;
   f.part_p = a.part_p;
   f.tpe = tpe;
@@ -322,15 +753,9 @@ int launch_route(moonep_ctx *ctx, const void *logits, int bf16, int scoring, flo
   f.alpha = alpha;
   f.global = global;
   for (int r = 0; r < c.R; r++) a.ntok[r] = f.ntok[r] = num_tokens ? num_tokens[r] : c.S;
-  const int warps = warps_of(c.E);
-  const size_t smem = (size_t)(2 * warps + 1) * c.E * sizeof(float);
-  auto kern = bf16 ? route_kernel<__nv_bfloat16> : route_kernel<float>;
-  cudaError_t e = cudaSuccess;
-  if (smem > 48 * 1024)
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e == cudaSuccess)
-    e = launch_pdl(kern, dim3(a.bpr, c.R), dim3(warps * 32), smem, st, false, a);
-  if (e == cudaSuccess) e = launch_pdl(route_finish_kernel, dim3(1), dim3(1024), 0, st, false, f);
+  cudaError_t e = bf16 ? launch_forward<__nv_bfloat16>(a, bpr, st) : launch_forward<float>(a, bpr, st);
+  if (e == cudaSuccess && !a.tpe)
+    e = launch_pdl(route_finish_kernel, dim3(1), dim3(1024), 0, st, false, f);
   return cuda_status(e);
 }
 
@@ -353,11 +778,8 @@ int launch_route_backward(moonep_ctx *ctx, const void *logits, int bf16, int sco
   a.K = c.K;
   a.sigmoid = scoring;
   for (int r = 0; r < c.R; r++) a.ntok[r] = num_tokens ? num_tokens[r] : c.S;
-  const int64_t need = ((int64_t)c.R * c.S + kWarps - 1) / kWarps;
-  const int64_t cap = (int64_t)ctx->sms * 8;
-  auto kern = bf16 ? route_backward_kernel<__nv_bfloat16> : route_backward_kernel<float>;
-  return cuda_status(launch_pdl(kern, dim3((unsigned)(need < cap ? need : cap)), dim3(kWarps * 32),
-                                0, st, false, a));
+  return cuda_status(bf16 ? launch_backward<__nv_bfloat16>(a, ctx->sms, st)
+                          : launch_backward<float>(a, ctx->sms, st));
 }
 
 }  // namespace moonep
