@@ -10,31 +10,28 @@
 // pair of SMs with 128 each) and the segment's rows the N side, which comes in
 // steps of 16: segments are ragged and often short (a decode step has a few
 // rows per expert), so the side with the fine step wastes the least.  A
-// segment is cut into equal pieces of at most 208 rows.
+// segment is cut into equal pieces of at most 192 rows.
 //
 // One persistent pair of CTAs (cluster of two) per pair of SMs; warps:
-//   0      TMA: 512 values of k per stage, 128 weight rows and half the
-//          piece's rows per CTA.  A single-warp loop costs some 250 cycles
-//          per stage besides its instructions; 256 values of k, 352 cycles of
-//          products for 176 rows, were too few to hide that
+//   0      TMA: 256 values of k per stage, 128 weight rows and half the
+//          piece's rows per CTA
 //   1-6    scales: plain [rows, Kd/32] tensors (as prefetch and dispatch move
 //          them) rearranged to the tensor cores' 128 x 4 blocks on the way to
 //          shared memory; each lane loads 16 scales of four rows 32 apart and
-//          so holds whole 16-byte lines of four such blocks
-//   7      MMA, one thread of the pair's first CTA: eight 64-deep products per
-//          stage
+//          so holds whole 16-byte lines of four such blocks.  Two sets of
+//          three warps take turns: one set needed 600 cycles per stage, twice
+//          the products' time
+//   7      MMA, one thread of the pair's first CTA: scales to TMEM, then four
+//          64-deep products per stage
 //   8-15   epilogue: accumulator (lane = output column, TMEM column = row) to
 //          global memory, two neighbouring columns per store; the two groups
 //          of four warps take alternate 32 rows
 //   16     schedule: the CTA's next 32 tiles at a time, one per lane, to shared
 //          memory (every warp working its tiles out itself cost 4000 cycles
 //          per tile)
-//   17     scales to TMEM, one thread of the pair's first CTA (a thread that
-//          issued both copies and products needed 500 cycles per stage where
-//          the tensor pipe needs 352 for 176 rows)
-// Accumulators are double-buffered in TMEM (2 x 208 columns); the other 96
-// columns hold two stages' scales, overwritten once the products that read
-// them are done.
+// Accumulators are double-buffered in TMEM (2 x 192 columns); each of the five
+// shared-memory stages has its own 24 columns of scales, so a stage's scales
+// are only overwritten once its products are done (the stage's barrier).
 // Every wait has a limit of one second, after which the kernel latches
 // MOONEP_ERR_TIMEOUT, drains and returns.
 #include <cuda.h>
@@ -45,36 +42,33 @@
 namespace moonep {
 namespace {
 
-constexpr int kThreads = 576;
-constexpr int kStages = 3;
-constexpr int kSlots = 2;                 // stages whose scales TMEM holds
-constexpr int kMaxCols = 208;             // rows of a piece (MMA N)
+constexpr int kThreads = 544;
+constexpr int kStages = 5;
+constexpr int kMaxCols = 192;             // rows of a piece (MMA N)
 constexpr int kTileN = 256;               // outputs per tile (MMA M of the pair)
-constexpr int kStageK = 512;              // values of k per stage, two operand tiles of 128
-                                          // bytes a row
+constexpr int kStageK = 256;              // values of k per stage (128 bytes)
 constexpr int kBoxRows = 32;              // rows per TMA box of the row side,
 constexpr int kWideRows = kMaxCols / 2;   // or all of half a piece in one
-constexpr int kATile = 128 * 128;
-constexpr int kBTile = kMaxCols / 2 * 128;  // half a piece
-constexpr int kBOff = 2 * kATile, kSfOff = kBOff + 2 * kBTile;
-constexpr int kSfBytes = 4 * 512 + 8 * 512;  // for 128 values of k: one weight block, two row blocks
-constexpr int kStageBytes = kSfOff + kSfBytes;
-constexpr int kSfBoxBytes = (128 + 128 + kMaxCols - 128) * 16;
-constexpr int kSfCols = 48;               // TMEM columns of one stage's scales
+constexpr int kABytes = 128 * 128;
+constexpr int kBBytes = 96 * 128;         // half a piece
+constexpr int kSfBytes = 2 * 512 + 4 * 512;  // two weight blocks, four row blocks
+constexpr int kStageBytes = kABytes + kBBytes + kSfBytes;
+constexpr int kSfCols = 24;               // TMEM columns of one stage's scales
 constexpr int kSfBase = 2 * kMaxCols;
 constexpr int kEntries = 1024;            // tile table entries
 constexpr long long kLimitNs = 1000000000LL;
-static_assert(kSfBase + kSlots * kSfCols <= 512, "TMEM columns");
-static_assert(kStageBytes % 1024 == 0 && kBTile % 1024 == 0, "operand tiles start on 1 KB");
+static_assert(kSfBase + kStages * kSfCols <= 512, "TMEM columns");
+static_assert(kStageBytes % 1024 == 0, "operand tiles start on 1 KB");
 
 struct __align__(1024) Shared {
   uint8_t stage[kStages][kStageBytes];
-  uint8_t sfbox[2][kSfBoxBytes];  // scale rows as loaded, one chunk of each set
-  int32_t last[kEntries];         // tiles up to and including the entry's groups
+  int32_t last[kEntries];   // tiles up to and including the entry's groups
+  int32_t start[kEntries];  // first row (rank-local) of the entry's one group
+  int32_t rows[kEntries];
   int32_t wsum[8];
   int4 tile[2][32];  // the CTA's tiles: group, first output, first row, rows
-  uint64_t full[kStages], scaled[kStages], empty[kStages], acc_full[2], acc_empty[2];
-  uint64_t tile_full[2], tile_empty[2], sf_full[2][3];
+  uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2];
+  uint64_t tile_full[2], tile_empty[2];
   uint32_t tmem;
   int32_t dead;
 };
@@ -86,7 +80,7 @@ struct ProductArgs {
   int64_t lds;
   int R, E, B, L, EB, NvS, N, Kd;
   int groups, per;  // groups, groups per table entry
-  int sf_tma;       // both sides' scale rows are whole aligned 16-byte vectors
+  int as16, ws16;   // scale rows are whole aligned 16-byte vectors
   int32_t *status;
 };
 
@@ -199,17 +193,6 @@ __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t
       : "memory");
 }
 
-// A stage's scales to its TMEM columns (the second 128 rows' too, used or not).
-__device__ __forceinline__ void stage_scales(uint32_t base, uint32_t col) {
-  const uint32_t sf = base + kSfOff;
-#pragma unroll
-  for (int i = 0; i < 4; i++) {
-    scales_to_tmem(col + i * 4, sf + i * 512);
-    scales_to_tmem(col + 16 + i * 8, sf + 2048 + i * 1024);
-    scales_to_tmem(col + 16 + i * 8 + 4, sf + 2048 + i * 1024 + 512);
-  }
-}
-
 // Rows [start, start + rows) of group g in its rank's window; offsets outside
 // the window are reported and the segment treated as empty.
 __device__ __forceinline__ bool segment(const ProductArgs &a, int g, int *start, int *rows) {
@@ -234,13 +217,14 @@ __device__ int4 tile_of(const ProductArgs &a, const Shared *sh, int t) {
     if (sh->last[mid] > t) hi = mid; else lo = mid + 1;
   }
   int rest = t - (lo ? sh->last[lo - 1] : 0);
-  int g = lo * a.per, start, rows;
-  for (;; g++) {
-    segment(a, g, &start, &rows);
-    const int n = pieces(rows) * nb;
-    if (rest < n) break;
-    rest -= n;
-  }
+  int g = lo * a.per, start = sh->start[lo], rows = sh->rows[lo];
+  if (a.per > 1)
+    for (;; g++) {
+      segment(a, g, &start, &rows);
+      const int n = pieces(rows) * nb;
+      if (rest < n) break;
+      rest -= n;
+    }
   const int p = pieces(rows), m = rest / nb;
   const int each = ((rows + p - 1) / p + 15) & ~15;
   const int j = g < a.E ? g / a.L : (g - a.E) / a.B;
@@ -254,7 +238,7 @@ __device__ __noinline__ int build_table(const ProductArgs &a, Shared *sh) {
   const int entries = (a.groups + a.per - 1) / a.per;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   for (int i = tid; i < kEntries; i += kThreads) {
-    int n = 0, start, rows;
+    int n = 0, start = 0, rows = 0;
     if (i < entries)
       for (int g = i * a.per; g < min(a.groups, (i + 1) * a.per); g++) {
         if (!segment(a, g, &start, &rows) && blockIdx.x == 0)
@@ -262,6 +246,8 @@ __device__ __noinline__ int build_table(const ProductArgs &a, Shared *sh) {
         n += pieces(rows) * nb;
       }
     sh->last[i] = n;
+    sh->start[i] = start;
+    sh->rows[i] = rows;
   }
   __syncthreads();
   // eight warps scan 128 entries each, four per lane
@@ -290,14 +276,12 @@ __device__ __noinline__ int build_table(const ProductArgs &a, Shared *sh) {
   return sh->last[kEntries - 1];
 }
 
-// Sixteen scales of a row at p, the first `need` of them wanted and 1.0 in
-// place of the others, from the aligned words around them; bytes outside
-// [base, end) are never touched.  Out of line: inlined for every row of every
-// scale warp it made the kernel 150 KB of code, which no instruction cache
-// holds.
+// Sixteen scale bytes at p, the first `need` of them wanted and 1.0 in place of
+// the others, from the aligned words around them; bytes outside [base, end)
+// are never touched.  Out of line: inlined for every row of every scale warp
+// it made the kernel 150 KB of code, which no instruction cache holds.
 __device__ __noinline__ uint4 load_bytes(const uint8_t *base, const uint8_t *end, const uint8_t *p,
                                          int need) {
-  if (need <= 0) return make_uint4(0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu);
   const uint32_t shift = (uint32_t)((uintptr_t)p & 3) * 8;
   const uint8_t *w0 = p - ((uintptr_t)p & 3);
   uint32_t w[5];
@@ -329,25 +313,26 @@ __device__ __noinline__ uint4 load_bytes(const uint8_t *base, const uint8_t *end
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
+// Sixteen scales of one row from column c on, 1.0 past the row's end or for a
+// row that is not there.  `vec`: rows of whole aligned vectors.
+__device__ __forceinline__ uint4 load_scales(const uint8_t *base, int64_t total, int64_t row,
+                                             int64_t pitch, int c, int n, bool vec, bool there) {
+  const uint32_t one = 0x7f7f7f7fu;
+  if (!there || c >= n) return make_uint4(one, one, one, one);
+  const uint8_t *p = base + row * pitch + c;
+  if (vec) return __ldg((const uint4 *)p);
+  return load_bytes(base, base + total, p, min(16, n - c));
+}
+
 __device__ __forceinline__ uint32_t word(const uint4 &v, int i) {
   return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
 
-// Two rows of one output column (this lane's) and the neighbouring lane's same
-// rows become both columns of one row, the even lane's first row or the odd
-// lane's second.
-__device__ __forceinline__ void store_pair(float *p, uint32_t lo, uint32_t hi, bool odd, uint32_t) {
-  const uint32_t mine = odd ? hi : lo, got = __shfl_xor_sync(0xffffffffu, odd ? lo : hi, 1);
-  if (p) *(uint2 *)p = odd ? make_uint2(got, mine) : make_uint2(mine, got);
+__device__ __forceinline__ void store_pair(float *p, float lo, float hi) {
+  *(float2 *)p = make_float2(lo, hi);
 }
-__device__ __forceinline__ void store_pair(__nv_bfloat16 *p, uint32_t lo, uint32_t hi, bool,
-                                           uint32_t pick) {
-  uint32_t w;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;"
-      : "=r"(w)
-      : "f"(__uint_as_float(hi)), "f"(__uint_as_float(lo)));
-  const uint32_t got = __shfl_xor_sync(0xffffffffu, w, 1);
-  if (p) *(uint32_t *)p = __byte_perm(w, got, pick);
+__device__ __forceinline__ void store_pair(__nv_bfloat16 *p, float lo, float hi) {
+  *(__nv_bfloat162 *)p = __floats2bfloat162_rn(lo, hi);
 }
 
 // The i-th tile of this CTA, for a whole warp that reads them in order.
@@ -361,146 +346,22 @@ __device__ __forceinline__ bool next_tile(Shared *sh, int i, int32_t *status, in
   return true;
 }
 
-// 32 accumulator columns of this warp's 32 lanes; valid after tmem_wait.
-__device__ __forceinline__ void tmem_load(uint32_t v[32], uint32_t addr) {
+// 16 accumulator columns of this warp's 32 lanes.
+__device__ __forceinline__ void tmem_load(uint32_t *v, uint32_t addr) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
-      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
-      "%30, %31}, [%32];"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, "
+      "%10, %11, %12, %13, %14, %15}, [%16];"
       : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
         "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
-        "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]),
-        "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]),
-        "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        "=r"(v[14]), "=r"(v[15])
       : "r"(addr));
-}
-// All loads so far; the registers pass through so that no use moves ahead.
-__device__ __forceinline__ void tmem_wait(uint32_t v[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]),
-                 "+r"(v[6]), "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]),
-                 "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]), "+r"(v[16]), "+r"(v[17]),
-                 "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]),
-                 "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]),
-                 "+r"(v[30]), "+r"(v[31])::"memory");
-}
-
-// A scale warp.  role 0: the CTA's 128 weight rows; 1, 2: the piece's rows
-// 0-127, 128-207.  A set of three warps takes every second stage (16 scales of
-// a row) of the CTA's sequence of tiles.  TMA: the warp's next box of 16-byte
-// rows is loaded to shared memory while the other set fills its stage; loads by the lanes themselves touch a
-// line per lane and kept the shared-memory pipe, which feeds the tensor cores
-// too, busy for 190 cycles per stage.  Otherwise (rows that are not whole
-// aligned vectors) the lanes load.
-template <bool TMA>
-__device__ __forceinline__ void scale_warp(Shared *sh, const ProductArgs &a, uint32_t rank,
-                                           int mine, int chunks, const CUtensorMap *map) {
-  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  const int role = (warp - 1) % 3, turn = (warp - 1) / 3;
-  const int nsc = a.Kd / 32;
-  const uint8_t *base = role ? a.as : a.ws;
-  const int64_t pitch = role ? a.lds : nsc;
-  const uint8_t *end = base + (role ? ((int64_t)a.R * a.NvS - 1) * a.lds + nsc
-                                    : (int64_t)a.groups * a.N * nsc);
-  const uint32_t at = kSfOff + (role ? 2048 + (role - 1) * 512 : 0) + lane * 16;
-  const uint32_t box = smem_addr(sh->sfbox[turn]) + role * 2048;
-  const uint64_t *bar = &sh->sf_full[turn][role];
-  const int box_rows = role == 2 ? kMaxCols - 128 : 128;
-  uint32_t s = 0, phase = 0, box_phase = 0;
-  bool ok = true;
-  int li = 0, lc = turn, have = -1;  // tile and chunk to load next; tile in `tile`
-  int4 tile = make_int4(0, 0, 0, 0);
-  uint4 v[4];
-  // starts (TMA) or does the next chunk's load
-  auto load = [&] {
-    for (; lc >= chunks; lc -= chunks) li++;
-    if (!ok) return;
-    for (; have < li && have < mine - 1; have++)
-      if (!(ok = next_tile(sh, have + 1, a.status, &tile))) return;
-    if (li >= mine) return;
-    const int first = role ? (role - 1) * 128 : tile.y + (int)rank * 128;
-    const int64_t row0 = role ? (int64_t)tile.z + first : (int64_t)tile.x * a.N + first;
-    if (TMA) {
-      if (elect()) {
-        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(
-                         smem_addr(bar)),
-                     "r"(box_rows * 16)
-                     : "memory");
-        asm volatile(
-            "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes "
-            "[%0], [%1, {%2, %3}], [%4];" ::"r"(box),
-            "l"(map), "r"(lc * 16), "r"((int)row0), "r"(smem_addr(bar))
-            : "memory");
-      }
-    } else {
-      const int rows = (role ? tile.w : a.N) - first;
-#pragma unroll
-      for (int i = 0; i < 4; i++)
-        v[i] = load_bytes(base, end, base + (row0 + lane + 32 * i) * pitch + lc * 16,
-                          lane + 32 * i < rows ? min(16, nsc - lc * 16) : 0);
-    }
-    lc += 2;
-  };
-  int t = 0, c = 0;  // tile and chunk to fill next
-  auto next = [&] {
-    if (++s == kStages) {
-      s = 0;
-      phase ^= 1;
-    }
-    if (++c == chunks) {
-      c = 0;
-      t++;
-    }
-  };
-  load();
-  if (turn) next();
-  while (t < mine && ok) {
-    if (TMA) {
-      if (!(ok = wait(sh, bar, box_phase, a.status))) break;
-      box_phase ^= 1;
-#pragma unroll
-      for (int i = 0; i < 4; i++)
-        if (role < 2 || i * 32 + lane < kMaxCols - 128)
-          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(v[i].x), "=r"(v[i].y), "=r"(v[i].z), "=r"(v[i].w)
-                       : "r"(box + (i * 32 + lane) * 16)
-                       : "memory");
-        else
-          v[i] = make_uint4(0, 0, 0, 0);
-      __syncwarp();
-    }
-    const uint4 w[4] = {v[0], v[1], v[2], v[3]};
-    load();
-    if (!ok || !(ok = wait(sh, &sh->empty[s], phase ^ 1, a.status))) break;
-    const uint32_t p = smem_addr(sh->stage[s]) + at;
-#pragma unroll
-    for (int i = 0; i < 4; i++)
-      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(p + i * (role ? 1024 : 512)),
-                   "r"(word(w[0], i)), "r"(word(w[1], i)), "r"(word(w[2], i)), "r"(word(w[3], i))
-                   : "memory");
-    // the tensor cores read these lines through the async proxy
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    __syncwarp();
-    if (lane == 0) arrive_leader(&sh->full[s]);
-    next();
-    if (t < mine) next();  // past the other set's stage
-  }
-  // given up: a box in flight ends before the CTA does
-  if (TMA && !ok) {
-    const long long t0 = now_ns();
-    while (!try_wait(smem_addr(bar), box_phase) && now_ns() - t0 < kLimitNs / 4) {
-    }
-  }
 }
 
 template <typename T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     product_kernel(const __grid_constant__ CUtensorMap map_w,
                    const __grid_constant__ CUtensorMap map_a,
-                   const __grid_constant__ CUtensorMap map_wide,
-                   const __grid_constant__ CUtensorMap map_ws,
-                   const __grid_constant__ CUtensorMap map_as,
-                   const __grid_constant__ CUtensorMap map_as2, const ProductArgs a) {
+                   const __grid_constant__ CUtensorMap map_wide, const ProductArgs a) {
   extern __shared__ uint8_t raw[];
   Shared *sh = (Shared *)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
   const int tid = threadIdx.x, lane = tid & 31;
@@ -512,7 +373,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int s = 0; s < kStages; s++) {
       // full: the leader's expect_tx and one set of scale warps of each CTA
       asm volatile("mbarrier.init.shared::cta.b64 [%0], 7;" ::"r"(smem_addr(&sh->full[s])));
-      asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_addr(&sh->scaled[s])));
       asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_addr(&sh->empty[s])));
     }
     for (int b = 0; b < 2; b++) {
@@ -520,8 +380,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_addr(&sh->tile_full[b])));
       asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(&sh->tile_empty[b])),
                    "r"(rank == 0 ? 16 : 15));
-      for (int i = 0; i < 3; i++)
-        asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_addr(&sh->sf_full[b][i])));
       asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_addr(&sh->acc_full[b])));
       // eight epilogue warps of each CTA
       asm volatile("mbarrier.init.shared::cta.b64 [%0], 16;" ::"r"(smem_addr(&sh->acc_empty[b])));
@@ -555,31 +413,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int half = ((tile.w + 15) & ~15) >> 1;
       const bool wide = half > 2 * kBoxRows;
       const int boxes = (half + kBoxRows - 1) / kBoxRows;
-      const uint32_t bytes = 2u * (kATile + (wide ? kWideRows : boxes * kBoxRows) * 128);
+      const uint32_t bytes = 2u * (kABytes + (wide ? kWideRows : boxes * kBoxRows) * 128);
       const int wrow = tile.x * a.N + tile.y + (int)rank * 128;
       const int arow = tile.z + (int)rank * half;
       for (int k = 0; k < stages; k++) {
         if (!(ok = wait(sh, &sh->empty[s], phase ^ 1, a.status))) break;
         const uint32_t base = smem_addr(sh->stage[s]);
         const uint32_t full = smem_addr(&sh->full[s]), bar = full + to_leader;
-        const int n = k * kStageK + 256 < a.Kd ? 2 : 1;  // operand tiles
         if (elect()) {
           if (rank == 0)
             asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(full),
-                         "r"(n * bytes)
+                         "r"(bytes)
                          : "memory");
-#pragma unroll
-          for (int i = 0; i < 2; i++) {
-            if (i >= n) break;
-            const int x = k * (kStageK / 2) + i * 128;
-            const uint32_t rows = base + kBOff + i * kBTile;
-            tma_load(base + i * kATile, &map_w, x, wrow, bar);
-            if (wide) {
-              tma_load(rows, &map_wide, x, arow, bar);
-            } else {
-              tma_load(rows, &map_a, x, arow, bar);
-              if (boxes > 1) tma_load(rows + kBoxRows * 128, &map_a, x, arow + kBoxRows, bar);
-            }
+          tma_load(base, &map_w, k * 128, wrow, bar);
+          if (wide) {
+            tma_load(base + kABytes, &map_wide, k * 128, arow, bar);
+          } else {
+            tma_load(base + kABytes, &map_a, k * 128, arow, bar);
+            if (boxes > 1)
+              tma_load(base + kABytes + kBoxRows * 128, &map_a, k * 128, arow + kBoxRows, bar);
           }
         }
         pending |= 1u << s;
@@ -599,15 +451,95 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
       }
   } else if (warp < 7) {
-    const int role = (warp - 1) % 3;
-    if (a.sf_tma)
-      scale_warp<true>(sh, a, rank, mine, stages,
-                       role == 0 ? &map_ws : role == 1 ? &map_as : &map_as2);
-    else
-      scale_warp<false>(sh, a, rank, mine, stages, nullptr);
+    // role 0: the CTA's 128 weight rows; 1, 2: the piece's rows 0-127, 128-191.
+    // A warp takes every second chunk (512 values of k, two stages) of the
+    // CTA's sequence of tiles, two of its chunks' loads in flight.
+    const int role = (warp - 1) % 3, turn = (warp - 1) / 3;
+    const int nsc = a.Kd / 32, chunks = (a.Kd + 511) / 512;
+    const bool vec = role ? a.as16 : a.ws16;
+    const uint8_t *base = role ? a.as : a.ws;
+    const int64_t pitch = role ? a.lds : nsc;
+    const int64_t total = role ? ((int64_t)a.R * a.NvS - 1) * a.lds + nsc
+                               : (int64_t)a.groups * a.N * nsc;
+    const uint32_t at = kABytes + kBBytes + (role ? 1024 + (role - 1) * 512 : 0) + lane * 16;
+    uint32_t s = 0, phase = 0;
+    bool ok = true;
+    int li = 0, lc = turn, have = -1;  // tile and chunk to load next; tile in `tile`
+    int4 tile = make_int4(0, 0, 0, 0);
+    auto load = [&](uint4 v[4]) {
+      for (; lc >= chunks; lc -= chunks) li++;
+      if (!ok) return;
+      for (; have < li && have < mine - 1; have++)
+        if (!(ok = next_tile(sh, have + 1, a.status, &tile))) return;
+      if (li >= mine) return;
+      const int lim = role ? tile.w - (role - 1) * 128 : a.N - tile.y - (int)rank * 128;
+      const int64_t row0 = role ? (int64_t)tile.z + (role - 1) * 128
+                                : (int64_t)tile.x * a.N + tile.y + rank * 128;
+#pragma unroll
+      for (int i = 0; i < 4; i++)
+        v[i] = load_scales(base, total, row0 + lane + 32 * i, pitch, lc * 16, nsc, vec,
+                           lane + 32 * i < lim);
+      lc += 2;
+    };
+    // moves the stage on by n, at most kStages
+    auto skip = [&](int n) {
+      s += n;
+      if (s >= kStages) {
+        s -= kStages;
+        phase ^= 1;
+      }
+    };
+    // writes a chunk's scales into its one or two stages
+    auto fill = [&](const uint4 v[4], int c) {
+#pragma unroll
+      for (int h = 0; h < 2; h++) {
+        if (c * 2 + h >= stages) break;
+        if (!wait(sh, &sh->empty[s], phase ^ 1, a.status)) return false;
+        const uint32_t p = smem_addr(sh->stage[s]) + at;
+#pragma unroll
+        for (int i = 0; i < 2; i++)
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                           p + i * (role ? 1024 : 512)),
+                       "r"(word(v[0], 2 * h + i)), "r"(word(v[1], 2 * h + i)),
+                       "r"(word(v[2], 2 * h + i)), "r"(word(v[3], 2 * h + i))
+                       : "memory");
+        // the tensor cores read these lines through the async proxy
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) arrive_leader(&sh->full[s]);
+        skip(1);
+      }
+      return true;
+    };
+    uint4 buf[2][4];
+    load(buf[0]);
+    load(buf[1]);
+    int t = 0, c = 0;  // tile and chunk to fill next
+    auto move = [&] {
+      if (++c == chunks) {
+        c = 0;
+        t++;
+      }
+    };
+    // past the other set's chunk
+    auto pass = [&] {
+      skip(min(2, stages - 2 * c));
+      move();
+    };
+    if (turn) pass();
+    while (t < mine && ok) {
+#pragma unroll
+      for (int i = 0; i < 2; i++) {
+        if (t >= mine || !ok) break;
+        if (!(ok = fill(buf[i], c))) break;
+        load(buf[i]);
+        move();
+        if (t < mine) pass();
+      }
+    }
   } else if (warp == 7) {
     if (rank == 0) {
-      uint32_t s = 0, phase = 0, slot = 0;
+      uint32_t s = 0, phase = 0;
       int it = 0;
       bool ok = true;
       const uint32_t stage0 = smem_addr(sh->stage[0]);
@@ -620,26 +552,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // E2M1 both sides, E8M0 scales, M = 256, N = cols
         const uint32_t idesc = (1u << 7) | (1u << 10) | (1u << 23) | ((uint32_t)(cols >> 3) << 17) |
                                (16u << 24);
-        const uint32_t odd = (1u << 5) | (1u << 30);  // the second two scales of a word
+        const bool wide = cols > 128;
         for (int k = 0; k < stages; k++) {
-          // the operands too: the scales are copied after they arrive
-          if (!(ok = wait(sh, &sh->scaled[s], phase, a.status))) break;
+          if (!(ok = wait(sh, &sh->full[s], phase, a.status))) break;
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
           const uint32_t base = stage0 + s * kStageBytes;
-          const uint32_t ca = tmem + kSfBase + slot * kSfCols, cb = ca + 16;
+          const uint32_t sf = base + kABytes + kBBytes;
+          const uint32_t ca = tmem + kSfBase + s * kSfCols, cb = ca + 8;
           const int deep = (a.Kd - k * kStageK + 63) >> 6;
-          const uint64_t da = operand_desc(base), db = operand_desc(base + kBOff);
+          const uint64_t da = operand_desc(base), db = operand_desc(base + kABytes);
           if (elect()) {
 #pragma unroll
-            for (int q = 0; q < 8; q++)
+            for (int i = 0; i < 2; i++) {
+              scales_to_tmem(ca + i * 4, sf + i * 512);
+              scales_to_tmem(cb + i * 8, sf + 1024 + i * 1024);
+              if (wide) scales_to_tmem(cb + i * 8 + 4, sf + 1024 + i * 1024 + 512);
+            }
+#pragma unroll
+            for (int q = 0; q < 4; q++)
               if (q < deep)
-                mma(d, da + (q >> 2) * (kATile >> 4) + 2 * (q & 3),
-                    db + (q >> 2) * (kBTile >> 4) + 2 * (q & 3), q & 1 ? idesc | odd : idesc,
+                mma(d, da + 2 * q, db + 2 * q,
+                    idesc | ((uint32_t)(q & 1) << 5) | ((uint32_t)(q & 1) << 30),
                     ca + (q >> 1) * 4, cb + (q >> 1) * 8, k + q > 0);
             commit(&sh->empty[s]);
             if (k == stages - 1) commit(&sh->acc_full[it & 1]);
           }
-          slot = (slot + 1) % kSlots;
           if (++s == kStages) {
             s = 0;
             phase ^= 1;
@@ -651,8 +588,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // epilogue: lane = output n, accumulator columns = rows
     const int q = warp & 3, group = (warp >> 2) & 1;
     const bool odd = lane & 1;
-    // bytes of a row's two columns in (own two rows, neighbour's two rows)
-    const uint32_t pick = odd ? 0x3276u : 0x5410u;
     for (int it = 0; it < mine; it++) {
       int4 tile;
       if (!next_tile(sh, it, a.status, &tile)) break;
@@ -662,34 +597,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int n = tile.y + (int)rank * 128 + q * 32 + (lane & ~1);
       const int rows = n < a.N ? tile.w - odd : 0;
       T *out = (T *)a.out + ((int64_t)tile.z + odd) * a.N + n;
-      // 32 columns while the next 32 load.  The last 16 of a piece may be
-      // another accumulator's: read, not stored.
-      auto store = [&](const uint32_t v[32], int c) {
-        T *p = out + (int64_t)c * a.N;
+      for (int c = group * 32; c < tile.w; c += 64) {
+        // the last 16 columns of a piece may be another accumulator's: read,
+        // not stored
+        uint32_t v[32];
+        tmem_load(v, d + c);
+        tmem_load(v + 16, d + c + 16);
+        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+        // neighbouring lanes swap so that each holds both columns of one row
 #pragma unroll
         for (int i = 0; i < 32; i += 2) {
-          store_pair(c + i < rows ? p : (T *)nullptr, v[i], v[i + 1], odd, pick);
-          p += 2 * a.N;
-        }
-      };
-      uint32_t u[32], v[32];
-      int c = group * 32;
-      if (c < tile.w) tmem_load(u, d + c);
-      for (; c < tile.w; c += 128) {
-        tmem_wait(u);
-        if (c + 64 < tile.w) tmem_load(v, d + c + 64);
-        store(u, c);
-        if (c + 64 < tile.w) {
-          tmem_wait(v);
-          if (c + 128 < tile.w) tmem_load(u, d + c + 128);
-          store(v, c + 64);
+          const float mine = __uint_as_float(odd ? v[i + 1] : v[i]);
+          const float give = __uint_as_float(odd ? v[i] : v[i + 1]);
+          const float got = __shfl_xor_sync(0xffffffffu, give, 1);
+          if (c + i < rows)
+            store_pair(out + (int64_t)(c + i) * a.N, odd ? got : mine, odd ? mine : got);
         }
       }
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
       __syncwarp();
       if (lane == 0) arrive_leader(&sh->acc_empty[it & 1]);
     }
-  } else if (warp == 16) {
+  } else {
     // 32 tiles at a time, two such batches
     for (int i = 0; i < mine; i += 32) {
       const int b = (i >> 5) & 1;
@@ -697,33 +626,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (i + lane < mine) sh->tile[b][lane] = tile_of(a, sh, first + (i + lane) * step);
       __syncwarp();
       if (lane == 0) arrive(&sh->tile_full[b]);
-    }
-  } else if (rank == 0) {
-    uint32_t s = 0, phase = 0, slot = 0, used = 0, used_phase = 0;
-    const int64_t all = (int64_t)mine * stages;
-    for (int64_t i = 0; i < all; i++) {
-      if (!wait(sh, &sh->full[s], phase, a.status)) break;
-      // the slot's last products are done: those of the stage kSlots before
-      if (i >= kSlots) {
-        if (!wait(sh, &sh->empty[used], used_phase, a.status)) break;
-        if (++used == kStages) {
-          used = 0;
-          used_phase ^= 1;
-        }
-      }
-      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      if (elect()) {
-        stage_scales(smem_addr(sh->stage[s]), tmem + kSfBase + slot * kSfCols);
-        asm volatile(
-            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                smem_addr(&sh->scaled[s]))
-            : "memory");
-      }
-      slot = (slot + 1) % kSlots;
-      if (++s == kStages) {
-        s = 0;
-        phase ^= 1;
-      }
     }
   }
   __syncwarp();
@@ -772,17 +674,15 @@ EncodeFn encoder() {
   return fn;
 }
 
-// Rows of `bytes` bytes, `pitch` apart, in boxes of `box` rows x 128 swizzled
-// bytes (operands) or 16 plain bytes (scales).
-bool make_map(CUtensorMap *m, const void *p, int64_t bytes, int64_t rows, int64_t pitch, int box,
-              bool scales = false) {
+// Rows of `bytes` packed bytes, `pitch` apart, in boxes of `box` rows x 128
+// bytes.
+bool make_map(CUtensorMap *m, const void *p, int64_t bytes, int64_t rows, int64_t pitch, int box) {
   const cuuint64_t dims[2] = {(cuuint64_t)bytes, (cuuint64_t)rows};
   const cuuint64_t strides[1] = {(cuuint64_t)pitch};
-  const cuuint32_t boxes[2] = {scales ? 16u : 128u, (cuuint32_t)box}, one[2] = {1, 1};
+  const cuuint32_t boxes[2] = {128, (cuuint32_t)box}, one[2] = {1, 1};
   return encoder() &&
          encoder()(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, (void *)p, dims, strides, boxes, one,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE,
-                   scales ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -825,16 +725,10 @@ int launch_product(moonep_ctx *ctx, const int32_t *cu, const uint8_t *rows, int6
   }
   if (ctx->product_clusters <= 0) return MOONEP_ERR_CUDA;
   const int64_t groups = (int64_t)c.E + (int64_t)c.R * c.B;
-  const int64_t all_rows = (int64_t)c.R * ctx->NvS;
-  const bool sf_tma = Kd % 512 == 0 && lds % 16 == 0 && aligned16(row_scales) && aligned16(w_scales);
-  CUtensorMap mw, ma, mwide, mws{}, mas[2] = {};
+  CUtensorMap mw, ma, mwide;
   if (!make_map(&mw, w, Kd / 2, groups * N, Kd / 2, 128) ||
-      !make_map(&ma, rows, Kd / 2, all_rows, lda, kBoxRows) ||
-      !make_map(&mwide, rows, Kd / 2, all_rows, lda, kWideRows))
-    return MOONEP_ERR_CUDA;
-  if (sf_tma && (!make_map(&mws, w_scales, Kd / 32, groups * N, Kd / 32, 128, true) ||
-                 !make_map(&mas[0], row_scales, Kd / 32, all_rows, lds, 128, true) ||
-                 !make_map(&mas[1], row_scales, Kd / 32, all_rows, lds, kMaxCols - 128, true)))
+      !make_map(&ma, rows, Kd / 2, (int64_t)c.R * ctx->NvS, lda, kBoxRows) ||
+      !make_map(&mwide, rows, Kd / 2, (int64_t)c.R * ctx->NvS, lda, kWideRows))
     return MOONEP_ERR_CUDA;
   ProductArgs a{};
   a.as = row_scales;
@@ -852,11 +746,12 @@ int launch_product(moonep_ctx *ctx, const int32_t *cu, const uint8_t *rows, int6
   a.Kd = Kd;
   a.groups = (int)groups;
   a.per = (int)((groups + kEntries - 1) / kEntries);
-  a.sf_tma = sf_tma;
+  a.as16 = Kd % 512 == 0 && lds % 16 == 0 && aligned16(row_scales);
+  a.ws16 = Kd % 512 == 0 && aligned16(w_scales);
   a.status = ctx->d_status;
   auto kern = fp32 ? product_kernel<float> : product_kernel<__nv_bfloat16>;
   return cuda_status(launch_pdl(kern, dim3(2 * ctx->product_clusters), dim3(kThreads), kSmem, st,
-                                false, mw, ma, mwide, mws, mas[0], mas[1], a));
+                                false, mw, ma, mwide, a));
 }
 
 }  // namespace moonep
