@@ -214,6 +214,54 @@ __device__ void finish_block(const RouteArgs &a, int32_t *cnt, float *acc, int w
                  ::: "memory");
 }
 
+// The K largest of a warp's keys (V per lane, index col + i), in order, into
+// stage[0..K): the K-th largest of the lanes' maxima is at most the K-th
+// largest key, so the few keys at or above it (usually K to K + 4 of 256)
+// move to one per lane, through buf, and the rounds work on a single register:
+// 170 instructions for K = 8, V = 8, against 400 over all keys.  False, with
+// nothing written, when more than a warp's worth of keys qualify (equal
+// logits).
+template <int V>
+__device__ __forceinline__ bool pick_few(const uint32_t key[V], int col, int K, int lane,
+                                         uint2 *buf, uint2 *stage) {
+  uint32_t best = key[0];
+#pragma unroll
+  for (int i = 1; i < V; i++) best = max(best, key[i]);
+  uint32_t least = 0;
+  for (int k = 0; k < K; k++) {
+    least = __reduce_max_sync(0xffffffffu, best);
+    const int src = __ffs(__ballot_sync(0xffffffffu, best == least)) - 1;
+    if (lane == src) best = 0;
+  }
+  if (least == 0) least = 1;  // fewer lanes than picks hold logits
+  int n = 0;
+  unsigned in[V];
+#pragma unroll
+  for (int i = 0; i < V; i++) {
+    in[i] = __ballot_sync(0xffffffffu, key[i] >= least);
+    n += __popc(in[i]);
+  }
+  if (n > 32) return false;
+  const unsigned before = (1u << lane) - 1;
+  int at = 0;
+#pragma unroll
+  for (int i = 0; i < V; i++) {
+    if (key[i] >= least) buf[at + __popc(in[i] & before)] = make_uint2(key[i], col + i);
+    at += __popc(in[i]);
+  }
+  __syncwarp();
+  uint2 c = lane < n ? buf[lane] : make_uint2(0u, 0xffffffffu);
+  for (int k = 0; k < K; k++) {
+    const uint32_t top = __reduce_max_sync(0xffffffffu, c.x);
+    const uint32_t id = __reduce_min_sync(0xffffffffu, c.x == top ? c.y : 0xffffffffu);
+    if (c.y == id) {
+      stage[k] = c;
+      c.x = 0;
+    }
+  }
+  return true;
+}
+
 // Rows of at most LP * V logits in registers, LP lanes to a token, lane l
 // holding columns l*V .. l*V + V - 1 (so the lowest lane and the lowest of its
 // values is the lowest index).  A round finds the largest key that is left:
@@ -228,6 +276,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(RouteArgs a, bool ve
   float *acc = sh;                                             // [kWarps, E]
   int32_t *cnt = (int32_t *)(sh + (size_t)kWarps * a.E);       // [E]
   uint2 *stage = (uint2 *)(cnt + ((a.E + 1) & ~1));            // [tokens, K] (key, index)
+  uint2 *few = stage + (size_t)kWarps * kTok * a.K + (threadIdx.x >> 5) * 32;  // LP == 32
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = lane / LP, col = (lane % LP) * V;
   const int r = blockIdx.y, n = a.ntok[r];
@@ -248,8 +297,8 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(RouteArgs a, bool ve
     uint32_t key[V];
 #pragma unroll
     for (int i = 0; i < V; i++) key[i] = col + i < a.E ? order_key(z[i]) : 0u;
-    float m = -INFINITY;
-    for (int k = 0; k < a.K; k++) {
+    const bool done = LP == 32 && V >= 8 && pick_few<V>(key, col, a.K, lane, few, stage);
+    for (int k = 0; k < a.K && !done; k++) {
       uint32_t best = key[0];
 #pragma unroll
       for (int i = 1; i < V; i++) best = max(best, key[i]);
@@ -278,7 +327,6 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(RouteArgs a, bool ve
         }
         win = tid == id;
       }
-      if (k == 0) m = key_value(top);
       // the winner notes its pick and drops it
       bool look = win;
 #pragma unroll
@@ -291,6 +339,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(RouteArgs a, bool ve
       if (win) stage[k] = make_uint2(top, id);
     }
     __syncwarp();
+    const float m = key_value(stage[0].x);
     // weights: the group's lanes share the picks
     float Zk = 0.0f;
     for (int k = lane % LP; k < a.K; k += LP) Zk += score(key_value(stage[k].x), m, a.sigmoid);
@@ -657,13 +706,14 @@ bool whole_vectors(int E, int bf16) { return E % (bf16 ? 8 : 4) == 0; }
 int warps_of(int E) { return E <= 1024 ? kWarps : 4; }
 
 // Blocks per rank of the forward pass: enough for the rank's tokens, at most
-// two per SM over all ranks; a power of two up to the cluster size, then a
+// four per SM over all ranks (the selection is a chain of warp-wide steps, so
+// it wants warps: two per SM took 48 us for 32768 x 256); a power of two up to the cluster size, then a
 // multiple of it.
 int blocks_per_rank(int R, int S, int E, int sms) {
   const Form f = form_of(E);
   const int per = (f == kLong ? warps_of(E) : kWarps) * tokens_per_warp(f);
   const int64_t need = ((int64_t)S + per - 1) / per;
-  const int64_t cap = (2 * sms + R - 1) / R;
+  const int64_t cap = (4 * sms + R - 1) / R;
   int64_t b = need < cap ? need : cap;
   if (b >= kCluster) return (int)(b / kCluster * kCluster);
   int p = 1;
@@ -677,7 +727,8 @@ cudaError_t launch_forward(const RouteArgs &a, int bpr, cudaStream_t st) {
   const Form f = form_of(a.E);
   const bool vec = whole_vectors(a.E, sizeof(T) == 2);
   size_t smem = ((size_t)kWarps * a.E + ((a.E + 1) & ~1)) * 4 +
-                (size_t)kWarps * tokens_per_warp(f) * a.K * sizeof(uint2);
+                (size_t)kWarps * tokens_per_warp(f) * a.K * sizeof(uint2) +
+                (tokens_per_warp(f) == 1 ? (size_t)kWarps * 32 * sizeof(uint2) : 0);
   switch (f) {
     case kThread8: return launch_pdl_ex(route_kernel<T, 1, 8>, grid, block, smem, st, false, a.cluster, a, vec);
     case kFour8: return launch_pdl_ex(route_kernel<T, 4, 8>, grid, block, smem, st, false, a.cluster, a, vec);
@@ -720,8 +771,8 @@ cudaError_t launch_backward(const RouteBwdArgs &a, int sms, cudaStream_t st) {
 }  // namespace
 
 int64_t route_scratch_words(int R, int E, int sms) {
-  // at most 2 * sms / R + 1 blocks per rank
-  return (int64_t)2 * R * ((2 * sms + R - 1) / R / kCluster + 1) * E;
+  // at most 4 * sms / R + 1 blocks per rank
+  return (int64_t)2 * R * ((4 * sms + R - 1) / R / kCluster + 1) * E;
 }
 
 int launch_route(moonep_ctx *ctx, const void *logits, int bf16, int scoring, float alpha, int global,
