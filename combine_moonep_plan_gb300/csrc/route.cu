@@ -39,12 +39,12 @@ struct RouteArgs {
   int32_t ntok[kMaxRanks];
 };
 
-// Order-preserving bits: a larger logit has a larger key, -0 equals +0, NaN
-// is largest; 0 is below every logit.
+// Order-preserving bits: a larger logit has a larger key, -0 equals +0 and NaN
+// is largest (adding +0 turns -0 into +0 and every NaN into 0x7fffffff); 0 is
+// below every logit.
 __device__ __forceinline__ uint32_t order_key(float v) {
-  if (v != v) return 0xffffffffu;
-  const uint32_t b = __float_as_uint(v + 0.0f);
-  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+  const uint32_t b = __float_as_uint(__fadd_rn(v, 0.0f));
+  return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
 
 // The logit of a key (NaN for the NaN key).
@@ -66,10 +66,24 @@ __device__ __forceinline__ float group_sum(float v) {
   return v;
 }
 
-// Score of one logit; m is the row's maximum (softmax).
+// exp(x) as a power of two: two parts in 2^23, and the rounding of x log2(e)
+// (|x| parts in 2^24); below 2^-126 zero.  1/x within an ulp.
+__device__ __forceinline__ float exp_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
+  return r;
+}
+__device__ __forceinline__ float inverse(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// Score of one logit; m is the row's maximum (softmax).  exp(-z) may be
+// infinite, its inverse is then zero.
 __device__ __forceinline__ float score(float z, float m, bool sigmoid) {
-  if (sigmoid) return __fdividef(1.0f, 1.0f + __expf(-z));
-  return m == -INFINITY ? 0.0f : __expf(z - m);
+  if (sigmoid) return inverse(1.0f + exp_fast(-z));
+  return m == -INFINITY ? 0.0f : exp_fast(z - m);
 }
 
 __device__ __forceinline__ float to_f(float v) { return v; }
@@ -230,8 +244,7 @@ __device__ __forceinline__ bool pick_few(const uint32_t key[V], int col, int K, 
   uint32_t least = 0;
   for (int k = 0; k < K; k++) {
     least = __reduce_max_sync(0xffffffffu, best);
-    const int src = __ffs(__ballot_sync(0xffffffffu, best == least)) - 1;
-    if (lane == src) best = 0;
+    if (best == least) best = 0;  // equal maxima together: only more keys qualify
   }
   if (least == 0) least = 1;  // fewer lanes than picks hold logits
   int n = 0;
@@ -357,7 +370,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(RouteArgs a, bool ve
       float Z = 0.0f;
 #pragma unroll
       for (int i = 0; i < V; i++) {
-        z[i] = col + i < a.E ? score(z[i], m, a.sigmoid) : 0.0f;
+        z[i] = score(z[i], m, a.sigmoid);  // -inf past the row's end: 0
         Z += z[i];
       }
       Z = group_sum<LP>(Z);
@@ -448,7 +461,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_long_kernel(RouteArgs a) {
 }
 
 struct FinishArgs {
-  const float *part_p;
+  float *part_p;
   const int32_t *part_c;
   int32_t *tpe;  // [R, E]
   float *coef;   // [R, E] or null
@@ -458,68 +471,89 @@ struct FinishArgs {
   int32_t ntok[kMaxRanks];
 };
 
-// Sums the clusters' partials in order: counts, coefficients, loss.  A warp
-// takes 32 experts of one rank (rank scope), so its loads are rows of 128
-// bytes; the loss is added up over (rank, expert) in a fixed order.
-__global__ void __launch_bounds__(1024) route_finish_kernel(FinishArgs a) {
+constexpr int kFinishBlocks = 8;
+
+__device__ __forceinline__ void finish_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+
+// Sums the route kernel's partials in order: counts, coefficients, loss.  One
+// cluster; block b takes ranks b, b + 8, ... and, in global scope, a share of
+// the experts once every rank is summed.
+__global__ void __cluster_dims__(kFinishBlocks, 1, 1) __launch_bounds__(256)
+    route_finish_kernel(FinishArgs a) {
   pdl_wait();
   pdl_launch_dependents();
-  __shared__ float red[32];
+  __shared__ float red[8];
+  __shared__ float share[kFinishBlocks];  // block 0's: the blocks' parts of the loss
+  const int b = blockIdx.x;
   int64_t total = 0;
   int busy = 0;
   for (int r = 0; r < a.R; r++) {
     total += a.ntok[r];
     busy += a.ntok[r] > 0;
   }
+  const float groups = (float)(busy > 0 ? busy : 1);
   float loss = 0.0f;
-  if (!a.global || !a.loss) {
-    for (int i = threadIdx.x; i < a.R * a.E; i += blockDim.x) {
-      const int r = i / a.E, e = i - r * a.E;
+  for (int r = b; r < a.R; r += kFinishBlocks) {
+    const int n = a.ntok[r];
+    const float t = (float)(n > 0 ? n : 1);
+    const float q0 = a.alpha * (float)a.E / ((float)a.K * t * t * groups);
+    for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
       const int64_t o = (int64_t)r * a.parts * a.E + e;
       int c = 0;
       float p = 0.0f;
-#pragma unroll 4
-      for (int b = 0; b < a.parts; b++) {
-        c += __ldg(a.part_c + o + (int64_t)b * a.E);
-        if (a.loss) p += __ldg(a.part_p + o + (int64_t)b * a.E);
+#pragma unroll 8
+      for (int i = 0; i < a.parts; i++) {
+        c += a.part_c[o + (int64_t)i * a.E];
+        if (a.loss) p += a.part_p[o + (int64_t)i * a.E];
       }
-      const int n = a.ntok[r];
-      a.tpe[i] = c + (e == 0 ? (a.S - n) * a.K : 0);
+      a.tpe[(int64_t)r * a.E + e] = c + (e == 0 ? (a.S - n) * a.K : 0);
       if (!a.loss) continue;
-      const float t = (float)(n > 0 ? n : 1);
-      const float q = a.alpha * (float)a.E * (float)c /
-                      ((float)a.K * t * t * (float)(busy > 0 ? busy : 1));
-      a.coef[i] = q;
-      loss += q * p;
-    }
-  } else {
-    for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
-      int64_t call = 0;
-      float pall = 0.0f;
-      for (int r = 0; r < a.R; r++) {
-        const int64_t o = (int64_t)r * a.parts * a.E + e;
-        int c = 0;
-#pragma unroll 4
-        for (int b = 0; b < a.parts; b++) {
-          c += __ldg(a.part_c + o + (int64_t)b * a.E);
-          pall += __ldg(a.part_p + o + (int64_t)b * a.E);
-        }
-        a.tpe[(int64_t)r * a.E + e] = c + (e == 0 ? (a.S - a.ntok[r]) * a.K : 0);
-        call += c;
+      if (a.global) {
+        a.part_p[o] = p;  // read again below, by another block
+      } else {
+        a.coef[(int64_t)r * a.E + e] = q0 * (float)c;
+        loss += q0 * (float)c * p;
       }
-      const float t = (float)(total > 0 ? total : 1);
-      const float q = a.alpha * (float)a.E * (float)call / ((float)a.K * t * t);
-      for (int r = 0; r < a.R; r++) a.coef[(int64_t)r * a.E + e] = q;
-      loss += q * pall;
     }
   }
   if (!a.loss) return;
+  if (a.global) {
+    finish_sync();
+    const float t = (float)(total > 0 ? total : 1);
+    const float q0 = a.alpha * (float)a.E / ((float)a.K * t * t);
+    for (int e = b * blockDim.x + threadIdx.x; e < a.E; e += kFinishBlocks * blockDim.x) {
+      int64_t c = 0;
+      float p = 0.0f;
+#pragma unroll 8
+      for (int r = 0; r < a.R; r++) {
+        c += a.tpe[(int64_t)r * a.E + e] - (e == 0 ? (a.S - a.ntok[r]) * a.K : 0);
+        p += a.part_p[(int64_t)r * a.parts * a.E + e];
+      }
+      for (int r = 0; r < a.R; r++) a.coef[(int64_t)r * a.E + e] = q0 * (float)c;
+      loss += q0 * (float)c * p;
+    }
+  }
   loss = warp_sum(loss);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = loss;
   __syncthreads();
-  if (threadIdx.x < 32) {
-    const float v = warp_sum(red[threadIdx.x]);
-    if (threadIdx.x == 0) *a.loss = v;
+  if (threadIdx.x == 0) {
+    float v = 0.0f;
+    for (int i = 0; i < (int)(blockDim.x >> 5); i++) v += red[i];
+    uint32_t to;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;"
+                 : "=r"(to)
+                 : "r"((uint32_t)__cvta_generic_to_shared(share + b)));
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to), "f"(v) : "memory");
+  }
+  __syncwarp();
+  finish_sync();
+  if (b == 0 && threadIdx.x == 0) {
+    float v = 0.0f;
+    for (int i = 0; i < kFinishBlocks; i++) v += share[i];
+    *a.loss = v;
   }
 }
 
@@ -536,9 +570,7 @@ struct RouteBwdArgs {
 };
 
 // 1 - sigmoid(z), without cancellation.
-__device__ __forceinline__ float one_minus_sigmoid(float z) {
-  return __fdividef(1.0f, 1.0f + __expf(z));
-}
+__device__ __forceinline__ float one_minus_sigmoid(float z) { return inverse(1.0f + exp_fast(z)); }
 
 // The same layout of rows in registers; blockIdx.y is the rank, whose
 // coefficients stay in registers too.  A pick's term reaches the lane of its
@@ -561,40 +593,79 @@ __global__ void __launch_bounds__(kWarps * 32) route_backward_kernel(RouteBwdArg
     row[col + i] = 0.0f;
   }
   __syncwarp();
-  for (int s0 = (blockIdx.x * kWarps + warp) * kTok; s0 < a.S; s0 += gridDim.x * kWarps * kTok) {
+  // a row and its picks, loaded while the row before is worked on; a warp to a
+  // token holds one pick per lane
+  constexpr int kPicks = LP == 32 ? 1 : 8;  // K is at most LP * V, and at most 32
+  const int stride = gridDim.x * kWarps * kTok;
+  float ahead[V], pw[kPicks], pd[kPicks];
+  int pid[kPicks];
+  auto fetch = [&](int s) {
+    const int64_t t = (int64_t)r * a.S + s;
+#pragma unroll
+    for (int i = 0; i < V; i++) ahead[i] = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kPicks; i++) {
+      pid[i] = -1;
+      pw[i] = pd[i] = 0.0f;
+    }
+    if (s >= n) return;
+    load_row<V>((const T *)a.logits + t * a.E, col, a.E, vec, ahead);
+    if (!a.dw) return;
+#pragma unroll
+    for (int i = 0; i < kPicks; i++) {
+      const int k = i * LP + lane % LP;
+      if (k < a.K) {
+        pid[i] = __ldg(a.topk + t * a.K + k);
+        pw[i] = __ldg(a.w + t * a.K + k);
+        pd[i] = __ldg(a.dw + t * a.K + k);
+      }
+    }
+  };
+  fetch((blockIdx.x * kWarps + warp) * kTok + sub);
+  for (int s0 = (blockIdx.x * kWarps + warp) * kTok; s0 < a.S; s0 += stride) {
     const int s = s0 + sub;
     const int64_t t = (int64_t)r * a.S + s;
     const bool on = s < n;
     float z[V], g[V];
 #pragma unroll
-    for (int i = 0; i < V; i++) z[i] = -INFINITY;
-    float wd = 0.0f;
-    if (on) {
-      load_row<V>((const T *)a.logits + t * a.E, col, a.E, vec, z);
-      if (a.dw)
-        for (int k = lane % LP; k < a.K; k += LP)
-          wd += __ldg(a.w + t * a.K + k) * __ldg(a.dw + t * a.K + k);
+    for (int i = 0; i < V; i++) z[i] = ahead[i];
+    if (a.dw) {
+      float wd = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kPicks; i++) wd += pw[i] * pd[i];
+      wd = group_sum<LP>(wd);
+#pragma unroll
+      for (int i = 0; i < kPicks; i++)
+        if (pid[i] >= 0 && pid[i] < a.E) row[pid[i]] = pw[i] * (pd[i] - wd);
+      __syncwarp();
     }
-    wd = group_sum<LP>(wd);
-    if (on && a.dw)
-      for (int k = lane % LP; k < a.K; k += LP) {
-        const int id = __ldg(a.topk + t * a.K + k);
-        if (id >= 0 && id < a.E)
-          row[id] = __ldg(a.w + t * a.K + k) * (__ldg(a.dw + t * a.K + k) - wd);
-      }
-    __syncwarp();
+    fetch(s + stride);
 #pragma unroll
     for (int i = 0; i < V; i++) g[i] = row[col + i];
-    if (a.coef) {
-      float m = z[0];
+    float slope[V];  // d log(score) / d logit
 #pragma unroll
-      for (int i = 1; i < V; i++) m = fmaxf(m, z[i]);
+    for (int i = 0; i < V; i++) slope[i] = 1.0f;
+    if (a.coef || a.sigmoid) {
+      float m = 0.0f;
+      if (!a.sigmoid) {
+        m = z[0];
 #pragma unroll
-      for (int o = LP / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        for (int i = 1; i < V; i++) m = fmaxf(m, z[i]);
+#pragma unroll
+        for (int o = LP / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      }
       float p[V], Z = 0.0f, pc = 0.0f;
 #pragma unroll
       for (int i = 0; i < V; i++) {
-        p[i] = col + i < a.E ? score(z[i], m, a.sigmoid) : 0.0f;
+        if (a.sigmoid) {
+          // both sigmoid(z) and sigmoid(-z) from one exponential
+          const float e = exp_fast(-fabsf(z[i])), q = inverse(1.0f + e);
+          p[i] = z[i] < 0.0f ? e * q : q;
+          slope[i] = z[i] < 0.0f ? q : e * q;
+        } else {
+          p[i] = score(z[i], m, false);
+        }
+        // past the row's end z is -inf and p is 0
         Z += p[i];
         pc += p[i] * cf[i];
       }
@@ -604,23 +675,14 @@ __global__ void __launch_bounds__(kWarps * 32) route_backward_kernel(RouteBwdArg
       pc *= inv;
       const float f = dl * inv;
 #pragma unroll
-      for (int i = 0; i < V; i++) g[i] += f * p[i] * (cf[i] - pc);
-    }
-    if (a.sigmoid) {
-#pragma unroll
-      for (int i = 0; i < V; i++) g[i] *= one_minus_sigmoid(z[i]);
-    }
-    if (!on) {
-#pragma unroll
-      for (int i = 0; i < V; i++) g[i] = 0.0f;
+      for (int i = 0; i < V; i++) g[i] = on ? (g[i] + f * p[i] * (cf[i] - pc)) * slope[i] : 0.0f;
     }
     if (s < a.S) store_row<V>((T *)a.dz + t * a.E, col, a.E, vec, g);
     __syncwarp();
-    if (on && a.dw)
-      for (int k = lane % LP; k < a.K; k += LP) {
-        const int id = __ldg(a.topk + t * a.K + k);
-        if (id >= 0 && id < a.E) row[id] = 0.0f;
-      }
+    if (a.dw) {
+#pragma unroll
+      for (int i = 0; i < V; i++) row[col + i] = 0.0f;
+    }
     __syncwarp();
   }
 }
@@ -754,7 +816,7 @@ cudaError_t launch_backward(const RouteBwdArgs &a, int sms, cudaStream_t st) {
   const Form f = form_of(a.E);
   const bool vec = whole_vectors(a.E, sizeof(T) == 2);
   const int per = kWarps * tokens_per_warp(f);
-  const int64_t need = ((int64_t)a.S + per - 1) / per, cap = ((int64_t)sms * 8 + a.R - 1) / a.R;
+  const int64_t need = ((int64_t)a.S + per - 1) / per, cap = ((int64_t)sms * 3 + a.R - 1) / a.R;
   const dim3 grid((unsigned)(need < cap ? need : cap), a.R), block(kWarps * 32);
   switch (f) {
     case kThread8: return launch_pdl(route_backward_kernel<T, 1, 8>, grid, block, 0, st, false, a, vec);
@@ -797,7 +859,7 @@ int launch_route(moonep_ctx *ctx, const void *logits, int bf16, int scoring, flo
   a.part_p = loss ? (float *)(ctx->d_route + half) : nullptr;
   a.tpe = !loss && f.parts == 1 ? tpe : nullptr;
   f.part_c = a.part_c;
-  f.part_p = a.part_p;
+  f.part_p = a.part_p;  // the route kernel's sums; global scope reuses their first rows
   f.tpe = tpe;
   f.coef = coef;
   f.loss = loss;
@@ -806,7 +868,7 @@ int launch_route(moonep_ctx *ctx, const void *logits, int bf16, int scoring, flo
   for (int r = 0; r < c.R; r++) a.ntok[r] = f.ntok[r] = num_tokens ? num_tokens[r] : c.S;
   cudaError_t e = bf16 ? launch_forward<__nv_bfloat16>(a, bpr, st) : launch_forward<float>(a, bpr, st);
   if (e == cudaSuccess && !a.tpe)
-    e = launch_pdl(route_finish_kernel, dim3(1), dim3(1024), 0, st, false, f);
+    e = launch_pdl(route_finish_kernel, dim3(kFinishBlocks), dim3(256), 0, st, false, f);
   return cuda_status(e);
 }
 
