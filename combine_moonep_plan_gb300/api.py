@@ -139,13 +139,45 @@ class CommPlan:
 class Route:
     """What Buffer.route returns and Buffer.route_backward reads: topk
     [R, S, K] int32, weights [R, S, K] fp32, tokens_per_expert [R, E] int32,
-    and with a balance loss loss [1] fp32 and coef [R, E] fp32."""
+    and with a balance loss loss [1] fp32 and coef [R, E] fp32 (None without)."""
 
-    __slots__ = ("topk", "weights", "tokens_per_expert", "loss", "coef", "scoring", "num_tokens")
+    __slots__ = ("_tensors", "scoring", "num_tokens", "_ptrs", "_dims")
 
-    def __init__(self, topk, weights, tokens_per_expert, loss, coef, scoring, num_tokens):
-        self.topk, self.weights, self.tokens_per_expert = topk, weights, tokens_per_expert
-        self.loss, self.coef, self.scoring, self.num_tokens = loss, coef, scoring, num_tokens
+    def __init__(self, tensors, scoring, num_tokens, ptrs, dims):
+        self._tensors, self.scoring, self.num_tokens = tensors, scoring, num_tokens
+        self._ptrs, self._dims = ptrs, dims
+
+    topk = property(lambda self: self._tensors[0])
+    weights = property(lambda self: self._tensors[1])
+    tokens_per_expert = property(lambda self: self._tensors[2])
+    loss = property(lambda self: self._tensors[3])
+    coef = property(lambda self: self._tensors[4])
+
+
+class GatedCheckpoint:
+    """gated_act's 8-bit checkpoint, one allocation: as a sequence, the E4M3
+    codes of gate and up [rows, F] and their E8M0 scales [rows, F/32], uint8."""
+
+    __slots__ = ("_store", "_shape", "_ptrs")
+
+    def __init__(self, rows: int, F: int, device):
+        # codes first: both start on 16 bytes, since rows of codes are whole
+        # blocks of 32
+        self._store = torch.empty(2 * rows * (F + F // 32), dtype=torch.uint8, device=device)
+        self._shape = (rows, F)
+        p, n = self._store.data_ptr(), rows * F
+        self._ptrs = (p, p + n, p + 2 * n, p + 2 * n + n // 32)
+
+    def __len__(self):
+        return 4
+
+    def __getitem__(self, i):
+        rows, F = self._shape
+        n = rows * F
+        at = (0, n, 2 * n, 2 * n + n // 32, 2 * n + 2 * (n // 32))
+        views = tuple(self._store[at[k]:at[k + 1]].view(rows, F if k < 2 else F // 32)
+                      for k in range(4))
+        return views[i]
 
 
 class Buffer:
@@ -175,6 +207,7 @@ class Buffer:
                                     ctypes.byref(h)), "moonep_ctx_create")
         self._ctx = h
         self._counts = ctypes.c_int32 * R
+        self._dims = (R, S, K, E)
         self._plan_flags = _lib.PLAN_DUP_RECORDS if dup_records else 0
         self._views = zero_copy_views
 
@@ -413,26 +446,28 @@ class Buffer:
         all ranks' tokens ("global").  num_tokens: valid tokens of each rank
         (host values); later rows get id 0 and weight 0 and stay out of the
         loss."""
-        R, S, K, E = self.R, self.S, self.K, self.E
-        if scoring not in _lib.SCORINGS:
-            raise ValueError(f"scoring: expected one of {sorted(_lib.SCORINGS)}")
-        if scope not in _lib.SCOPES:
-            raise ValueError(f"scope: expected one of {sorted(_lib.SCOPES)}")
+        R, S, K, E = dims = self._dims
+        try:
+            score, group = _lib.SCORINGS[scoring], _lib.SCOPES[scope]
+        except KeyError as e:
+            raise ValueError(f"scoring or scope: {e} is not one of {sorted(_lib.SCORINGS)} or "
+                             f"{sorted(_lib.SCOPES)}") from None
         lp = _check_tensor(logits, "logits", _one_of(logits, "logits", _FLOATS), (R, S, E))
-        nt = self._token_counts(num_tokens)
-        dev = logits.device
-        topk = torch.empty((R, S, K), dtype=torch.int32, device=dev)
-        weights = torch.empty((R, S, K), dtype=torch.float32, device=dev)
-        tpe = torch.empty((R, E), dtype=torch.int32, device=dev)
-        loss = coef = None
+        nt = None if num_tokens is None else self._token_counts(num_tokens)
+        dev, empty = logits.device, torch.empty
+        topk = empty((R, S, K), dtype=torch.int32, device=dev)
+        weights = empty((R, S, K), dtype=torch.float32, device=dev)
+        tpe = empty((R, E), dtype=torch.int32, device=dev)
+        loss = coef = loss_p = coef_p = None
         if balance:
-            loss = torch.empty((1,), dtype=torch.float32, device=dev)
-            coef = torch.empty((R, E), dtype=torch.float32, device=dev)
+            loss = empty((1,), dtype=torch.float32, device=dev)
+            coef = empty((R, E), dtype=torch.float32, device=dev)
+            loss_p, coef_p = loss.data_ptr(), coef.data_ptr()
+        topk_p, w_p = topk.data_ptr(), weights.data_ptr()
         check(_lib.load().moonep_route(
-            self._ctx, lp, logits.dtype == torch.bfloat16, _lib.SCORINGS[scoring], balance,
-            _lib.SCOPES[scope], nt, topk.data_ptr(), weights.data_ptr(), tpe.data_ptr(),
-            _ptr(coef), _ptr(loss), _stream()), "moonep_route")
-        return Route(topk, weights, tpe, loss, coef, scoring, nt)
+            self._ctx, lp, logits.dtype is torch.bfloat16, score, balance, group, nt, topk_p, w_p,
+            tpe.data_ptr(), coef_p, loss_p, _stream()), "moonep_route")
+        return Route((topk, weights, tpe, loss, coef), scoring, nt, (topk_p, w_p, coef_p), dims)
 
     def route_backward(self, route: Route, logits: torch.Tensor,
                        d_weights: torch.Tensor | None = None,
@@ -441,22 +476,24 @@ class Buffer:
         """Gradient of the logits that `route` was made from: d_weights
         [R, S, K] fp32 (None: zero) and, when the route has a balance loss,
         d_loss [1] fp32 (None: 1).  Returns d_logits in the logits' type."""
-        R, S, K, E = self.R, self.S, self.K, self.E
+        R, S, K, E = self._dims
+        if route._dims != self._dims:
+            raise ValueError(f"route: made for (R, S, K, E) = {route._dims}, not {self._dims}")
         lp = _check_tensor(logits, "logits", _one_of(logits, "logits", _FLOATS), (R, S, E))
         dw = dl = None
         if d_weights is not None:
             dw = _check_tensor(d_weights, "d_weights", torch.float32, (R, S, K))
         if d_loss is not None:
             dl = _check_tensor(d_loss, "d_loss", torch.float32, (1,))
-        tk = _check_tensor(route.topk, "topk", torch.int32, (R, S, K))
-        wp = _check_tensor(route.weights, "weights", torch.float32, (R, S, K))
         if out is None:
             out = torch.empty_like(logits)
-        op = _check_tensor(out, "d_logits", logits.dtype, (R, S, E))
+            op = out.data_ptr()
+        else:
+            op = _check_tensor(out, "d_logits", logits.dtype, (R, S, E))
+        topk_p, w_p, coef_p = route._ptrs
         check(_lib.load().moonep_route_backward(
-            self._ctx, lp, logits.dtype == torch.bfloat16, _lib.SCORINGS[route.scoring],
-            route.num_tokens, tk, wp, dw, _ptr(route.coef), dl, op, _stream()),
-            "moonep_route_backward")
+            self._ctx, lp, logits.dtype is torch.bfloat16, _lib.SCORINGS[route.scoring],
+            route.num_tokens, topk_p, w_p, dw, coef_p, dl, op, _stream()), "moonep_route_backward")
         return out
 
     # ----------------------------------------------------------- experts
@@ -480,11 +517,14 @@ class Buffer:
             if tuple(lead) != (self.R * self.NvS,):
                 raise ValueError(f"x: expected {self.R * self.NvS} rows with cu_seqlens")
         if out is None:
-            out = (torch.empty((*lead, cols // 2), dtype=torch.uint8, device=x.device),
-                   torch.empty((*lead, cols // 32), dtype=torch.uint8, device=x.device))
-        packed, scales = out
-        pp = _check_tensor(packed, "packed", torch.uint8, (*lead, cols // 2))
-        sp = _check_tensor(scales, "scales", torch.uint8, (*lead, cols // 32))
+            dev = x.device
+            packed = torch.empty((*lead, cols // 2), dtype=torch.uint8, device=dev)
+            scales = torch.empty((*lead, cols // 32), dtype=torch.uint8, device=dev)
+            pp, sp = packed.data_ptr(), scales.data_ptr()
+        else:
+            packed, scales = out
+            pp = _check_tensor(packed, "packed", torch.uint8, (*lead, cols // 2))
+            sp = _check_tensor(scales, "scales", torch.uint8, (*lead, cols // 32))
         rows = x.numel() // cols if cols else 0
         check(_lib.load().moonep_quantize_mx(self._ctx, xp, x.dtype == torch.float32, rows, cols,
                                               cu, pp, sp, _stream()), "moonep_quantize_mx")
@@ -502,7 +542,9 @@ class Buffer:
         sp = _check_tensor(scales, "scales", torch.uint8, (*lead, cols // 32))
         if out is None:
             out = torch.empty((*lead, cols), dtype=dtype, device=packed.device)
-        op = _check_tensor(out, "out", dtype, (*lead, cols))
+            op = out.data_ptr()
+        else:
+            op = _check_tensor(out, "out", dtype, (*lead, cols))
         rows = packed.numel() * 2 // cols if cols else 0
         check(_lib.load().moonep_dequantize_mx(self._ctx, pp, sp, dtype == torch.float32, rows,
                                                 cols, op, _stream()), "moonep_dequantize_mx")
@@ -556,33 +598,38 @@ class Buffer:
             wp = _check_tensor(route_weights_nvs, "route_weights_nvs", torch.float32, (n,))
         if out is None:
             out = torch.empty_like(gate)
-        op = _check_tensor(out, "act", torch.bfloat16, (n, F))
-        ckpt = None
-        if checkpoint:
-            ckpt = tuple(torch.empty((n, c), dtype=torch.uint8, device=gate.device)
-                         for c in (F, F, F // 32, F // 32))
+            op = out.data_ptr()
+        else:
+            op = _check_tensor(out, "act", torch.bfloat16, (n, F))
+        ckpt = GatedCheckpoint(n, F, gate.device) if checkpoint else None
         check(_lib.load().moonep_gated_act(
             self._ctx, self._segments(cu_seqlens), gp, up_p, wp, F, op,
-            *((t.data_ptr() for t in ckpt) if checkpoint else (None,) * 4), _stream()),
-            "moonep_gated_act")
+            *(ckpt._ptrs if checkpoint else (None,) * 4), _stream()), "moonep_gated_act")
         return out, ckpt
 
-    def gated_act_backward(self, checkpoint: tuple, d_act: torch.Tensor,
+    def gated_act_backward(self, checkpoint, d_act: torch.Tensor,
                            cu_seqlens: torch.Tensor,
                            route_weights_nvs: torch.Tensor | None = None,
                            out: tuple | None = None):
-        """Gradients of gated_act from its checkpoint and d_act [R*NvS, F]
-        bf16: (d_gate, d_up) [R*NvS, F] bf16 and, with route weights, their
-        gradient [R*NvS] fp32 (None without), which combine gathers back to
-        [R, S, K].  out: the three tensors to write."""
+        """Gradients of gated_act from its checkpoint (a GatedCheckpoint, or its
+        four tensors) and d_act [R*NvS, F] bf16: (d_gate, d_up) [R*NvS, F] bf16
+        and, with route weights, their gradient [R*NvS] fp32 (None without),
+        which combine gathers back to [R, S, K].  out: the three tensors to
+        write."""
         n, F = self.R * self.NvS, d_act.shape[-1]
         dp = _check_tensor(d_act, "d_act", torch.bfloat16, (n, F))
         if F % 32:
             raise ValueError("d_act: the last dimension must be a multiple of 32")
-        if len(checkpoint) != 4:
-            raise ValueError("checkpoint: expected gated_act's four tensors")
-        cp = [_check_tensor(t, f"checkpoint[{i}]", torch.uint8, (n, F if i < 2 else F // 32))
-              for i, t in enumerate(checkpoint)]
+        if isinstance(checkpoint, GatedCheckpoint):
+            if checkpoint._shape != (n, F):
+                raise ValueError(f"checkpoint: made for rows and columns {checkpoint._shape}, "
+                                 f"not {(n, F)}")
+            cp = checkpoint._ptrs
+        else:
+            if len(checkpoint) != 4:
+                raise ValueError("checkpoint: expected gated_act's four tensors")
+            cp = [_check_tensor(t, f"checkpoint[{i}]", torch.uint8, (n, F if i < 2 else F // 32))
+                  for i, t in enumerate(checkpoint)]
         wp = dwp = None
         if out is None:
             out = (torch.empty_like(d_act), torch.empty_like(d_act),
