@@ -3,8 +3,7 @@
 //
 // Four lanes hold a block, eight values each: one or two 16-byte loads, the
 // block's largest magnitude by two exchanges, one 4-byte store of eight
-// codes, and one lane's scale byte.  Each thread has four such loads in
-// flight.
+// codes, and one lane's scale byte.
 #include "copy_common.cuh"
 #include "moonep_internal.cuh"
 #include "mx_common.cuh"
@@ -14,7 +13,11 @@ namespace {
 
 constexpr int kThreads = 256;
 
-constexpr int kBatch = 4;  // units (eight values) per thread, loads in flight together
+// Units (eight values) per thread whose loads are in flight together.  65536
+// x 7168 bf16 took 270, 198 and 189 us with 2, 4 and 8 to quantise, and 173 us
+// with 4 to read back (8: 184); small tensors want blocks more than batches
+// (1024 x 4096: 3.4 us with 4, 3.8 with 8).
+constexpr int kBatch = 4, kLongBatch = 8;
 
 struct MxArgs {
   const void *x;        // [rows, cols] bf16 or fp32
@@ -43,7 +46,7 @@ __device__ __forceinline__ void values8(const float *, const uint4 v[2], float f
 
 // blockIdx.y: rank (0 without cu).  A rank's used rows are one span of memory
 // from its window's start, walked without regard to rows.
-template <typename T>
+template <typename T, int BATCH>
 __global__ void __launch_bounds__(kThreads) quantize_kernel(MxArgs a) {
   pdl_wait();
   pdl_launch_dependents();
@@ -55,14 +58,14 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(MxArgs a) {
   uint8_t *scales = a.scales + first / 4;
   // the four lanes of a block are inside or outside together (n is a multiple
   // of 4); lanes outside take part in the exchanges
-  for (int64_t u0 = (int64_t)blockIdx.x * (kThreads * kBatch) + threadIdx.x;
-       u0 - threadIdx.x < n; u0 += (int64_t)gridDim.x * (kThreads * kBatch)) {
-    uint4 v[kBatch][sizeof(T) / 2] = {};
+  for (int64_t u0 = (int64_t)blockIdx.x * (kThreads * BATCH) + threadIdx.x;
+       u0 - threadIdx.x < n; u0 += (int64_t)gridDim.x * (kThreads * BATCH)) {
+    uint4 v[BATCH][sizeof(T) / 2] = {};
 #pragma unroll
-    for (int b = 0; b < kBatch; b++)
+    for (int b = 0; b < BATCH; b++)
       if (u0 + b * kThreads < n) load8(x, u0 + b * kThreads, v[b]);
 #pragma unroll
-    for (int b = 0; b < kBatch; b++) {
+    for (int b = 0; b < BATCH; b++) {
       const int64_t u = u0 + b * kThreads;
       float f[8];
       values8(x, v[b], f);
@@ -113,11 +116,12 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(const uint8_t *pac
   }
 }
 
-// Blocks for so many units in each of `spans` equal spans.
-dim3 grid_for(const moonep_ctx *ctx, int64_t units, int spans) {
-  const int64_t need = (units + kThreads * kBatch - 1) / (kThreads * kBatch);
-  const int64_t cap = ((int64_t)ctx->sms * 8 + spans - 1) / spans;
-  return dim3((unsigned)(need < cap ? need : cap), spans);
+// One block for every `batch` units per thread, in each of `spans` equal
+// spans (a capped grid that walks its span was 3 to 18 % slower); the loops
+// serve tensors whose blocks would not fit in a grid.
+dim3 grid_for(int64_t units, int spans, int batch) {
+  const int64_t need = (units + (int64_t)kThreads * batch - 1) / ((int64_t)kThreads * batch);
+  return dim3((unsigned)(need < INT32_MAX ? need : INT32_MAX), spans);
 }
 
 }  // namespace
@@ -126,15 +130,18 @@ int launch_quantize_mx(moonep_ctx *ctx, const void *x, int fp32, int64_t rows, i
                        const int32_t *cu, uint8_t *packed, uint8_t *scales, cudaStream_t st) {
   const int spans = cu ? ctx->cfg.R : 1;
   MxArgs a{x, packed, scales, cu, rows / spans * (cols / 8), (int)(cols / 8), ctx->EB, ctx->NvS};
-  auto kern = fp32 ? quantize_kernel<float> : quantize_kernel<__nv_bfloat16>;
-  return cuda_status(
-      launch_pdl(kern, grid_for(ctx, a.units, spans), dim3(kThreads), 0, st, false, a));
+  const bool lng = a.units * spans >= (int64_t)ctx->sms * 8 * kThreads * kLongBatch;
+  auto kern = lng ? (fp32 ? quantize_kernel<float, kLongBatch>
+                          : quantize_kernel<__nv_bfloat16, kLongBatch>)
+                  : (fp32 ? quantize_kernel<float, kBatch> : quantize_kernel<__nv_bfloat16, kBatch>);
+  return cuda_status(launch_pdl(kern, grid_for(a.units, spans, lng ? kLongBatch : kBatch),
+                                dim3(kThreads), 0, st, false, a));
 }
 
 int launch_dequantize_mx(moonep_ctx *ctx, const uint8_t *packed, const uint8_t *scales, int fp32,
                          int64_t rows, int64_t cols, void *y, cudaStream_t st) {
   const int64_t units = rows * (cols / 8);
-  const dim3 grid = grid_for(ctx, units, 1);
+  const dim3 grid = grid_for(units, 1, kBatch);
   if (fp32)
     return cuda_status(launch_pdl(dequantize_kernel<float>, grid, dim3(kThreads), 0, st, false,
                                   packed, scales, (float *)y, units));
