@@ -33,7 +33,23 @@
 // shared-memory stages has its own 24 columns of scales, so a stage's scales
 // are only overwritten once its products are done (the stage's barrier).
 // Every wait has a limit of one second, after which the kernel latches
-// MOONEP_ERR_TIMEOUT, drains and returns.
+// MOONEP_ERR_TIMEOUT, drains and returns; every warp reaches the cluster
+// barrier before the CTAs leave, on every path.
+//
+// A wait by parity must not come a whole use of its barrier early.  The sets of
+// scale warps alternate, but a warp's waits are at most four stages apart, and
+// a stage's barrier is used again after five: the products that the earlier
+// wait saw complete include those of the use before.
+//
+// Measured (the kernel alone): 128 experts with 9536 rows, N = 4096, Kd =
+// 1536: 107 us, 6.43 TB/s, 0.95 of the copy rate, bound by the weights' bytes.
+// 256 experts with 283520 rows, N = 2048, Kd = 7168: 1400 us, 5.94 PFLOP/s,
+// the tensor pipe busy 65 % of the time (352 cycles a stage for 176 rows, 530
+// needed).  Neither more stages, longer stages, scales written to TMEM by the
+// warps, a thread of its own for the scale copies, L2 prefetch nor clusters of
+// two pairs sharing the rows moved that (1390 to 1630 us); without its loads
+// the kernel takes 1228 us, without scales too 1059, so the rest is the ring
+// of barriers between the warps and what the loads add to it.
 #include <cuda.h>
 
 #include "moonep_internal.cuh"
@@ -146,6 +162,10 @@ __device__ __forceinline__ bool elect() {
   asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}" : "=r"(p));
   return p != 0;
 }
+// Without a cluster-scope release: that waits for every load in flight, 1 us
+// per stage.  What the arrivals announce is read by the tensor cores alone,
+// scales (behind a proxy fence) and accumulator columns (behind a tcgen05
+// fence), not by threads of the other CTA.
 __device__ __forceinline__ void arrive_leader(const void *bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(
                    in_leader(smem_addr(bar)))
@@ -328,11 +348,21 @@ __device__ __forceinline__ uint32_t word(const uint4 &v, int i) {
   return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
 
-__device__ __forceinline__ void store_pair(float *p, float lo, float hi) {
-  *(float2 *)p = make_float2(lo, hi);
+// Two rows of one output column (this lane's) and the neighbouring lane's same
+// rows become both columns of one row, the even lane's first row or the odd
+// lane's second.
+__device__ __forceinline__ void store_pair(float *p, uint32_t lo, uint32_t hi, bool odd, uint32_t) {
+  const uint32_t mine = odd ? hi : lo, got = __shfl_xor_sync(0xffffffffu, odd ? lo : hi, 1);
+  if (p) *(uint2 *)p = odd ? make_uint2(got, mine) : make_uint2(mine, got);
 }
-__device__ __forceinline__ void store_pair(__nv_bfloat16 *p, float lo, float hi) {
-  *(__nv_bfloat162 *)p = __floats2bfloat162_rn(lo, hi);
+__device__ __forceinline__ void store_pair(__nv_bfloat16 *p, uint32_t lo, uint32_t hi, bool,
+                                           uint32_t pick) {
+  uint32_t w;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;"
+      : "=r"(w)
+      : "f"(__uint_as_float(hi)), "f"(__uint_as_float(lo)));
+  const uint32_t got = __shfl_xor_sync(0xffffffffu, w, 1);
+  if (p) *(uint32_t *)p = __byte_perm(w, got, pick);
 }
 
 // The i-th tile of this CTA, for a whole warp that reads them in order.
@@ -346,15 +376,28 @@ __device__ __forceinline__ bool next_tile(Shared *sh, int i, int32_t *status, in
   return true;
 }
 
-// 16 accumulator columns of this warp's 32 lanes.
-__device__ __forceinline__ void tmem_load(uint32_t *v, uint32_t addr) {
+// 32 accumulator columns of this warp's 32 lanes; valid after tmem_wait.
+__device__ __forceinline__ void tmem_load(uint32_t v[32], uint32_t addr) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, "
-      "%10, %11, %12, %13, %14, %15}, [%16];"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
+      "%30, %31}, [%32];"
       : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
         "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
-        "=r"(v[14]), "=r"(v[15])
+        "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]),
+        "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]),
+        "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
       : "r"(addr));
+}
+// All loads so far; the registers pass through so that no use moves ahead.
+__device__ __forceinline__ void tmem_wait(uint32_t v[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]),
+                 "+r"(v[6]), "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]),
+                 "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]), "+r"(v[16]), "+r"(v[17]),
+                 "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]),
+                 "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]),
+                 "+r"(v[30]), "+r"(v[31])::"memory");
 }
 
 template <typename T>
@@ -588,6 +631,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // epilogue: lane = output n, accumulator columns = rows
     const int q = warp & 3, group = (warp >> 2) & 1;
     const bool odd = lane & 1;
+    // bytes of a row's two columns in (own two rows, neighbour's two rows)
+    const uint32_t pick = odd ? 0x3276u : 0x5410u;
     for (int it = 0; it < mine; it++) {
       int4 tile;
       if (!next_tile(sh, it, a.status, &tile)) break;
@@ -597,22 +642,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int n = tile.y + (int)rank * 128 + q * 32 + (lane & ~1);
       const int rows = n < a.N ? tile.w - odd : 0;
       T *out = (T *)a.out + ((int64_t)tile.z + odd) * a.N + n;
-      for (int c = group * 32; c < tile.w; c += 64) {
-        // the last 16 columns of a piece may be another accumulator's: read,
-        // not stored
-        uint32_t v[32];
-        tmem_load(v, d + c);
-        tmem_load(v + 16, d + c + 16);
-        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-        // neighbouring lanes swap so that each holds both columns of one row
+      // the last 16 columns of a piece may be another accumulator's: read, not
+      // stored
+      auto store = [&](const uint32_t v[32], int c) {
+        T *p = out + (int64_t)c * a.N;
 #pragma unroll
         for (int i = 0; i < 32; i += 2) {
-          const float mine = __uint_as_float(odd ? v[i + 1] : v[i]);
-          const float give = __uint_as_float(odd ? v[i] : v[i + 1]);
-          const float got = __shfl_xor_sync(0xffffffffu, give, 1);
-          if (c + i < rows)
-            store_pair(out + (int64_t)(c + i) * a.N, odd ? got : mine, odd ? mine : got);
+          store_pair(c + i < rows ? p : (T *)nullptr, v[i], v[i + 1], odd, pick);
+          p += 2 * a.N;
         }
+      };
+      for (int c = group * 32; c < tile.w; c += 64) {
+        uint32_t v[32];
+        tmem_load(v, d + c);
+        tmem_wait(v);
+        store(v, c);
       }
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
       __syncwarp();
