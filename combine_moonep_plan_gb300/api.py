@@ -150,8 +150,17 @@ class Route:
     topk = property(lambda self: self._tensors[0])
     weights = property(lambda self: self._tensors[1])
     tokens_per_expert = property(lambda self: self._tensors[2])
-    loss = property(lambda self: self._tensors[3])
-    coef = property(lambda self: self._tensors[4])
+
+    # the coefficients and, after them, the loss are one allocation
+    @property
+    def loss(self):
+        store = self._tensors[3]
+        return None if store is None else store.as_strided((1,), (1,), store.numel() - 1)
+
+    @property
+    def coef(self):
+        store, (R, _, _, E) = self._tensors[3], self._dims
+        return None if store is None else store.as_strided((R, E), (E, 1))
 
 
 class GatedCheckpoint:
@@ -458,16 +467,16 @@ class Buffer:
         topk = empty((R, S, K), dtype=torch.int32, device=dev)
         weights = empty((R, S, K), dtype=torch.float32, device=dev)
         tpe = empty((R, E), dtype=torch.int32, device=dev)
-        loss = coef = loss_p = coef_p = None
+        store = loss_p = coef_p = None
         if balance:
-            loss = empty((1,), dtype=torch.float32, device=dev)
-            coef = empty((R, E), dtype=torch.float32, device=dev)
-            loss_p, coef_p = loss.data_ptr(), coef.data_ptr()
+            store = empty((R * E + 1,), dtype=torch.float32, device=dev)
+            coef_p = store.data_ptr()
+            loss_p = coef_p + 4 * R * E
         topk_p, w_p = topk.data_ptr(), weights.data_ptr()
         check(_lib.load().moonep_route(
             self._ctx, lp, logits.dtype is torch.bfloat16, score, balance, group, nt, topk_p, w_p,
             tpe.data_ptr(), coef_p, loss_p, _stream()), "moonep_route")
-        return Route((topk, weights, tpe, loss, coef), scoring, nt, (topk_p, w_p, coef_p), dims)
+        return Route((topk, weights, tpe, store), scoring, nt, (topk_p, w_p, coef_p), dims)
 
     def route_backward(self, route: Route, logits: torch.Tensor,
                        d_weights: torch.Tensor | None = None,

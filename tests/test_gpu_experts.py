@@ -190,6 +190,30 @@ def test_product(R, S, K, E, B, tp, zipf, N, Kd, dtype):
     assert buf.get_status() == 0
 
 
+@pytest.mark.parametrize("num_sms,R,S,K,E,B,tp,N,Kd", [
+    (2, 8, 128, 8, 128, 16, 16, 512, 512),      # one pair of SMs: hundreds of tiles in a row
+    (2, 2, 300, 2, 4, 2, 1, 4096, 96),          # one stage per tile
+    (5, 8, 64, 4, 64, 8, 8, 1024, 1184),        # odd count of stages, scales not in vectors
+    (6, 1, 40, 4, 1100, 7, 1, 16, 64),          # more groups than the tile table has entries
+    (None, 8, 64, 8, 128, 16, 1, 8192, 64),     # more tiles than two batches of the schedule
+])
+def test_product_long_tile_sequences(num_sms, R, S, K, E, B, tp, N, Kd):
+    from combine_moonep_plan_gb300 import Buffer
+    sh = wl.Shape("t", R=R, E=E, K=K, S=S, H=32, Hp=32, B=B, tp=tp, weights="softmax")
+    topk, _ = wl.routing(sh, "zipf", zipf_s=0.8, seed=N)
+    buf = Buffer(S=S, H=32, K=K, E=E, num_ep_ranks=R, B=B, token_padding=tp, num_sms=num_sms,
+                 zero_copy_views=False)
+    cu = buf.plan(torch.from_numpy(topk).cuda()).cu_seqlens.clone()
+    n = R * buf.NvS
+    rows = buf.quantize_mx(torch.randn(n, Kd, device="cuda"))
+    weight = _weights(E + R * B, N, Kd, 4)
+    out = torch.full((n, N), 5.0, device="cuda")
+    for _ in range(3):                           # back to back: launches overlap their starts
+        buf.expert_product(rows, weight, cu, out=out)
+    _check_product(out, rows, weight, cu.cpu().numpy(), E, R, B, buf.NvS, 5.0)
+    assert buf.get_status() == 0
+
+
 def test_product_of_spaced_rows():
     """Rows that lie apart: codes and scales of a row in one record, the form
     a plan can dispatch in one copy."""
