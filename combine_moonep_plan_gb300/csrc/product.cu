@@ -642,8 +642,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int n = tile.y + (int)rank * 128 + q * 32 + (lane & ~1);
       const int rows = n < a.N ? tile.w - odd : 0;
       T *out = (T *)a.out + ((int64_t)tile.z + odd) * a.N + n;
-      // the last 16 columns of a piece may be another accumulator's: read, not
-      // stored
+      // columns past the piece's rows hold an earlier piece's: read, not stored
       auto store = [&](const uint32_t v[32], int c) {
         T *p = out + (int64_t)c * a.N;
 #pragma unroll
