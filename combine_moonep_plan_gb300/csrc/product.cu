@@ -42,14 +42,16 @@
 // wait saw complete include those of the use before.
 //
 // Measured (the kernel alone): 128 experts with 9536 rows, N = 4096, Kd =
-// 1536: 107 us, 6.43 TB/s, 0.95 of the copy rate, bound by the weights' bytes.
-// 256 experts with 283520 rows, N = 2048, Kd = 7168: 1400 us, 5.94 PFLOP/s,
-// the tensor pipe busy 65 % of the time (352 cycles a stage for 176 rows, 530
-// needed).  Neither more stages, longer stages, scales written to TMEM by the
-// warps, a thread of its own for the scale copies, L2 prefetch nor clusters of
-// two pairs sharing the rows moved that (1390 to 1630 us); without its loads
-// the kernel takes 1228 us, without scales too 1059, so the rest is the ring
-// of barriers between the warps and what the loads add to it.
+// 1536: 106 us, 6.5 TB/s, 0.96 of the copy rate, bound by the weights' bytes.
+// 256 experts with 283520 rows, N = 2048, Kd = 7168: 1358 us, 6.13 PFLOP/s,
+// the tensor pipe busy 67 % of the time (352 cycles a stage for 176 rows, some
+// 520 needed); after a few runs in a row the power limit adds 3 to 5 %.
+// More stages, longer stages, scales written to TMEM by the warps, a thread of
+// its own for the scale copies, L2 prefetch, and clusters of two pairs sharing
+// the rows took 1320 to 1630 us, and what gained in this shape lost in
+// another.  Without its loads the kernel took 1228 us, without scales too
+// 1059: the rest is the ring of barriers between the warps and what the loads
+// add to it.
 #include <cuda.h>
 
 #include "moonep_internal.cuh"
@@ -151,7 +153,14 @@ __device__ __noinline__ bool wait_long(Shared *sh, uint32_t bar, uint32_t parity
 __device__ __forceinline__ bool wait(Shared *sh, const void *bar, uint32_t parity,
                                      int32_t *status) {
   if (__all_sync(0xffffffffu, try_wait(smem_addr(bar), parity))) return true;
-  return wait_long(sh, smem_addr(bar), parity, status);
+  return __all_sync(0xffffffffu, wait_long(sh, smem_addr(bar), parity, status));
+}
+// A value that every lane holds alike, in a uniform register: what comes from
+// shared memory, a call or mapa is not known to be one, nor is anything that
+// depends on it, and every tensor-core or TMA operand would move first (2.5 to
+// 3 % of the kernel's time).
+__device__ __forceinline__ uint32_t uniform(uint32_t v) {
+  return __reduce_max_sync(0xffffffffu, v);
 }
 // One lane of the warp, the same each time.  The tensor-core and TMA
 // instructions take uniform operands: under this condition, in code that the
@@ -166,9 +175,8 @@ __device__ __forceinline__ bool elect() {
 // per stage.  What the arrivals announce is read by the tensor cores alone,
 // scales (behind a proxy fence) and accumulator columns (behind a tcgen05
 // fence), not by threads of the other CTA.
-__device__ __forceinline__ void arrive_leader(const void *bar) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(
-                   in_leader(smem_addr(bar)))
+__device__ __forceinline__ void arrive_leader(const void *bar, uint32_t to_leader) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(smem_addr(bar) + to_leader)
                : "memory");
 }
 __device__ __forceinline__ void arrive(const void *bar) {
@@ -368,7 +376,8 @@ __device__ __forceinline__ void store_pair(__nv_bfloat16 *p, uint32_t lo, uint32
 // The i-th tile of this CTA, for a whole warp that reads them in order.
 __device__ __forceinline__ bool next_tile(Shared *sh, int i, int32_t *status, int4 *tile) {
   if ((i & 31) == 0 && !wait(sh, &sh->tile_full[(i >> 5) & 1], (i >> 6) & 1, status)) return false;
-  *tile = sh->tile[(i >> 5) & 1][i & 31];
+  const int4 t = sh->tile[(i >> 5) & 1][i & 31];
+  *tile = make_int4(uniform(t.x), uniform(t.y), uniform(t.z), uniform(t.w));
   if ((i & 31) == 31) {
     __syncwarp();
     if ((threadIdx.x & 31) == 0) arrive(&sh->tile_empty[(i >> 5) & 1]);
@@ -409,7 +418,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   Shared *sh = (Shared *)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-  const uint32_t rank = cluster_rank();
+  const uint32_t rank = uniform(cluster_rank());
+  // from a shared address to the same one in the pair's first CTA
+  const uint32_t to_leader = uniform(in_leader(smem_addr(sh)) - smem_addr(sh));
   const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
   if (tid == 0) {
     sh->dead = 0;
@@ -437,19 +448,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
   pdl_wait();
   pdl_launch_dependents();
-  const int tiles = build_table(a, sh);
+  const int tiles = (int)uniform(build_table(a, sh));
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   cluster_sync();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-  const uint32_t tmem = *(volatile uint32_t *)&sh->tmem;
+  const uint32_t tmem = uniform(*(volatile uint32_t *)&sh->tmem);
   const int stages = (a.Kd + kStageK - 1) / kStageK;  // per tile
   const int mine = tiles > first ? (tiles - first + step - 1) / step : 0;  // tiles of this pair
 
   if (warp == 0) {
     uint32_t s = 0, phase = 0, pending = 0;
     bool ok = true;
-    const uint32_t to_leader = in_leader(smem_addr(sh)) - smem_addr(sh);
     for (int i = 0; i < mine && ok; i++) {
       int4 tile;
       if (!(ok = next_tile(sh, i, a.status, &tile))) break;
@@ -549,7 +559,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // the tensor cores read these lines through the async proxy
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (lane == 0) arrive_leader(&sh->full[s]);
+        if (lane == 0) arrive_leader(&sh->full[s], to_leader);
         skip(1);
       }
       return true;
@@ -659,7 +669,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
       __syncwarp();
-      if (lane == 0) arrive_leader(&sh->acc_empty[it & 1]);
+      if (lane == 0) arrive_leader(&sh->acc_empty[it & 1], to_leader);
     }
   } else {
     // 32 tiles at a time, two such batches
