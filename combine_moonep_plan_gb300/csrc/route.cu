@@ -129,13 +129,22 @@ __device__ __forceinline__ void load_row(const __nv_bfloat16 *z, int c, int E, b
     }
     return;
   }
-  if (V < 8 && vec) {
+  if (V % 4 == 0 && vec) {
 #pragma unroll
-    for (int i = 0; i < V; i += 2) {
-      const uint32_t v = c < E ? __ldg((const uint32_t *)(z + c + i)) : 0xff80ff80u;
-      f[i] = __uint_as_float(v << 16);
-      f[i + 1] = __uint_as_float(v & 0xffff0000u);
+    for (int i = 0; i < V; i += 4) {
+      const uint2 v = c + i < E ? __ldg((const uint2 *)(z + c + i))
+                                : make_uint2(0xff80ff80u, 0xff80ff80u);
+      f[i] = __uint_as_float(v.x << 16);
+      f[i + 1] = __uint_as_float(v.x & 0xffff0000u);
+      f[i + 2] = __uint_as_float(v.y << 16);
+      f[i + 3] = __uint_as_float(v.y & 0xffff0000u);
     }
+    return;
+  }
+  if (V == 2 && vec) {
+    const uint32_t v = c < E ? __ldg((const uint32_t *)(z + c)) : 0xff80ff80u;
+    f[0] = __uint_as_float(v << 16);
+    f[V - 1] = __uint_as_float(v & 0xffff0000u);
     return;
   }
 #pragma unroll
@@ -167,11 +176,10 @@ __device__ __forceinline__ void store_row(__nv_bfloat16 *z, int c, int E, bool v
       if (c + i < E) *(uint4 *)(z + c + i) = to_bf16x8(f + i);
     return;
   }
-  if (V < 8 && vec) {
-    if (c < E)
+  if (V % 2 == 0 && vec) {
 #pragma unroll
-      for (int i = 0; i < V; i += 2)
-        *(__nv_bfloat162 *)(z + c + i) = __floats2bfloat162_rn(f[i], f[i + 1]);
+    for (int i = 0; i < V; i += 2)
+      if (c + i < E) *(__nv_bfloat162 *)(z + c + i) = __floats2bfloat162_rn(f[i], f[i + 1]);
     return;
   }
 #pragma unroll
@@ -310,7 +318,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(RouteArgs a, bool ve
     uint32_t key[V];
 #pragma unroll
     for (int i = 0; i < V; i++) key[i] = col + i < a.E ? order_key(z[i]) : 0u;
-    const bool done = LP == 32 && V >= 8 && pick_few<V>(key, col, a.K, lane, few, stage);
+    const bool done = LP == 32 && V >= 4 && pick_few<V>(key, col, a.K, lane, few, stage);
     for (int k = 0; k < a.K && !done; k++) {
       uint32_t best = key[0];
 #pragma unroll
@@ -753,10 +761,10 @@ __global__ void __launch_bounds__(kWarps * 32) route_backward_long_kernel(RouteB
 // How a row of E logits is held: lanes per token and values per lane.  A
 // thread to a token of up to 8 experts, four lanes up to 32, then a warp with
 // 2 to 16 values per lane; longer rows in shared memory.
-enum Form { kThread8, kFour8, kWarp2, kWarp4, kWarp8, kWarp16, kLong };
+enum Form { kThread8, kFour8, kWarp2, kWarp4, kWarp8, kWarp12, kWarp16, kLong };
 Form form_of(int E) {
   return E <= 8 ? kThread8 : E <= 32 ? kFour8 : E <= 64 ? kWarp2 : E <= 128 ? kWarp4
-         : E <= 256 ? kWarp8 : E <= 512 ? kWarp16 : kLong;
+         : E <= 256 ? kWarp8 : E <= 384 ? kWarp12 : E <= 512 ? kWarp16 : kLong;
 }
 int tokens_per_warp(Form f) { return f == kThread8 ? 32 : f == kFour8 ? 8 : 1; }
 
@@ -797,6 +805,7 @@ cudaError_t launch_forward(const RouteArgs &a, int bpr, cudaStream_t st) {
     case kWarp2: return launch_pdl_ex(route_kernel<T, 32, 2>, grid, block, smem, st, false, a.cluster, a, vec);
     case kWarp4: return launch_pdl_ex(route_kernel<T, 32, 4>, grid, block, smem, st, false, a.cluster, a, vec);
     case kWarp8: return launch_pdl_ex(route_kernel<T, 32, 8>, grid, block, smem, st, false, a.cluster, a, vec);
+    case kWarp12: return launch_pdl_ex(route_kernel<T, 32, 12>, grid, block, smem, st, false, a.cluster, a, vec);
     case kWarp16: return launch_pdl_ex(route_kernel<T, 32, 16>, grid, block, smem, st, false, a.cluster, a, vec);
     default: break;
   }
@@ -816,7 +825,8 @@ cudaError_t launch_backward(const RouteBwdArgs &a, int sms, cudaStream_t st) {
   const Form f = form_of(a.E);
   const bool vec = whole_vectors(a.E, sizeof(T) == 2);
   const int per = kWarps * tokens_per_warp(f);
-  const int64_t need = ((int64_t)a.S + per - 1) / per, cap = ((int64_t)sms * 3 + a.R - 1) / a.R;
+  const int per_sm = f == kWarp16 ? 2 : 3;  // what the registers allow
+  const int64_t need = ((int64_t)a.S + per - 1) / per, cap = ((int64_t)sms * per_sm + a.R - 1) / a.R;
   const dim3 grid((unsigned)(need < cap ? need : cap), a.R), block(kWarps * 32);
   switch (f) {
     case kThread8: return launch_pdl(route_backward_kernel<T, 1, 8>, grid, block, 0, st, false, a, vec);
@@ -824,6 +834,7 @@ cudaError_t launch_backward(const RouteBwdArgs &a, int sms, cudaStream_t st) {
     case kWarp2: return launch_pdl(route_backward_kernel<T, 32, 2>, grid, block, 0, st, false, a, vec);
     case kWarp4: return launch_pdl(route_backward_kernel<T, 32, 4>, grid, block, 0, st, false, a, vec);
     case kWarp8: return launch_pdl(route_backward_kernel<T, 32, 8>, grid, block, 0, st, false, a, vec);
+    case kWarp12: return launch_pdl(route_backward_kernel<T, 32, 12>, grid, block, 0, st, false, a, vec);
     case kWarp16: return launch_pdl(route_backward_kernel<T, 32, 16>, grid, block, 0, st, false, a, vec);
     default: break;
   }
