@@ -34,6 +34,7 @@
  *     context's device status word and read with moonep_get_status; outputs of
  *     the failing call and of calls that use its plan are then unspecified but
  *     every kernel stays inside the buffers it was given.
+ *   - Outputs do not overlap inputs, except where a call says "in place".
  *   - The caller owns every tensor argument.  The library owns the context's
  *     scratch and status word, the plan's arrays and the optional zero-copy
  *     buffers behind moonep_hidden_view / moonep_weight_view.
@@ -379,7 +380,9 @@ int moonep_reduce_redundant_grad(moonep_ctx *ctx, const moonep_comm_plan *plan,
  *           p_e = s_e / sum s
  *   topk [R, S, K]  the K largest logits, largest first, equal ones by lowest
  *           index (a NaN logit ranks first)
- *   w_sk [R, S, K]  p of the picks over their sum (0 when every score is 0)
+ *   w_sk [R, S, K]  p of the picks over their sum (0 when every score is 0;
+ *           a score below 2^-126, a sigmoid of less than about -87, counts
+ *           as 0)
  * Rows past num_tokens get id 0 and weight 0, as moonep_prepare leaves them.
  *   tokens_per_expert [R, E]  counts of the written ids (moonep_plan's)
  * and, when loss is given, the balance loss over the valid tokens' picks
@@ -446,7 +449,8 @@ int moonep_dequantize_mx(moonep_ctx *ctx, const uint8_t *packed,
  *   a_scales     R*NvS rows of Kd/32 bytes, scale_row_bytes apart
  *   w, w_scales  dense [E + R*B, N, Kd/2] (16-byte aligned), [E + R*B, N, Kd/32]
  *   out          [R*NvS, N], 16-byte aligned; other rows are not written
- * N % 8 == 0, Kd % 32 == 0. */
+ * N % 8 == 0, Kd % 32 == 0.  Runs on pairs of SMs: at least one pair, however
+ * few SMs the context may use. */
 int moonep_expert_product(moonep_ctx *ctx, const int32_t *cu_seqlens,
                           const uint8_t *a, int64_t row_bytes,
                           const uint8_t *a_scales, int64_t scale_row_bytes,
