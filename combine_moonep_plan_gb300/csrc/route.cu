@@ -481,14 +481,19 @@ struct FinishArgs {
 
 constexpr int kFinishBlocks = 8;
 
-__device__ __forceinline__ void finish_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::
-                   : "memory");
+__device__ __forceinline__ void finish_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void finish_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // Sums the route kernel's partials in order: counts, coefficients, loss.  One
 // cluster; block b takes ranks b, b + 8, ... and, in global scope, a share of
-// the experts once every rank is summed.
+// the experts once every rank is summed.  Every block meets the others once
+// before its part of the loss goes to block 0's shared memory, which is there
+// only from block 0's start on: in rank scope the arrival is the first thing
+// done, so the wait costs nothing.
 __global__ void __cluster_dims__(kFinishBlocks, 1, 1) __launch_bounds__(256)
     route_finish_kernel(FinishArgs a) {
   pdl_wait();
@@ -496,6 +501,7 @@ __global__ void __cluster_dims__(kFinishBlocks, 1, 1) __launch_bounds__(256)
   __shared__ float red[8];
   __shared__ float share[kFinishBlocks];  // block 0's: the blocks' parts of the loss
   const int b = blockIdx.x;
+  if (a.loss && !a.global) finish_arrive();
   int64_t total = 0;
   int busy = 0;
   for (int r = 0; r < a.R; r++) {
@@ -528,8 +534,9 @@ __global__ void __cluster_dims__(kFinishBlocks, 1, 1) __launch_bounds__(256)
     }
   }
   if (!a.loss) return;
+  if (a.global) finish_arrive();
+  finish_wait();
   if (a.global) {
-    finish_sync();
     const float t = (float)(total > 0 ? total : 1);
     const float q0 = a.alpha * (float)a.E / ((float)a.K * t * t);
     for (int e = b * blockDim.x + threadIdx.x; e < a.E; e += kFinishBlocks * blockDim.x) {
@@ -557,7 +564,8 @@ __global__ void __cluster_dims__(kFinishBlocks, 1, 1) __launch_bounds__(256)
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to), "f"(v) : "memory");
   }
   __syncwarp();
-  finish_sync();
+  finish_arrive();
+  finish_wait();
   if (b == 0 && threadIdx.x == 0) {
     float v = 0.0f;
     for (int i = 0; i < kFinishBlocks; i++) v += share[i];

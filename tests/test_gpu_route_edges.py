@@ -1,0 +1,38 @@
+"""The router at its edges: long runs of short calls."""
+import numpy as np
+import pytest
+import torch
+
+from tests import expert_refs as ref
+
+pytestmark = pytest.mark.gpu
+
+EPS = 2.0 ** -23
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from combine_moonep_plan_gb300 import build
+    build.build()
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+
+
+def _buffer(R, S, K, E, **kw):
+    from combine_moonep_plan_gb300 import Buffer
+    return Buffer(S=S, H=8, K=K, E=E, num_ep_ranks=R, zero_copy_views=False, **kw)
+
+
+@pytest.mark.parametrize("scope", ["rank", "global"])
+def test_loss_repeats_over_many_short_calls(scope):
+    """The blocks that add up the loss start at different times; every one of a
+    long run of short calls gives the same loss, and the formula's."""
+    R, S, E, K = 8, 16, 16, 2
+    zn = np.random.default_rng(4).standard_normal((R, S, E)).astype(np.float32)
+    z = torch.from_numpy(zn).cuda()
+    buf = _buffer(R, S, K, E)
+    first = buf.route(z, balance=0.5, scope=scope)
+    losses = torch.cat([buf.route(z, balance=0.5, scope=scope).loss for _ in range(500)])
+    assert torch.equal(losses, first.loss.expand_as(losses))
+    _, _, _, loss, _, _ = ref.route(zn, K, "softmax", [S] * R, 0.5, scope)
+    assert abs(first.loss.item() - loss) <= (np.ptp(zn) + S + R * E + 32) * EPS * loss
+    assert buf.get_status() == 0
