@@ -37,7 +37,7 @@
 // barrier before the CTAs leave, on every path.
 //
 // A wait by parity must not come a whole use of its barrier early.  The sets of
-// scale warps alternate, but a warp's waits are at most four stages apart, and
+// scale warps alternate, but a warp's waits are at most three stages apart, and
 // a stage's barrier is used again after five: the products that the earlier
 // wait saw complete include those of the use before.
 //
@@ -62,6 +62,17 @@ namespace {
 
 constexpr int kThreads = 544;
 constexpr int kStages = 5;
+constexpr int kScaleSets = 2;             // sets of scale warps that take turns,
+constexpr int kScaleWarps = 3;            // warps of a set,
+constexpr int kChunkStages = 2;           // and stages of a turn (512 values of k)
+constexpr int kTileBatch = 32;            // tiles that the schedule warp hands out at a time
+// Arrivals: a stage is full with the leader's expect_tx and one set of scale
+// warps of each CTA; an accumulator is free with the epilogue warps of both
+// CTAs; a batch of tiles is read by a CTA's load, scale and epilogue warps, and
+// by the leader's product warp.
+constexpr int kFullArrivals = 1 + 2 * kScaleWarps;
+constexpr int kAccReaders = 16;
+constexpr int kTileReaders = 1 + kScaleSets * kScaleWarps + kAccReaders / 2;
 constexpr int kMaxCols = 192;             // rows of a piece (MMA N)
 constexpr int kTileN = 256;               // outputs per tile (MMA M of the pair)
 constexpr int kStageK = 256;              // values of k per stage (128 bytes)
@@ -77,6 +88,9 @@ constexpr int kEntries = 1024;            // tile table entries
 constexpr long long kLimitNs = 1000000000LL;
 static_assert(kSfBase + kStages * kSfCols <= 512, "TMEM columns");
 static_assert(kStageBytes % 1024 == 0, "operand tiles start on 1 KB");
+static_assert(kChunkStages * (kScaleSets - 1) + 1 <= kStages,
+              "a scale warp's waits lie at most one use of a stage apart");
+static_assert(kThreads == 32 * (1 + kScaleSets * kScaleWarps + 1 + kAccReaders / 2 + 1), "warps");
 
 struct __align__(1024) Shared {
   uint8_t stage[kStages][kStageBytes];
@@ -425,18 +439,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     sh->dead = 0;
     for (int s = 0; s < kStages; s++) {
-      // full: the leader's expect_tx and one set of scale warps of each CTA
-      asm volatile("mbarrier.init.shared::cta.b64 [%0], 7;" ::"r"(smem_addr(&sh->full[s])));
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(&sh->full[s])),
+                   "r"(kFullArrivals));
       asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_addr(&sh->empty[s])));
     }
     for (int b = 0; b < 2; b++) {
-      // read by the TMA, scale and epilogue warps, and the leader's MMA warp
       asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_addr(&sh->tile_full[b])));
       asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(&sh->tile_empty[b])),
-                   "r"(rank == 0 ? 16 : 15));
+                   "r"(kTileReaders + (rank == 0)));
       asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_addr(&sh->acc_full[b])));
-      // eight epilogue warps of each CTA
-      asm volatile("mbarrier.init.shared::cta.b64 [%0], 16;" ::"r"(smem_addr(&sh->acc_empty[b])));
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(&sh->acc_empty[b])),
+                   "r"(kAccReaders));
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -507,7 +520,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // role 0: the CTA's 128 weight rows; 1, 2: the piece's rows 0-127, 128-191.
     // A warp takes every second chunk (512 values of k, two stages) of the
     // CTA's sequence of tiles, two of its chunks' loads in flight.
-    const int role = (warp - 1) % 3, turn = (warp - 1) / 3;
+    const int role = (warp - 1) % kScaleWarps, turn = (warp - 1) / kScaleWarps;
     const int nsc = a.Kd / 32, chunks = (a.Kd + 511) / 512;
     const bool vec = role ? a.as16 : a.ws16;
     const uint8_t *base = role ? a.as : a.ws;
