@@ -36,10 +36,12 @@
 // MOONEP_ERR_TIMEOUT, drains and returns; every warp reaches the cluster
 // barrier before the CTAs leave, on every path.
 //
-// A wait by parity must not come a whole use of its barrier early.  The sets of
-// scale warps alternate, but a warp's waits are at most three stages apart, and
-// a stage's barrier is used again after five: the products that the earlier
-// wait saw complete include those of the use before.
+// A wait by parity must come neither a whole use of its barrier early nor two
+// phases late, and nothing promises that the releases of two stages arrive in
+// their order, so every warp waits for every phase of its barriers.  A scale
+// warp waits for the stages of the other set's next chunk before its last
+// arrival on its own: they cannot be used, and their barriers cannot move on,
+// without that arrival.
 //
 // Measured (the kernel alone): 128 experts with 9536 rows, N = 4096, Kd =
 // 1536: 106 us, 6.5 TB/s, 0.96 of the copy rate, bound by the weights' bytes.
@@ -88,8 +90,6 @@ constexpr int kEntries = 1024;            // tile table entries
 constexpr long long kLimitNs = 1000000000LL;
 static_assert(kSfBase + kStages * kSfCols <= 512, "TMEM columns");
 static_assert(kStageBytes % 1024 == 0, "operand tiles start on 1 KB");
-static_assert(kChunkStages * (kScaleSets - 1) + 1 <= kStages,
-              "a scale warp's waits lie at most one use of a stage apart");
 static_assert(kThreads == 32 * (1 + kScaleSets * kScaleWarps + 1 + kAccReaders / 2 + 1), "warps");
 
 struct __align__(1024) Shared {
@@ -555,8 +555,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         phase ^= 1;
       }
     };
-    // writes a chunk's scales into its one or two stages
-    auto fill = [&](const uint4 v[4], int c) {
+    // writes a chunk's scales into its one or two stages; `other`: stages of the
+    // other set's chunk after it
+    auto fill = [&](const uint4 v[4], int c, int other) {
 #pragma unroll
       for (int h = 0; h < 2; h++) {
         if (c * 2 + h >= stages) break;
@@ -572,6 +573,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // the tensor cores read these lines through the async proxy
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
+        if (h == 1 || c * 2 + 1 >= stages)
+          for (int n = 1; n <= other; n++) {
+            const bool wrap = s + n >= kStages;
+            if (!wait(sh, &sh->empty[wrap ? s + n - kStages : s + n], phase ^ !wrap, a.status))
+              return false;
+          }
         if (lane == 0) arrive_leader(&sh->full[s], to_leader);
         skip(1);
       }
@@ -597,7 +604,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int i = 0; i < 2; i++) {
         if (t >= mine || !ok) break;
-        if (!(ok = fill(buf[i], c))) break;
+        const bool ends = c + 1 == chunks;
+        const int other = ends && t + 1 == mine ? 0 : min(2, ends ? stages : stages - 2 * (c + 1));
+        if (!(ok = fill(buf[i], c, other))) break;
         load(buf[i]);
         move();
         if (t < mine) pass();

@@ -17,10 +17,13 @@ SOURCE = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))
 
 
 def constants():
-    """The kernel's integer constants, by name."""
-    c = {}
-    for name, value in re.findall(r"^constexpr int (k\w+) = ([^;]+);", open(SOURCE).read(), re.M):
+    """The kernel's integer constants, by name, and whether its scale warps wait
+    for the other set's stages too (passed)."""
+    c, text = {}, open(SOURCE).read()
+    for name, value in re.findall(r"^constexpr int (k\w+) = ([^;]+);", text, re.M):
         c[name] = eval(value.replace("/", "//"), {}, c)
+    scales = text[text.index("auto fill = "):text.index("auto pass = ")]
+    c["passed"] = scales.count("wait(sh, &sh->empty[") == 2
     return c
 
 
@@ -169,10 +172,14 @@ def run(c, tiles, stages, seed, ring=0):
                     raise Fault("scales of another chunk")
                 yield rnd.random() * 3
                 cta[r]["box_empty"][q % ring].arrive()
-            for _ in range(here):
+            for h in range(here):
                 yield cta[r]["empty"][pos[0]], pos[1] ^ 1
                 yield rnd.random() * rnd.choice((1, 1, 20))
                 put(r, pos[0], "scales%d" % role, pos[2])
+                if h == here - 1 and c["passed"] and q + 1 < tiles * chunks:
+                    for n in range(1, 1 + min(wide, stages - (q + 1) % chunks * wide)):
+                        wrap = pos[0] + n >= S
+                        yield cta[r]["empty"][pos[0] + n - S * wrap], pos[1] ^ 1 ^ wrap
                 lead["full"][pos[0]].arrive()
                 skip(1)
             yield from load()
@@ -198,10 +205,10 @@ def run(c, tiles, stages, seed, ring=0):
                     done[0] += 1
                     if last:
                         acc[i & 1] = i
-                    for t in cta:  # the two CTAs hear of it at different times
-                        at(now[0] + rnd.uniform(0, 3), t["empty"][s].arrive)
-                        if last:
-                            at(now[0] + rnd.uniform(0, 3), t["acc_full"][i & 1].arrive)
+                    # the CTAs hear of it at any time after
+                    for t in cta:
+                        for bar in [t["empty"][s]] + [t["acc_full"][i & 1]] * last:
+                            at(now[0] + rnd.random() * rnd.choice((3, 3, 3, 60)), bar.arrive)
                 at(pipe[0], finish)
                 g += 1
                 s, phase = (0, phase ^ 1) if s == S - 1 else (s + 1, phase)
@@ -237,11 +244,11 @@ def run(c, tiles, stages, seed, ring=0):
             except StopIteration:
                 live.remove(p)
                 continue
-            if isinstance(step, tuple):
-                p[2], p[3] = step, 0.0
+            if isinstance(step, tuple):  # a wait, that any warp may come late to
+                p[2], p[3] = step, now[0] + rnd.choice((0, 0, 0, 0, 0, 0, 0, 60)) * rnd.random()
             else:
                 p[2], p[3] = None, now[0] + step
-                at(p[3], lambda: None)
+            at(p[3], lambda: None)
         if not moved:
             if not events:
                 raise Fault("deadlock of " + ", ".join(sorted({p[1] for p in live})))
