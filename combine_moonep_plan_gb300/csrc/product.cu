@@ -507,6 +507,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
     }
+    // the last products release their stages in both CTAs, some time after the
+    // accumulator is announced: a CTA does not leave before its own are
+    for (int q = 0; q < kStages && ok; q++)
+      ok = wait(sh, &sh->empty[q], (uint32_t)q < s ? phase : phase ^ 1, a.status);
     // given up: the copies in flight end before the CTA does
     if (!ok && rank == 0)
       for (int q = 0; q < kStages; q++) {

@@ -2,7 +2,8 @@
 every warp that waits or arrives, and the asynchronous copies and products, with
 random delays.  It reports a deadlock, an arrival too many, an operand written
 before the products that read it are done, a product that reads another stage's
-operands, and an accumulator or tile batch used by two at once.
+operands, an accumulator or tile batch used by two at once, and an arrival that
+reaches a CTA after it has left.
 
 Its numbers come from the kernel's source (constants()), so a change of a
 constant there is a change of the model.
@@ -18,12 +19,15 @@ SOURCE = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))
 
 def constants():
     """The kernel's integer constants, by name, and whether its scale warps wait
-    for the other set's stages too (passed)."""
+    for the other set's stages too (passed) and its load warps, before they
+    leave, for the last stages to be released (drain)."""
     c, text = {}, open(SOURCE).read()
     for name, value in re.findall(r"^constexpr int (k\w+) = ([^;]+);", text, re.M):
         c[name] = eval(value.replace("/", "//"), {}, c)
+    loads = text[text.index("if (warp == 0) {"):text.index("} else if (warp < 7) {")]
     scales = text[text.index("auto fill = "):text.index("auto pass = ")]
     c["passed"] = scales.count("wait(sh, &sh->empty[") == 2
+    c["drain"] = "wait(sh, &sh->empty[q]" in loads
     return c
 
 
@@ -34,6 +38,7 @@ class Fault(Exception):
 class Bar:
     def __init__(self, name, count):
         self.name, self.count, self.left, self.tx, self.phase = name, count, count, 0, 0
+        self.gone = False
 
     def _settle(self):
         if self.left == 0 and self.tx == 0:
@@ -41,6 +46,8 @@ class Bar:
             self.left = self.count
 
     def arrive(self, tx=0):
+        if self.gone:
+            raise Fault("late arrival at " + self.name)
         self.tx += tx
         self.left -= 1
         if self.left < 0:
@@ -129,6 +136,8 @@ def run(c, tiles, stages, seed, ring=0):
                 at(now[0] + rnd.uniform(2, 30), landed)
                 g += 1
                 s, phase = (0, phase ^ 1) if s == S - 1 else (s + 1, phase)
+        for q in range(S if c["drain"] else 0):
+            yield cta[r]["empty"][q], phase if q < s else phase ^ 1
 
     def boxes(r):
         for q in range(tiles * chunks):
@@ -255,3 +264,10 @@ def run(c, tiles, stages, seed, ring=0):
             t, _, f = heapq.heappop(events)
             now[0] = max(now[0], t)
             f()
+    # both CTAs have left
+    for t in cta:
+        for group in t.values():
+            for bar in group:
+                bar.gone = True
+    for _, _, f in events:
+        f()

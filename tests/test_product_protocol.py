@@ -51,3 +51,10 @@ def test_finds_a_shared_ring_of_boxes():
 def test_finds_wrong_counts(name, by):
     count = model.constants()[name]
     assert any_fault([(70, 2)], seeds=4, **{name: count + by})
+
+
+def test_finds_releases_that_outlive_a_cta():
+    """The last products release their stages in both CTAs some time after the
+    accumulator is announced: a CTA that does not wait for them may be gone."""
+    found = any_fault([(1, 1), (2, 6), (5, 14)], drain=False)
+    assert found and all(f.startswith("late arrival at empty") for f in found)
