@@ -134,6 +134,7 @@ int moonep_ctx_create(const moonep_config *cfg, int alloc_views, moonep_ctx **ou
     if (e == cudaSuccess) e = cudaMalloc(&ctx->d_weight_view, rows * sizeof(float) + 16);
   }
   if (e == cudaSuccess) e = plan_configure(c.R, c.E, c.B);
+  if (e == cudaSuccess) e = route_configure(c.E);
   {
     const char *t = getenv("MOONEP_TEST_PLANNER_TIMEOUT");
     ctx->test_planner_timeout = (t && t[0] == '1') ? 1 : 0;

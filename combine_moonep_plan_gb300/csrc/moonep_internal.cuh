@@ -183,6 +183,12 @@ int launch_gated_backward(moonep_ctx *ctx, const int32_t *cu, const uint8_t *g8,
                           const uint8_t *gs, const uint8_t *us, const uint16_t *d_act,
                           const float *w, int F, uint16_t *d_gate, uint16_t *d_up, float *d_w,
                           cudaStream_t st);
+// Raise a kernel's dynamic shared memory limit to at least `bytes` (never
+// lower it: contexts of different shapes, on different host threads, share the
+// kernels).
+cudaError_t raise_dyn_smem(const void *f, int bytes);
+// The shared memory that the router's kernel for long rows needs for E experts.
+cudaError_t route_configure(int E);
 // Opt the planner kernels into the dynamic shared memory E experts need.
 cudaError_t plan_configure(int R, int E, int B);
 // Blocks of the single-launch planner when they can run as one thread-block

@@ -1321,11 +1321,9 @@ static bool bal_in_shared(int R, int E, int B) {
   return bal_tables_words(R, E, B) * sizeof(int32_t) <= kPlanSmemLimit;
 }
 
-// Raise a kernel's dynamic shared memory limit to at least `bytes` (never
-// lower it: contexts of different shapes share the kernels).  The default
-// limit is 48 KB minus the kernel's static shared memory, so any size is set
-// explicitly.
-static cudaError_t raise_dyn_smem(const void *f, int bytes) {
+// The default limit is 48 KB minus the kernel's static shared memory, so any
+// size is set explicitly.
+cudaError_t raise_dyn_smem(const void *f, int bytes) {
   static std::mutex mu;
   static std::map<std::pair<int, const void *>, int> limit;
   int dev = 0;

@@ -779,9 +779,11 @@ int tokens_per_warp(Form f) { return f == kThread8 ? 32 : f == kFour8 ? 8 : 1; }
 // Whether rows are whole 16-byte vectors.
 bool whole_vectors(int E, int bf16) { return E % (bf16 ? 8 : 4) == 0; }
 
-// Warps of a block of the shared-memory form: fewer where two rows of all
-// experts per warp would not fit.
+// Warps of a block of the shared-memory form, two rows of all experts each: at
+// four from 1025 experts on, several blocks still fit an SM up to 2048, and one
+// up to 4096 (147 KB).
 int warps_of(int E) { return E <= 1024 ? kWarps : 4; }
+size_t long_smem(int E) { return (size_t)(2 * warps_of(E) + 1) * E * sizeof(float); }
 
 // Blocks per rank of the forward pass: enough for the rank's tokens, at most
 // four per SM over all ranks (the selection is a chain of warp-wide steps, so
@@ -804,9 +806,9 @@ cudaError_t launch_forward(const RouteArgs &a, int bpr, cudaStream_t st) {
   const dim3 grid(bpr, a.R), block(kWarps * 32);
   const Form f = form_of(a.E);
   const bool vec = whole_vectors(a.E, sizeof(T) == 2);
-  size_t smem = ((size_t)kWarps * a.E + ((a.E + 1) & ~1)) * 4 +
-                (size_t)kWarps * tokens_per_warp(f) * a.K * sizeof(uint2) +
-                (tokens_per_warp(f) == 1 ? (size_t)kWarps * 32 * sizeof(uint2) : 0);
+  const size_t smem = ((size_t)kWarps * a.E + ((a.E + 1) & ~1)) * 4 +
+                      (size_t)kWarps * tokens_per_warp(f) * a.K * sizeof(uint2) +
+                      (tokens_per_warp(f) == 1 ? (size_t)kWarps * 32 * sizeof(uint2) : 0);
   switch (f) {
     case kThread8: return launch_pdl_ex(route_kernel<T, 1, 8>, grid, block, smem, st, false, a.cluster, a, vec);
     case kFour8: return launch_pdl_ex(route_kernel<T, 4, 8>, grid, block, smem, st, false, a.cluster, a, vec);
@@ -817,15 +819,8 @@ cudaError_t launch_forward(const RouteArgs &a, int bpr, cudaStream_t st) {
     case kWarp16: return launch_pdl_ex(route_kernel<T, 32, 16>, grid, block, smem, st, false, a.cluster, a, vec);
     default: break;
   }
-  const int warps = warps_of(a.E);
-  smem = (size_t)(2 * warps + 1) * a.E * sizeof(float);
-  cudaError_t e = cudaSuccess;
-  if (smem > 48 * 1024)
-    e = cudaFuncSetAttribute(route_long_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)smem);
-  return e != cudaSuccess ? e
-                          : launch_pdl_ex(route_long_kernel<T>, grid, dim3(warps * 32), smem, st,
-                                          false, a.cluster, a);
+  return launch_pdl_ex(route_long_kernel<T>, grid, dim3(warps_of(a.E) * 32), long_smem(a.E), st,
+                       false, a.cluster, a);
 }
 
 template <typename T>
@@ -850,6 +845,14 @@ cudaError_t launch_backward(const RouteBwdArgs &a, int sms, cudaStream_t st) {
 }
 
 }  // namespace
+
+cudaError_t route_configure(int E) {
+  if (form_of(E) != kLong) return cudaSuccess;
+  cudaError_t e = raise_dyn_smem((const void *)route_long_kernel<float>, (int)long_smem(E));
+  if (e == cudaSuccess)
+    e = raise_dyn_smem((const void *)route_long_kernel<__nv_bfloat16>, (int)long_smem(E));
+  return e;
+}
 
 int64_t route_scratch_words(int R, int E, int sms) {
   // at most 4 * sms / R + 1 blocks per rank

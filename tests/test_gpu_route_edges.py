@@ -36,3 +36,29 @@ def test_loss_repeats_over_many_short_calls(scope):
     _, _, _, loss, _, _ = ref.route(zn, K, "softmax", [S] * R, 0.5, scope)
     assert abs(first.loss.item() - loss) <= (np.ptp(zn) + S + R * E + 32) * EPS * loss
     assert buf.get_status() == 0
+
+
+def test_threads_with_contexts_of_different_sizes():
+    """The kernel for long rows needs shared memory by its number of experts;
+    contexts of different sizes route at the same time, each from a thread."""
+    import threading
+    failures = []
+
+    def work(E):
+        try:
+            buf = _buffer(1, 8, 2, E)
+            with torch.cuda.stream(torch.cuda.Stream()):
+                z = torch.randn(1, 8, E, device="cuda")
+                want = buf.route(z).topk
+                for _ in range(4000):
+                    got = buf.route(z)
+                assert torch.equal(got.topk, want)
+        except Exception as e:  # noqa: BLE001
+            failures.append((E, repr(e)))
+
+    threads = [threading.Thread(target=work, args=(E,)) for E in (4096, 640, 1024)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failures
