@@ -588,6 +588,10 @@ struct RouteBwdArgs {
 // 1 - sigmoid(z), without cancellation.
 __device__ __forceinline__ float one_minus_sigmoid(float z) { return inverse(1.0f + exp_fast(z)); }
 
+// Coefficients are held times 2^40: their products with scores near 2^-126 are
+// then ordinary numbers, as the shares that they stand for are.
+constexpr float kCoefScale = 0x1p40f, kCoefUnscale = 0x1p-40f;
+
 // The same layout of rows in registers; blockIdx.y is the rank, whose
 // coefficients stay in registers too.  A pick's term reaches the lane of its
 // column through a zeroed row of shared memory.
@@ -605,7 +609,8 @@ __global__ void __launch_bounds__(kWarps * 32) route_backward_kernel(RouteBwdArg
   float cf[V];
 #pragma unroll
   for (int i = 0; i < V; i++) {
-    cf[i] = a.coef && col + i < a.E ? __ldg(a.coef + (int64_t)r * a.E + col + i) : 0.0f;
+    cf[i] = a.coef && col + i < a.E
+                ? __ldg(a.coef + (int64_t)r * a.E + col + i) * kCoefScale : 0.0f;
     row[col + i] = 0.0f;
   }
   __syncwarp();
@@ -689,9 +694,10 @@ __global__ void __launch_bounds__(kWarps * 32) route_backward_kernel(RouteBwdArg
       pc = group_sum<LP>(pc);
       const float inv = Z == 0.0f ? 0.0f : 1.0f / Z;
       pc *= inv;
-      const float f = dl * inv;
+      const float f = dl * kCoefUnscale;
 #pragma unroll
-      for (int i = 0; i < V; i++) g[i] = on ? (g[i] + f * p[i] * (cf[i] - pc)) * slope[i] : 0.0f;
+      for (int i = 0; i < V; i++)
+        g[i] = on ? (g[i] + p[i] * inv * (f * (cf[i] - pc))) * slope[i] : 0.0f;
     }
     if (s < a.S) store_row<V>((T *)a.dz + t * a.E, col, a.E, vec, g);
     __syncwarp();
@@ -732,13 +738,13 @@ __global__ void __launch_bounds__(kWarps * 32) route_backward_long_kernel(RouteB
       for (int e = lane; e < a.E; e += 32) {
         const float s1 = score(to_f(z[e]), m, a.sigmoid);
         Z += s1;
-        pc += s1 * cf[e];
+        pc += s1 * (cf[e] * kCoefScale);
       }
       Z = warp_sum(Z);
       pc = warp_sum(pc);
     }
     const float inv = Z == 0.0f ? 0.0f : 1.0f / Z;
-    pc *= inv;
+    pc = pc * inv * kCoefUnscale;
     float wk = 0.0f, dk = 0.0f;
     int id = -1;
     if (lane < a.K) {
@@ -751,7 +757,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_backward_long_kernel(RouteB
     for (int e = lane; e < a.E; e += 32) {
       const float x = to_f(z[e]);
       float g = 0.0f;
-      if (cf) g = dl * score(x, m, a.sigmoid) * inv * (cf[e] - pc);
+      if (cf) g = score(x, m, a.sigmoid) * inv * (dl * (cf[e] - pc));
       if (a.sigmoid) g *= one_minus_sigmoid(x);
       put(out + e, g);
     }
@@ -759,7 +765,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_backward_long_kernel(RouteB
     if (id >= 0) {
       const float x = to_f(z[id]);
       float g = wk * (dk - wd);
-      if (cf) g += dl * score(x, m, a.sigmoid) * inv * (cf[id] - pc);
+      if (cf) g += score(x, m, a.sigmoid) * inv * (dl * (cf[id] - pc));
       if (a.sigmoid) g *= one_minus_sigmoid(x);
       put(out + id, g);
     }

@@ -62,3 +62,33 @@ def test_threads_with_contexts_of_different_sizes():
     for t in threads:
         t.join()
     assert not failures
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("d_loss", [1.0, 1e4, 1e-6])
+@pytest.mark.parametrize("E", [8, 24, 48, 128, 200, 300, 500, 640])
+def test_gradient_of_very_small_scores(E, d_loss, dtype):
+    """Sigmoid scores near 2^-120: their shares are ordinary numbers, and so is
+    the gradient.  Bounds as for ordinary scores, the exponential's error that
+    of its argument (up to 84, 2^-24 each)."""
+    R, S, K = 2, 37, 2
+    rng = np.random.default_rng(E)
+    z = torch.from_numpy(-83.0 + rng.standard_normal((R, S, E)) * 0.3).to(getattr(torch, dtype))
+    zn = z.double().numpy()
+    buf = _buffer(R, S, K, E)
+    z = z.cuda()
+    out = buf.route(z, scoring="sigmoid", balance=0.3)
+    ids, w, tpe, loss, coef, _ = ref.route(zn, K, "sigmoid", [S] * R, 0.3, "rank")
+    assert np.array_equal(out.topk.cpu().numpy(), ids)
+    assert np.all(np.abs(out.weights.cpu().numpy() - w) <= (90 + K + 16) * EPS * w)
+    assert abs(out.loss.item() - loss) <= (90 + S + R * E + 32) * EPS * loss
+    dw = rng.standard_normal((R, S, K)).astype(np.float32)
+    for d in (dw, None):
+        dz = buf.route_backward(out, z, None if d is None else torch.from_numpy(d).cuda(),
+                                torch.tensor([d_loss], device="cuda"))
+        want, mag = ref.route_grad(zn, ids, w, np.zeros_like(dw, np.float64) if d is None
+                                   else d.astype(np.float64), coef, d_loss, "sigmoid", [S] * R)
+        tol = (3 * 90 + E + K + 48) * EPS * mag
+        if dtype == "bfloat16":
+            tol = tol + np.abs(want) * 2.0 ** -8
+        assert np.all(np.abs(dz.double().cpu().numpy() - want) <= tol)
