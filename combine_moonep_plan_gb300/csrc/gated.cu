@@ -190,13 +190,16 @@ bool few_rows(const moonep_ctx *ctx) {
 }
 
 // Blocks over a rank's rows, at most `per_sm` per SM over all ranks (0: one
-// for every rows_per_block rows).  At 327168 x 2048 the forward pass took 604,
-// 511 and 495 us with 8, 16 and no limit, the backward pass 706, 696 and 711.
-dim3 grid_for(const moonep_ctx *ctx, int rows_per_block, int per_sm) {
-  int64_t need = ((int64_t)ctx->NvS + rows_per_block - 1) / rows_per_block;
-  const int64_t cap = ((int64_t)ctx->sms * per_sm + ctx->cfg.R - 1) / ctx->cfg.R;
-  if (per_sm && need > cap) need = cap;
-  return dim3((unsigned)need, ctx->cfg.R);
+// for every rows_per_block rows), and no more than num_sms SMs hold (`cap`, at
+// least one per rank).  At 327168 x 2048 the forward pass took 604, 511 and
+// 495 us with 8, 16 and no limit, the backward pass 706, 696 and 711.
+dim3 grid_for(const moonep_ctx *ctx, int rows_per_block, int per_sm, int64_t cap) {
+  const int R = ctx->cfg.R;
+  int64_t blocks = ((int64_t)ctx->NvS + rows_per_block - 1) / rows_per_block;
+  const int64_t most = ((int64_t)ctx->sms * per_sm + R - 1) / R;
+  if (per_sm && blocks > most) blocks = most;
+  if (blocks > cap / R) blocks = cap / R > 0 ? cap / R : 1;
+  return dim3((unsigned)blocks, R);
 }
 
 }  // namespace
@@ -216,8 +219,8 @@ int launch_gated(moonep_ctx *ctx, const int32_t *cu, const uint16_t *gate, const
   const bool few = few_rows(ctx);
   auto kern = few ? (g8 ? gated_kernel<true, 8> : gated_kernel<false, 8>)
                   : (g8 ? gated_kernel<true, 1> : gated_kernel<false, 1>);
-  return cuda_status(
-      launch_pdl(kern, grid_for(ctx, few ? 1 : 8, 0), dim3(kThreads), 0, st, false, a));
+  const dim3 grid = grid_for(ctx, few ? 1 : 8, 0, blocks_in_cap(ctx, kern, kThreads, 0));
+  return cuda_status(launch_pdl(kern, grid, dim3(kThreads), 0, st, false, a));
 }
 
 int launch_gated_backward(moonep_ctx *ctx, const int32_t *cu, const uint8_t *g8, const uint8_t *u8,
@@ -235,8 +238,9 @@ int launch_gated_backward(moonep_ctx *ctx, const int32_t *cu, const uint8_t *g8,
   a.d_up = d_up;
   a.d_w = d_w;
   const bool few = few_rows(ctx);
-  return cuda_status(launch_pdl(few ? gated_backward_kernel<8> : gated_backward_kernel<1>,
-                                grid_for(ctx, few ? 1 : 8, 16), dim3(kThreads), 0, st, false, a));
+  auto kern = few ? gated_backward_kernel<8> : gated_backward_kernel<1>;
+  const dim3 grid = grid_for(ctx, few ? 1 : 8, 16, blocks_in_cap(ctx, kern, kThreads, 0));
+  return cuda_status(launch_pdl(kern, grid, dim3(kThreads), 0, st, false, a));
 }
 
 }  // namespace moonep

@@ -264,6 +264,19 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
                        std::forward<Args>(args)...);
 }
 
+// Blocks of a kernel that the SMs of a capped context hold (num_sms); without a
+// cap the hardware is the limit and INT32_MAX is returned.
+template <typename... KArgs>
+int64_t blocks_in_cap(const moonep_ctx *ctx, void (*kernel)(KArgs...), int threads, size_t smem) {
+  if (ctx->sms >= ctx->sms_device) return INT32_MAX;
+  int n = 0;
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem) != cudaSuccess) {
+    cudaGetLastError();
+    n = 1;
+  }
+  return (int64_t)ctx->sms * (n > 0 ? n : 1);
+}
+
 // Latch the first error code into the status word.
 __device__ __forceinline__ void set_status(int32_t *status, int code) {
   atomicCAS(status, 0, code);

@@ -118,10 +118,12 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(const uint8_t *pac
 
 // One block for every `batch` units per thread, in each of `spans` equal
 // spans (a capped grid that walks its span was 3 to 18 % slower); the loops
-// serve tensors whose blocks would not fit in a grid.
-dim3 grid_for(int64_t units, int spans, int batch) {
+// serve tensors whose blocks would not fit in a grid, or in num_sms SMs (`cap`
+// blocks, at least one per span).
+dim3 grid_for(int64_t units, int spans, int batch, int64_t cap) {
   const int64_t need = (units + (int64_t)kThreads * batch - 1) / ((int64_t)kThreads * batch);
-  return dim3((unsigned)(need < INT32_MAX ? need : INT32_MAX), spans);
+  const int64_t most = cap / spans > 0 ? cap / spans : 1;
+  return dim3((unsigned)(need < most ? need : most), spans);
 }
 
 }  // namespace
@@ -134,18 +136,22 @@ int launch_quantize_mx(moonep_ctx *ctx, const void *x, int fp32, int64_t rows, i
   auto kern = lng ? (fp32 ? quantize_kernel<float, kLongBatch>
                           : quantize_kernel<__nv_bfloat16, kLongBatch>)
                   : (fp32 ? quantize_kernel<float, kBatch> : quantize_kernel<__nv_bfloat16, kBatch>);
-  return cuda_status(launch_pdl(kern, grid_for(a.units, spans, lng ? kLongBatch : kBatch),
-                                dim3(kThreads), 0, st, false, a));
+  const dim3 grid = grid_for(a.units, spans, lng ? kLongBatch : kBatch,
+                             blocks_in_cap(ctx, kern, kThreads, 0));
+  return cuda_status(launch_pdl(kern, grid, dim3(kThreads), 0, st, false, a));
 }
 
 int launch_dequantize_mx(moonep_ctx *ctx, const uint8_t *packed, const uint8_t *scales, int fp32,
                          int64_t rows, int64_t cols, void *y, cudaStream_t st) {
   const int64_t units = rows * (cols / 8);
-  const dim3 grid = grid_for(units, 1, kBatch);
+  auto grid = [&](auto kern) {
+    return grid_for(units, 1, kBatch, blocks_in_cap(ctx, kern, kThreads, 0));
+  };
   if (fp32)
-    return cuda_status(launch_pdl(dequantize_kernel<float>, grid, dim3(kThreads), 0, st, false,
-                                  packed, scales, (float *)y, units));
-  return cuda_status(launch_pdl(dequantize_kernel<__nv_bfloat16>, grid, dim3(kThreads), 0, st,
+    return cuda_status(launch_pdl(dequantize_kernel<float>, grid(dequantize_kernel<float>),
+                                  dim3(kThreads), 0, st, false, packed, scales, (float *)y, units));
+  return cuda_status(launch_pdl(dequantize_kernel<__nv_bfloat16>,
+                                grid(dequantize_kernel<__nv_bfloat16>), dim3(kThreads), 0, st,
                                 false, packed, scales, (__nv_bfloat16 *)y, units));
 }
 

@@ -793,61 +793,84 @@ size_t long_smem(int E) { return (size_t)(2 * warps_of(E) + 1) * E * sizeof(floa
 
 // Blocks per rank of the forward pass: enough for the rank's tokens, at most
 // four per SM over all ranks (the selection is a chain of warp-wide steps, so
-// it wants warps: two per SM took 48 us for 32768 x 256); a power of two up to the cluster size, then a
+// it wants warps: two per SM took 48 us for 32768 x 256; rows of 257 logits and
+// more need the registers of two and so take two waves) and no more than num_sms
+// SMs hold (`held`), but one; a power of two up to the cluster size, then a
 // multiple of it.
-int blocks_per_rank(int R, int S, int E, int sms) {
+int blocks_per_rank(int R, int S, int E, int sms, int64_t held) {
   const Form f = form_of(E);
   const int per = (f == kLong ? warps_of(E) : kWarps) * tokens_per_warp(f);
   const int64_t need = ((int64_t)S + per - 1) / per;
-  const int64_t cap = (4 * sms + R - 1) / R;
-  int64_t b = need < cap ? need : cap;
+  int64_t cap = (4 * sms + R - 1) / R;
+  if (held / R < cap) cap = held / R > 0 ? held / R : 1;
+  const int64_t b = need < cap ? need : cap;
   if (b >= kCluster) return (int)(b / kCluster * kCluster);
   int p = 1;
-  while (p < b) p <<= 1;
+  while (p < b && 2 * p <= cap) p <<= 1;
   return p;
+}
+
+// The kernel of rows in registers (any form but kLong), and its shared memory.
+template <typename T>
+auto route_kernel_of(Form f) {
+  return f == kThread8 ? route_kernel<T, 1, 8> : f == kFour8 ? route_kernel<T, 4, 8>
+         : f == kWarp2 ? route_kernel<T, 32, 2> : f == kWarp4 ? route_kernel<T, 32, 4>
+         : f == kWarp8 ? route_kernel<T, 32, 8> : f == kWarp12 ? route_kernel<T, 32, 12>
+                                                               : route_kernel<T, 32, 16>;
+}
+size_t route_smem(Form f, int E, int K) {
+  return ((size_t)kWarps * E + ((E + 1) & ~1)) * 4 +
+         (size_t)kWarps * tokens_per_warp(f) * K * sizeof(uint2) +
+         (tokens_per_warp(f) == 1 ? (size_t)kWarps * 32 * sizeof(uint2) : 0);
+}
+
+// Blocks of the forward kernel that num_sms SMs hold.
+template <typename T>
+int64_t route_held(const moonep_ctx *ctx) {
+  const int E = ctx->cfg.E;
+  const Form f = form_of(E);
+  return f == kLong ? blocks_in_cap(ctx, route_long_kernel<T>, warps_of(E) * 32, long_smem(E))
+                    : blocks_in_cap(ctx, route_kernel_of<T>(f), kWarps * 32,
+                                    route_smem(f, E, ctx->cfg.K));
 }
 
 template <typename T>
 cudaError_t launch_forward(const RouteArgs &a, int bpr, cudaStream_t st) {
-  const dim3 grid(bpr, a.R), block(kWarps * 32);
+  const dim3 grid(bpr, a.R);
   const Form f = form_of(a.E);
-  const bool vec = whole_vectors(a.E, sizeof(T) == 2);
-  const size_t smem = ((size_t)kWarps * a.E + ((a.E + 1) & ~1)) * 4 +
-                      (size_t)kWarps * tokens_per_warp(f) * a.K * sizeof(uint2) +
-                      (tokens_per_warp(f) == 1 ? (size_t)kWarps * 32 * sizeof(uint2) : 0);
-  switch (f) {
-    case kThread8: return launch_pdl_ex(route_kernel<T, 1, 8>, grid, block, smem, st, false, a.cluster, a, vec);
-    case kFour8: return launch_pdl_ex(route_kernel<T, 4, 8>, grid, block, smem, st, false, a.cluster, a, vec);
-    case kWarp2: return launch_pdl_ex(route_kernel<T, 32, 2>, grid, block, smem, st, false, a.cluster, a, vec);
-    case kWarp4: return launch_pdl_ex(route_kernel<T, 32, 4>, grid, block, smem, st, false, a.cluster, a, vec);
-    case kWarp8: return launch_pdl_ex(route_kernel<T, 32, 8>, grid, block, smem, st, false, a.cluster, a, vec);
-    case kWarp12: return launch_pdl_ex(route_kernel<T, 32, 12>, grid, block, smem, st, false, a.cluster, a, vec);
-    case kWarp16: return launch_pdl_ex(route_kernel<T, 32, 16>, grid, block, smem, st, false, a.cluster, a, vec);
-    default: break;
-  }
-  return launch_pdl_ex(route_long_kernel<T>, grid, dim3(warps_of(a.E) * 32), long_smem(a.E), st,
-                       false, a.cluster, a);
+  if (f == kLong)
+    return launch_pdl_ex(route_long_kernel<T>, grid, dim3(warps_of(a.E) * 32), long_smem(a.E), st,
+                         false, a.cluster, a);
+  return launch_pdl_ex(route_kernel_of<T>(f), grid, dim3(kWarps * 32), route_smem(f, a.E, a.K), st,
+                       false, a.cluster, a, whole_vectors(a.E, sizeof(T) == 2));
 }
 
 template <typename T>
-cudaError_t launch_backward(const RouteBwdArgs &a, int sms, cudaStream_t st) {
+auto route_backward_kernel_of(Form f) {
+  return f == kThread8 ? route_backward_kernel<T, 1, 8> : f == kFour8 ? route_backward_kernel<T, 4, 8>
+         : f == kWarp2 ? route_backward_kernel<T, 32, 2>
+         : f == kWarp4 ? route_backward_kernel<T, 32, 4>
+         : f == kWarp8 ? route_backward_kernel<T, 32, 8>
+         : f == kWarp12 ? route_backward_kernel<T, 32, 12>
+                        : route_backward_kernel<T, 32, 16>;
+}
+
+template <typename T>
+cudaError_t launch_backward(const moonep_ctx *ctx, const RouteBwdArgs &a, cudaStream_t st) {
   const Form f = form_of(a.E);
-  const bool vec = whole_vectors(a.E, sizeof(T) == 2);
-  const int per = kWarps * tokens_per_warp(f);
+  const int per = kWarps * tokens_per_warp(f), threads = kWarps * 32;
   const int per_sm = f == kWarp16 ? 2 : 3;  // what the registers allow
-  const int64_t need = ((int64_t)a.S + per - 1) / per, cap = ((int64_t)sms * per_sm + a.R - 1) / a.R;
-  const dim3 grid((unsigned)(need < cap ? need : cap), a.R), block(kWarps * 32);
-  switch (f) {
-    case kThread8: return launch_pdl(route_backward_kernel<T, 1, 8>, grid, block, 0, st, false, a, vec);
-    case kFour8: return launch_pdl(route_backward_kernel<T, 4, 8>, grid, block, 0, st, false, a, vec);
-    case kWarp2: return launch_pdl(route_backward_kernel<T, 32, 2>, grid, block, 0, st, false, a, vec);
-    case kWarp4: return launch_pdl(route_backward_kernel<T, 32, 4>, grid, block, 0, st, false, a, vec);
-    case kWarp8: return launch_pdl(route_backward_kernel<T, 32, 8>, grid, block, 0, st, false, a, vec);
-    case kWarp12: return launch_pdl(route_backward_kernel<T, 32, 12>, grid, block, 0, st, false, a, vec);
-    case kWarp16: return launch_pdl(route_backward_kernel<T, 32, 16>, grid, block, 0, st, false, a, vec);
-    default: break;
-  }
-  return launch_pdl(route_backward_long_kernel<T>, grid, block, 0, st, false, a);
+  const int64_t held = f == kLong
+                           ? blocks_in_cap(ctx, route_backward_long_kernel<T>, threads, 0)
+                           : blocks_in_cap(ctx, route_backward_kernel_of<T>(f), threads, 0);
+  const int64_t need = ((int64_t)a.S + per - 1) / per;
+  int64_t cap = ((int64_t)ctx->sms * per_sm + a.R - 1) / a.R;
+  if (held / a.R < cap) cap = held / a.R > 0 ? held / a.R : 1;
+  const dim3 grid((unsigned)(need < cap ? need : cap), a.R);
+  if (f == kLong)
+    return launch_pdl(route_backward_long_kernel<T>, grid, dim3(threads), 0, st, false, a);
+  return launch_pdl(route_backward_kernel_of<T>(f), grid, dim3(threads), 0, st, false, a,
+                    whole_vectors(a.E, sizeof(T) == 2));
 }
 
 }  // namespace
@@ -871,7 +894,8 @@ int launch_route(moonep_ctx *ctx, const void *logits, int bf16, int scoring, flo
   const moonep_config &c = ctx->cfg;
   RouteArgs a{};
   FinishArgs f{};
-  const int bpr = blocks_per_rank(c.R, c.S, c.E, ctx->sms);
+  const int bpr = blocks_per_rank(
+      c.R, c.S, c.E, ctx->sms, bf16 ? route_held<__nv_bfloat16>(ctx) : route_held<float>(ctx));
   a.R = f.R = c.R;
   a.S = f.S = c.S;
   a.E = f.E = c.E;
@@ -919,8 +943,8 @@ int launch_route_backward(moonep_ctx *ctx, const void *logits, int bf16, int sco
   a.K = c.K;
   a.sigmoid = scoring;
   for (int r = 0; r < c.R; r++) a.ntok[r] = num_tokens ? num_tokens[r] : c.S;
-  return cuda_status(bf16 ? launch_backward<__nv_bfloat16>(a, ctx->sms, st)
-                          : launch_backward<float>(a, ctx->sms, st));
+  return cuda_status(bf16 ? launch_backward<__nv_bfloat16>(ctx, a, st)
+                          : launch_backward<float>(ctx, a, st));
 }
 
 }  // namespace moonep

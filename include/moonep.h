@@ -73,8 +73,12 @@ extern "C" {
  * rank (B = E/R is what training needs [README, How to set B]; smaller B is
  * allowed and reported as MOONEP_ERR_SLOTS when a plan needs more);
  * token_padding = row alignment of every non-empty segment; num_sms caps the
- * SMs the copy kernels use (<= 0: the MOONEP_NUM_SMS environment variable
- * when set to a positive count, else every SM). */
+ * SMs that the copy kernels, the router and the expert stage use (<= 0: the
+ * MOONEP_NUM_SMS environment variable when set to a positive count, else every
+ * SM): a launch has no more blocks than that many SMs hold.  At the least, the
+ * router, moonep_quantize_mx and moonep_gated_act launch one block per rank,
+ * the router's sums one cluster of eight blocks and moonep_expert_product one
+ * pair of SMs. */
 typedef struct moonep_config {
   int R;             /* expert-parallel ranks (logical partitions), >= 1 */
   int E;             /* experts, multiple of R */
