@@ -20,10 +20,17 @@ from . import _lib
 from ._lib import MoonepCommPlan, MoonepConfig, check
 
 
+# The current stream's address without a torch.cuda.Stream object, which takes
+# 3 us, a third of a decode-sized call.  Not part of torch's public interface:
+# where a torch lacks it, the object is asked.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream():
-    """The current stream of the current device, as its address (asking for it
-    as a torch.cuda.Stream object takes 3 us, a third of a decode-sized call)."""
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    """The current stream of the current device, as its address."""
+    if _raw_stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(torch.cuda.current_device())
 
 
 class _DeviceArray:
@@ -68,10 +75,6 @@ def _one_of(t, name, dtypes):
     if t.dtype not in dtypes:
         raise TypeError(f"{name}: expected one of {dtypes}, got {t.dtype}")
     return t.dtype
-
-
-def _ptr(t):
-    return None if t is None else t.data_ptr()
 
 
 def _check_rows(t, name, rows, cols):
