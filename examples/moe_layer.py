@@ -102,12 +102,12 @@ class MoELayer:
         buf, n = self.buf, self.R * self.buf.NvS
         d_y, _, _, _ = buf.dispatch(d_out, plan=s.plan)
         zeros = lambda c: torch.zeros(n, c, device="cuda")  # noqa: E731
-        d_act = self._back_product(d_y, self.down, s.cu, zeros(self.F)).bfloat16()
-        d_gate, d_up, s.d_weights_nvs = buf.gated_act_backward(s.checkpoint, d_act, s.cu,
-                                                               s.weights)
-        d_rows = self._back_product(d_gate, self.gate, s.cu, zeros(self.H))
-        d_rows = self._back_product(d_up, self.up, s.cu, d_rows).bfloat16()
-        d_hidden, s.d_weights = buf.combine(s.plan, d_rows, s.d_weights_nvs)
+        s.d_act = self._back_product(d_y, self.down, s.cu, zeros(self.F)).bfloat16()
+        s.d_gate, s.d_up, s.d_weights_nvs = buf.gated_act_backward(s.checkpoint, s.d_act, s.cu,
+                                                                   s.weights)
+        d_rows = self._back_product(s.d_gate, self.gate, s.cu, zeros(self.H))
+        s.d_rows = self._back_product(s.d_up, self.up, s.cu, d_rows).bfloat16()
+        d_hidden, s.d_weights = buf.combine(s.plan, s.d_rows, s.d_weights_nvs)
         s.d_logits = buf.route_backward(s.route, s.logits, s.d_weights, d_loss)
         d_router = torch.einsum("rse,rsh->eh", s.d_logits, s.hidden.float())
         return d_router, d_hidden.float() + s.d_logits @ self.router
