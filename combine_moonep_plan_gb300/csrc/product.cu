@@ -36,12 +36,14 @@
 // MOONEP_ERR_TIMEOUT, drains and returns; every warp reaches the cluster
 // barrier before the CTAs leave, on every path.
 //
-// A wait by parity must come neither a whole use of its barrier early nor two
-// phases late, and nothing promises that the releases of two stages arrive in
-// their order, so every warp waits for every phase of its barriers.  A scale
-// warp waits for the stages of the other set's next chunk before its last
-// arrival on its own: they cannot be used, and their barriers cannot move on,
-// without that arrival.
+// A wait by parity must not come a whole use of its barrier early, and nothing
+// promises that the releases of two stages arrive in their order.  The load
+// warp waits for every release and passes it on (`passed`); the scale warps,
+// which skip the other set's stages, wait for that: arrivals of one thread in
+// their own CTA are seen in order, a warp's waits are at most three stages apart
+// and a stage is used again after five, so the one that it saw last implies the
+// use before.  (Waiting for the releases themselves, every one of them, held a
+// scale warp to three stages ahead: 1.43 ms for the largest case below.)
 //
 // Measured (the kernel alone): 128 experts with 9536 rows, N = 4096, Kd =
 // 1536: 106 us, 6.5 TB/s, 0.96 of the copy rate, bound by the weights' bytes.
@@ -90,6 +92,8 @@ constexpr int kEntries = 1024;            // tile table entries
 constexpr long long kLimitNs = 1000000000LL;
 static_assert(kSfBase + kStages * kSfCols <= 512, "TMEM columns");
 static_assert(kStageBytes % 1024 == 0, "operand tiles start on 1 KB");
+static_assert(kChunkStages * (kScaleSets - 1) + 1 <= kStages,
+              "a scale warp's waits lie at most one use of a stage apart");
 static_assert(kThreads == 32 * (1 + kScaleSets * kScaleWarps + 1 + kAccReaders / 2 + 1), "warps");
 
 struct __align__(1024) Shared {
@@ -99,7 +103,7 @@ struct __align__(1024) Shared {
   int32_t rows[kEntries];
   int32_t wsum[8];
   int4 tile[2][32];  // the CTA's tiles: group, first output, first row, rows
-  uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2];
+  uint64_t full[kStages], empty[kStages], passed[kStages], acc_full[2], acc_empty[2];
   uint64_t tile_full[2], tile_empty[2];
   uint32_t tmem;
   int32_t dead;
@@ -442,6 +446,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(&sh->full[s])),
                    "r"(kFullArrivals));
       asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_addr(&sh->empty[s])));
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_addr(&sh->passed[s])));
     }
     for (int b = 0; b < 2; b++) {
       asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_addr(&sh->tile_full[b])));
@@ -484,6 +489,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int arow = tile.z + (int)rank * half;
       for (int k = 0; k < stages; k++) {
         if (!(ok = wait(sh, &sh->empty[s], phase ^ 1, a.status))) break;
+        if (lane == 0) arrive(&sh->passed[s]);
         const uint32_t base = smem_addr(sh->stage[s]);
         const uint32_t full = smem_addr(&sh->full[s]), bar = full + to_leader;
         if (elect()) {
@@ -559,13 +565,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         phase ^= 1;
       }
     };
-    // writes a chunk's scales into its one or two stages; `other`: stages of the
-    // other set's chunk after it
-    auto fill = [&](const uint4 v[4], int c, int other) {
+    // writes a chunk's scales into its one or two stages
+    auto fill = [&](const uint4 v[4], int c) {
 #pragma unroll
       for (int h = 0; h < 2; h++) {
         if (c * 2 + h >= stages) break;
-        if (!wait(sh, &sh->empty[s], phase ^ 1, a.status)) return false;
+        if (!wait(sh, &sh->passed[s], phase, a.status)) return false;
         const uint32_t p = smem_addr(sh->stage[s]) + at;
 #pragma unroll
         for (int i = 0; i < 2; i++)
@@ -577,12 +582,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // the tensor cores read these lines through the async proxy
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (h == 1 || c * 2 + 1 >= stages)
-          for (int n = 1; n <= other; n++) {
-            const bool wrap = s + n >= kStages;
-            if (!wait(sh, &sh->empty[wrap ? s + n - kStages : s + n], phase ^ !wrap, a.status))
-              return false;
-          }
         if (lane == 0) arrive_leader(&sh->full[s], to_leader);
         skip(1);
       }
@@ -608,9 +607,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int i = 0; i < 2; i++) {
         if (t >= mine || !ok) break;
-        const bool ends = c + 1 == chunks;
-        const int other = ends && t + 1 == mine ? 0 : min(2, ends ? stages : stages - 2 * (c + 1));
-        if (!(ok = fill(buf[i], c, other))) break;
+        if (!(ok = fill(buf[i], c))) break;
         load(buf[i]);
         move();
         if (t < mine) pass();

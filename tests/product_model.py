@@ -18,16 +18,17 @@ SOURCE = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))
 
 
 def constants():
-    """The kernel's integer constants, by name, and whether its scale warps wait
-    for the other set's stages too (passed) and its load warps, before they
-    leave, for the last stages to be released (drain)."""
+    """The kernel's integer constants, by name; which barrier its scale warps wait
+    at for a stage (scales_wait), and whether its load warps wait for the last
+    stages to be released before they leave (drain)."""
     c, text = {}, open(SOURCE).read()
     for name, value in re.findall(r"^constexpr int (k\w+) = ([^;]+);", text, re.M):
         c[name] = eval(value.replace("/", "//"), {}, c)
     loads = text[text.index("if (warp == 0) {"):text.index("} else if (warp < 7) {")]
-    scales = text[text.index("auto fill = "):text.index("auto pass = ")]
-    c["passed"] = scales.count("wait(sh, &sh->empty[") == 2
     c["drain"] = "wait(sh, &sh->empty[q]" in loads
+    scales = text[text.index("auto fill = "):text.index("auto pass = ")]
+    c["scales_wait"], = re.findall(r"wait\(sh, &sh->(\w+)\[s\]", scales)
+    assert ("arrive(&sh->passed[s])" in loads) == (c["scales_wait"] == "passed")
     return c
 
 
@@ -82,6 +83,7 @@ def run(c, tiles, stages, seed, ring=0):
         return [Bar("%s[%d] of CTA %d" % (name, i, r), count) for i in range(n)]
 
     cta = [dict(full=bars(r, "full", c["kFullArrivals"], S), empty=bars(r, "empty", 1, S),
+                passed=bars(r, "passed", 1, S),
                 acc_full=bars(r, "acc_full", 1, 2),
                 acc_empty=bars(r, "acc_empty", c["kAccReaders"], 2),
                 tile_full=bars(r, "tile_full", 1, 2),
@@ -124,6 +126,7 @@ def run(c, tiles, stages, seed, ring=0):
             yield from take_tile(r, i)
             for _ in range(stages):
                 yield cta[r]["empty"][s], phase ^ 1
+                cta[r]["passed"][s].arrive()
                 yield rnd.random()
                 if r == 0:
                     lead["full"][s].arrive(tx=2)
@@ -181,14 +184,13 @@ def run(c, tiles, stages, seed, ring=0):
                     raise Fault("scales of another chunk")
                 yield rnd.random() * 3
                 cta[r]["box_empty"][q % ring].arrive()
-            for h in range(here):
-                yield cta[r]["empty"][pos[0]], pos[1] ^ 1
+            for _ in range(here):
+                if c["scales_wait"] == "passed":
+                    yield cta[r]["passed"][pos[0]], pos[1]
+                else:
+                    yield cta[r]["empty"][pos[0]], pos[1] ^ 1
                 yield rnd.random() * rnd.choice((1, 1, 20))
                 put(r, pos[0], "scales%d" % role, pos[2])
-                if h == here - 1 and c["passed"] and q + 1 < tiles * chunks:
-                    for n in range(1, 1 + min(wide, stages - (q + 1) % chunks * wide)):
-                        wrap = pos[0] + n >= S
-                        yield cta[r]["empty"][pos[0] + n - S * wrap], pos[1] ^ 1 ^ wrap
                 lead["full"][pos[0]].arrive()
                 skip(1)
             yield from load()

@@ -29,21 +29,25 @@ def any_fault(shapes, seeds=12, **kw):
     return found - {None}
 
 
-def test_finds_waits_left_out():
-    """A scale warp that passes over the other set's stages without waiting for
-    them relies on the releases' order, which nothing promises."""
-    assert any_fault([(5, 14), (20, 3)], passed=False) & {"operand overwritten",
-                                                          "operand of another stage"}
+def test_finds_waits_that_rely_on_the_releases_order():
+    """A scale warp that waits for its own stages' releases sees one phase of a
+    barrier in two or three, and relies on releases to arrive in order."""
+    assert any_fault([(5, 14), (20, 3)], scales_wait="empty") & {"operand overwritten",
+                                                                 "operand of another stage"}
+
+
+def test_finds_a_stage_ring_too_short_for_the_turns():
+    shapes = [(5, 14), (20, 3)]
+    assert any_fault(shapes, kStages=2) & {"operand overwritten", "operand of another stage"}
+    assert not any_fault(shapes, kStages=3)
 
 
 def test_finds_a_shared_ring_of_boxes():
-    """Two sets that share three boxes and do not wait for each other's stages:
-    a set takes the parity of a use that the other set has still to finish for
-    its own."""
+    """Two sets that share three boxes: a set takes the parity of a use that
+    the other set has still to finish for its own."""
     shapes = [(5, 14), (38, 6)]
-    assert "scales of another chunk" in any_fault(shapes, ring=3, passed=False)
-    # two boxes are one for each set
-    assert "scales of another chunk" not in any_fault(shapes, ring=2, passed=False)
+    assert "scales of another chunk" in any_fault(shapes, ring=3)
+    assert not any_fault(shapes, ring=2)     # two boxes are one for each set
 
 
 @pytest.mark.parametrize("name", ["kFullArrivals", "kAccReaders"])
