@@ -31,8 +31,8 @@ struct GatedArgs {
   int R, EB, NvS, F8;
 };
 
-// Through exp(-|g|), which cannot overflow: below -88 the result is a small
-// number, not zero.  The denominator is in [1, 2].
+// Through exp(-|g|), which cannot overflow; for g below -87 it is a subnormal,
+// and zero from about -104 on.  The denominator is in [1, 2].
 __device__ __forceinline__ float sigmoid(float g) {
   const float e = __expf(-fabsf(g));
   return __fdividef(g < 0.0f ? e : 1.0f, 1.0f + e);

@@ -39,11 +39,11 @@
  *     scratch and status word, the plan's arrays and the optional zero-copy
  *     buffers behind moonep_hidden_view / moonep_weight_view.
  *   - One context plans one batch at a time: its planner scratch (counters,
- *     per-rank totals) is shared by its moonep_plan calls, and moonep_route's
- *     scratch by its moonep_route calls, so two of either
- *     must not overlap on the GPU (issue them on one stream, or order the
- *     streams); use one context per concurrent stream.  The copy entry points
- *     keep no state between calls and may overlap freely.
+ *     per-rank totals) is shared by its moonep_plan calls, and its router
+ *     scratch by its moonep_route calls, so two plans, or two routes, must not
+ *     overlap on the GPU (issue them on one stream, or order the streams); use
+ *     one context per concurrent stream.  A plan and a route may overlap.  The
+ *     other entry points keep no state between calls and may overlap freely.
  *   - Kernels are launched with programmatic dependent launch: each waits
  *     for the previous kernel on its stream before touching memory, so
  *     stream order is kept as with plain launches.
@@ -396,9 +396,9 @@ int moonep_reduce_redundant_grad(moonep_ctx *ctx, const moonep_comm_plan *plan,
  *   MOONEP_SCOPE_GLOBAL  a sum_e (E c[e]/(K T)) (P[e]/T), summed over ranks
  *   loss [1] fp32, coef [R, E] fp32: the factor of P[r, e] in the loss, which
  *           moonep_route_backward reads (both given, or both NULL)
- * Needs K <= E.  Uses the context's scratch: the rule of one batch at a time
- * covers moonep_route and moonep_plan together.  Results do not depend on
- * scheduling (sums in a fixed order). */
+ * Needs K <= E.  Uses the context's router scratch: two moonep_route calls of
+ * one context must not overlap.  Results do not depend on scheduling (sums in a
+ * fixed order). */
 #define MOONEP_SCORE_SOFTMAX 0
 #define MOONEP_SCORE_SIGMOID 1
 #define MOONEP_SCOPE_RANK 0
@@ -453,6 +453,7 @@ int moonep_dequantize_mx(moonep_ctx *ctx, const uint8_t *packed,
  *   a_scales     R*NvS rows of Kd/32 bytes, scale_row_bytes apart
  *   w, w_scales  dense [E + R*B, N, Kd/2] (16-byte aligned), [E + R*B, N, Kd/32]
  *   out          [R*NvS, N], 16-byte aligned; other rows are not written
+ *                (their codes may be read, as part of a tile, and never count)
  * N % 8 == 0, Kd % 32 == 0.  Runs on pairs of SMs: at least one pair, however
  * few SMs the context may use. */
 int moonep_expert_product(moonep_ctx *ctx, const int32_t *cu_seqlens,
