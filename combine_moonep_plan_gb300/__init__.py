@@ -16,7 +16,8 @@ def load_library():
 
 
 def __getattr__(name):
-    if name in ("Buffer", "CommPlan", "BufferPool", "Route", "GatedCheckpoint"):
+    if name in ("Buffer", "CommPlan", "BufferPool", "Route", "GatedCheckpoint",
+                "AdamWState"):
         from . import api
         return getattr(api, name)
     raise AttributeError(name)

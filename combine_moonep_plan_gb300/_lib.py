@@ -37,7 +37,8 @@ EXPORTS = (
     "moonep_plan_noalloc", "moonep_prepare", "moonep_plan_rank", "moonep_dispatch_rank",
     "moonep_combine_rank", "moonep_route", "moonep_route_backward", "moonep_quantize_mx",
     "moonep_dequantize_mx", "moonep_expert_product", "moonep_gated_act",
-    "moonep_gated_act_backward",
+    "moonep_gated_act_backward", "moonep_grad_norm_workspace", "moonep_grad_norm",
+    "moonep_adamw", "moonep_adamw_moments",
 )
 
 
@@ -58,6 +59,15 @@ class MoonepCommPlan(ctypes.Structure):
                 ("E", ctypes.c_int), ("B", ctypes.c_int), ("K", ctypes.c_int),
                 ("S", ctypes.c_int), ("NvS", ctypes.c_int), ("NvS_padded", ctypes.c_int),
                 ("flags", ctypes.c_int), ("internal_bytes", ctypes.c_size_t)]
+
+
+class MoonepAdamwConfig(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double),
+                ("lr_dev", ctypes.c_void_p), ("step_dev", ctypes.c_void_p),
+                ("norm", ctypes.c_void_p), ("max_norm", ctypes.c_float), ("step", ctypes.c_int32),
+                ("seed", ctypes.c_uint32), ("seeded", ctypes.c_int), ("bits", ctypes.c_int),
+                ("p_bf16", ctypes.c_int), ("g_bf16", ctypes.c_int)]
 
 
 class MoonepError(RuntimeError):
@@ -83,6 +93,7 @@ def load(path: str = LIB_PATH):
     cfgp = ctypes.POINTER(MoonepConfig)
     planp = ctypes.POINTER(MoonepCommPlan)
     i32p = ctypes.POINTER(ctypes.c_int32)
+    i64p, vpp = ctypes.POINTER(i64), ctypes.POINTER(vp)
     sig = {
         "moonep_query_sizes": (ci, [cfgp, ctypes.POINTER(ci), ctypes.POINTER(ci),
                                     ctypes.POINTER(ctypes.c_size_t)]),
@@ -121,6 +132,10 @@ def load(path: str = LIB_PATH):
         "moonep_expert_product": (ci, [vp, vp, vp, i64, vp, i64, vp, vp, ci, ci, ci, vp, vp]),
         "moonep_gated_act": (ci, [vp] * 5 + [ci] + [vp] * 6),
         "moonep_gated_act_backward": (ci, [vp] * 8 + [ci] + [vp] * 4),
+        "moonep_grad_norm_workspace": (ctypes.c_size_t, [vp]),
+        "moonep_grad_norm": (ci, [vp, ci, vpp, i64p, ci, vp, vp, vp]),
+        "moonep_adamw": (ci, [vp, ctypes.POINTER(MoonepAdamwConfig), ci, i64p] + [vpp] * 7 + [vp]),
+        "moonep_adamw_moments": (ci, [vp, i64] + [vp] * 4 + [ci] + [vp] * 3),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)

@@ -77,6 +77,24 @@ def _one_of(t, name, dtypes):
     return t.dtype
 
 
+def _check_list(tensors, name, dtypes, sizes):
+    """Contiguous CUDA tensors of one type out of `dtypes` (returned), of `sizes`
+    elements where given."""
+    if sizes is not None and len(tensors) != len(sizes):
+        raise ValueError(f"{name}: expected {len(sizes)} tensors, got {len(tensors)}")
+    dtype = _one_of(tensors[0], f"{name}[0]", dtypes) if tensors else dtypes[0]
+    for t in tensors:
+        if t.dtype is not dtype:
+            raise TypeError(f"{name}: expected all {dtype}, got {t.dtype}")
+        if not (t.is_cuda and t.is_contiguous()):
+            raise ValueError(f"{name}: must be contiguous CUDA tensors")
+    if sizes is not None:
+        for t, n in zip(tensors, sizes):
+            if t.numel() != n:
+                raise ValueError(f"{name}: expected a tensor of {n} elements, got {t.numel()}")
+    return dtype
+
+
 def _check_rows(t, name, rows, cols):
     """A uint8 [rows, cols] tensor whose rows may lie apart: (address, row
     distance in bytes)."""
@@ -190,6 +208,67 @@ class GatedCheckpoint:
         views = tuple(self._store[at[k]:at[k + 1]].view(rows, F if k < 2 else F // 32)
                       for k in range(4))
         return views[i]
+
+
+class AdamWState:
+    """AdamW's moments of a list of tensors [Buffer.adamw_state].
+
+    One allocation per kind, every tensor's part starting on a multiple of 32
+    elements; `tensors` is (m, v) in fp32, or with bits=8 (m codes, m scales,
+    v codes, v scales) in uint8, a scale for every 32 codes.  All zero is the
+    state before the first step.  `sizes` are the tensors' elements and
+    `offsets` the places of their first ones."""
+
+    __slots__ = ("tensors", "bits", "sizes", "offsets", "total", "_buffer", "_c_sizes", "_c_ptrs",
+                 "_base")
+
+    def __init__(self, buffer: "Buffer", sizes, bits: int, device):
+        self.bits, self.sizes, self._buffer = bits, tuple(sizes), buffer
+        self.offsets, at = [], 0
+        for n in self.sizes:
+            self.offsets.append(at)
+            at += -(-n // 32) * 32
+        self.total = at
+        if bits == 32:
+            self.tensors = tuple(torch.zeros(at, device=device) for _ in range(2))
+        else:
+            self.tensors = tuple(torch.zeros(at // d, dtype=torch.uint8, device=device)
+                                 for d in (1, 32, 1, 32))
+        self._c_sizes = (ctypes.c_int64 * len(self.sizes))(*self.sizes)
+        self._base = None
+
+    def _pointers(self):
+        """The C arrays of every tensor's moments: m, v, m scales, v scales."""
+        base = tuple(t.data_ptr() for t in self.tensors)
+        if base != self._base:
+            if self.bits == 32:
+                m, v = (_lib.ptr_array([b + 4 * o for o in self.offsets]) for b in base)
+                self._c_ptrs = (m, v, None, None)
+            else:
+                m, ms, v, vs = (_lib.ptr_array([b + o // d for o in self.offsets])
+                                for b, d in zip(base, (1, 32, 1, 32)))
+                self._c_ptrs = (m, v, ms, vs)
+            self._base = base
+        return self._c_ptrs
+
+    def moments(self, dtype: torch.dtype = torch.bfloat16):
+        """(m, v), flat: the fp32 moments themselves, or in `dtype` (bf16 or
+        fp32) the values that the 8-bit ones stand for."""
+        if self.bits == 32:
+            return self.tensors
+        if dtype not in _FLOATS:
+            raise TypeError(f"dtype: expected one of {_FLOATS}, got {dtype}")
+        m8, ms, v8, vs = self.tensors
+        m, v = (torch.empty(self.total, dtype=dtype, device=m8.device) for _ in range(2))
+        check(_lib.load().moonep_adamw_moments(
+            self._buffer._ctx, self.total, m8.data_ptr(), ms.data_ptr(), v8.data_ptr(),
+            vs.data_ptr(), dtype == torch.float32, m.data_ptr(), v.data_ptr(), _stream()),
+            "moonep_adamw_moments")
+        return m, v
+
+    def split(self, flat: torch.Tensor):
+        """The tensors' parts of a flat tensor of moments, as views."""
+        return [flat[o:o + n] for o, n in zip(self.offsets, self.sizes)]
 
 
 class Buffer:
@@ -657,6 +736,92 @@ class Buffer:
             self._ctx, self._segments(cu_seqlens), *cp, dp, wp, F, gp, up_p, dwp, _stream()),
             "moonep_gated_act_backward")
         return d_gate, d_up, d_w
+
+    # --------------------------------------------------------- optimizer
+    def adamw_state(self, params, bits: int = 32) -> AdamWState:
+        """Zero moments for `params`, in 32 bits or in 8 (blocks of 32 values
+        under one power of two)."""
+        params = list(params)
+        if bits not in (32, 8):
+            raise ValueError(f"bits: expected 32 or 8, got {bits}")
+        _check_list(params, "params", _FLOATS, None)
+        device = params[0].device if params else torch.device("cuda", torch.cuda.current_device())
+        return AdamWState(self, [t.numel() for t in params], bits, device)
+
+    def grad_norm(self, grads, out: torch.Tensor | None = None) -> torch.Tensor:
+        """The 2-norm [1] fp32 of all tensors in `grads` together (all fp32 or
+        all bf16), summed in a fixed order."""
+        grads = list(grads)
+        dtype = _check_list(grads, "grads", _FLOATS, None)
+        lib = _lib.load()
+        n = lib.moonep_grad_norm_workspace(self._ctx)
+        dev = grads[0].device if grads else torch.device("cuda", torch.cuda.current_device())
+        if out is None:
+            out = torch.empty(1, dtype=torch.float32, device=dev)
+        op = _check_tensor(out, "norm", torch.float32, (1,))
+        work = torch.empty(n // 8, dtype=torch.float64, device=dev)
+        check(lib.moonep_grad_norm(
+            self._ctx, len(grads), _lib.ptr_array([t.data_ptr() for t in grads]),
+            (ctypes.c_int64 * len(grads))(*[t.numel() for t in grads]), dtype == torch.bfloat16,
+            work.data_ptr(), op, _stream()), "moonep_grad_norm")
+        return out
+
+    def adamw(self, params, grads, state: AdamWState, lr, step, betas=(0.9, 0.999),
+              eps: float = 1e-8, weight_decay: float = 0.01, norm: torch.Tensor | None = None,
+              max_norm: float | None = None, seed: int | None = None, weights=None) -> None:
+        """One AdamW step, in place on `params` (all fp32 or all bf16) and on
+        their `state`; grads: matching tensors (all fp32 or all bf16).
+          lr, step   host numbers, or tensors [1] (fp32, int32) in device memory,
+                     which a captured step reads anew at every replay; the first
+                     step is 1
+          norm       grad_norm's: gradients are scaled by min(1, max_norm/norm),
+                     and a norm that is not finite leaves everything as it was
+          seed       moments in 8 bits and bf16 parameters are rounded at random,
+                     right on average (None: to nearest)
+          weights    for fp32 params: bf16 tensors (or None) that receive the
+                     rounded parameters, e.g. the experts' rows W[:E]"""
+        params, grads = list(params), list(grads)
+        pt = _check_list(params, "params", _FLOATS, state.sizes)
+        gt = _check_list(grads, "grads", _FLOATS, state.sizes)
+        wp = None
+        if weights is not None:
+            if pt != torch.float32:
+                raise TypeError("weights: only beside fp32 params")
+            weights = list(weights)
+            if len(weights) != len(params):
+                raise ValueError(f"weights: expected {len(params)} tensors")
+            for t, n in zip(weights, state.sizes):
+                if t is not None:
+                    _check_list([t], "weights", (torch.bfloat16,), (n,))
+            wp = _lib.ptr_array([0 if t is None else t.data_ptr() for t in weights])
+        pp = [t.data_ptr() for t in params]
+        if len(set(pp)) < len(pp) and len({p for p, n in zip(pp, state.sizes) if n}) < \
+                sum(n > 0 for n in state.sizes):
+            raise ValueError("params: a tensor is given twice")
+        if (norm is None) != (max_norm is None):
+            raise ValueError("norm and max_norm go together")
+        cfg = _lib.MoonepAdamwConfig(
+            beta1=betas[0], beta2=betas[1], eps=eps, weight_decay=weight_decay, bits=state.bits,
+            p_bf16=pt == torch.bfloat16, g_bf16=gt == torch.bfloat16, seeded=seed is not None,
+            seed=0 if seed is None else seed & 0xffffffff)
+        if torch.is_tensor(lr):
+            cfg.lr_dev = _check_tensor(lr, "lr", torch.float32, (1,))
+        else:
+            cfg.lr = lr
+        if torch.is_tensor(step):
+            cfg.step_dev = _check_tensor(step, "step", torch.int32, (1,))
+        else:
+            if not 1 <= step < 1 << 31:
+                raise ValueError(f"step: expected 1 or more, got {step}")
+            cfg.step = step
+        if norm is not None:
+            cfg.norm = _check_tensor(norm, "norm", torch.float32, (1,))
+            cfg.max_norm = max_norm
+        m, v, ms, vs = state._pointers()
+        check(_lib.load().moonep_adamw(
+            self._ctx, ctypes.byref(cfg), len(params), state._c_sizes,
+            _lib.ptr_array(pp), _lib.ptr_array([t.data_ptr() for t in grads]), m, v, ms, vs, wp,
+            _stream()), "moonep_adamw")
 
     # ------------------------------------------------- rank-local forms
     # The per-rank shape of the path when each EP rank is its own GPU: one

@@ -5,6 +5,7 @@
 // everything, idempotently; MoonEPCommPlan.clone() deep-copies the plan;
 // Buffer.hidden_nvsh_buffer_view / router_weight_buffer_view expose rank
 // windows of the persistent buffers without copying.
+#include <float.h>
 #include <stdlib.h>
 #include <string.h>
 
@@ -585,6 +586,94 @@ int moonep_gated_act_backward(moonep_ctx *ctx, const int32_t *cu_seqlens, const 
     return MOONEP_ERR_INVALID_ARG;
   return launch_gated_backward(ctx, cu_seqlens, gate8, up8, gate_scales, up_scales, d_act, w_nvs,
                                F, d_gate, d_up, d_w_nvs, (cudaStream_t)stream);
+}
+
+size_t moonep_grad_norm_workspace(const moonep_ctx *ctx) {
+  return check_ctx(ctx) ? 0 : (size_t)norm_blocks(ctx) * sizeof(double);
+}
+
+// Host arrays of n tensors: sizes in range, and pointers, aligned to `align`,
+// where there are elements (`null_ok`: or none).
+static bool sizes_ok(int n, const int64_t *sizes) {
+  if (n < 0 || (n > 0 && !sizes)) return false;
+  for (int k = 0; k < n; k++)
+    if (sizes[k] < 0 || sizes[k] > ((int64_t)1 << 41)) return false;
+  return true;
+}
+static bool tensors_ok(int n, const int64_t *sizes, const void *pointers, uintptr_t align,
+                       bool null_ok = false) {
+  const void *const *p = (const void *const *)pointers;
+  if (n > 0 && !p) return false;
+  for (int k = 0; k < n; k++)
+    if (sizes[k] > 0 && ((!p[k] && !null_ok) || ((uintptr_t)p[k] & (align - 1)))) return false;
+  return true;
+}
+
+int moonep_grad_norm(moonep_ctx *ctx, int n_tensors, const void *const *g, const int64_t *sizes,
+                     int g_bf16, void *workspace, float *norm, void *stream) {
+  int st = check_ctx(ctx);
+  if (st) return st;
+  if (!sizes_ok(n_tensors, sizes) || !tensors_ok(n_tensors, sizes, g, g_bf16 ? 2 : 4) ||
+      !workspace || ((uintptr_t)workspace & 7) || !norm || !aligned4(norm))
+    return MOONEP_ERR_INVALID_ARG;
+  AdamwCall c{};
+  c.count = n_tensors;
+  c.g = g;
+  c.sizes = sizes;
+  c.g_bf16 = g_bf16 != 0;
+  return launch_grad_norm(ctx, c, (double *)workspace, norm, (cudaStream_t)stream);
+}
+
+int moonep_adamw(moonep_ctx *ctx, const moonep_adamw_config *h, int n_tensors,
+                 const int64_t *sizes, void *const *p, const void *const *g, void *const *m,
+                 void *const *v, uint8_t *const *ms, uint8_t *const *vs, uint16_t *const *w,
+                 void *stream) {
+  int st = check_ctx(ctx);
+  if (st) return st;
+  if (!h || (h->bits != 32 && h->bits != 8) || !sizes_ok(n_tensors, sizes))
+    return MOONEP_ERR_INVALID_ARG;
+  // written so that a NaN is refused
+  if (!(h->beta1 >= 0 && h->beta1 < 1 && h->beta2 >= 0 && h->beta2 < 1 && h->eps > 0 &&
+        h->eps <= FLT_MAX && (float)h->eps > 0 && h->lr - h->lr == 0 &&
+        h->weight_decay - h->weight_decay == 0) ||
+      (!h->step_dev && h->step < 1) || (h->norm && !(h->max_norm > 0)) ||
+      !aligned4(h->norm) || !aligned4(h->lr_dev) || !aligned4(h->step_dev))
+    return MOONEP_ERR_INVALID_ARG;
+  if ((w && h->p_bf16) || !tensors_ok(n_tensors, sizes, p, h->p_bf16 ? 2 : 4) ||
+      !tensors_ok(n_tensors, sizes, g, h->g_bf16 ? 2 : 4) ||
+      !tensors_ok(n_tensors, sizes, m, 16) || !tensors_ok(n_tensors, sizes, v, 16) ||
+      (w && !tensors_ok(n_tensors, sizes, w, 2, true)))
+    return MOONEP_ERR_INVALID_ARG;
+  if (h->bits == 8 &&
+      (!tensors_ok(n_tensors, sizes, ms, 1) || !tensors_ok(n_tensors, sizes, vs, 1)))
+    return MOONEP_ERR_INVALID_ARG;
+  AdamwCall c{};
+  c.count = n_tensors;
+  c.p_bf16 = h->p_bf16 != 0;
+  c.g_bf16 = h->g_bf16 != 0;
+  c.bits = h->bits;
+  c.p = p;
+  c.g = g;
+  c.sizes = sizes;
+  c.m = m;
+  c.v = v;
+  c.ms = h->bits == 8 ? ms : nullptr;
+  c.vs = h->bits == 8 ? vs : nullptr;
+  c.w = w;
+  return launch_adamw(ctx, c, *h, (cudaStream_t)stream);
+}
+
+int moonep_adamw_moments(moonep_ctx *ctx, int64_t n, const uint8_t *m8, const uint8_t *ms,
+                         const uint8_t *v8, const uint8_t *vs, int fp32, void *m, void *v,
+                         void *stream) {
+  int st = check_ctx(ctx);
+  if (st) return st;
+  if (n < 0 || n % 32 != 0) return MOONEP_ERR_INVALID_ARG;
+  if (n == 0) return MOONEP_OK;
+  if (!m8 || !ms || !v8 || !vs || !m || !v || !aligned16(m8) || !aligned16(v8) || !aligned16(m) ||
+      !aligned16(v))
+    return MOONEP_ERR_INVALID_ARG;
+  return launch_adamw_moments(ctx, n, m8, ms, v8, vs, fp32 != 0, m, v, (cudaStream_t)stream);
 }
 
 void *moonep_hidden_view(moonep_ctx *ctx, int rank) {

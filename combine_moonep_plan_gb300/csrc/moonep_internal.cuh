@@ -183,6 +183,24 @@ int launch_gated_backward(moonep_ctx *ctx, const int32_t *cu, const uint8_t *g8,
                           const uint8_t *gs, const uint8_t *us, const uint16_t *d_act,
                           const float *w, int F, uint16_t *d_gate, uint16_t *d_up, float *d_w,
                           cudaStream_t st);
+// The optimizer: tensors of one call (host arrays of device pointers).
+struct AdamwCall {
+  int count, p_bf16, g_bf16, bits;
+  void *const *p;
+  const void *const *g;
+  const int64_t *sizes;
+  void *const *m, *const *v;
+  uint8_t *const *ms, *const *vs;  // 8 bits
+  uint16_t *const *w;              // or null
+};
+int norm_blocks(const moonep_ctx *ctx);  // most blocks of the norm's sums
+int launch_grad_norm(moonep_ctx *ctx, const AdamwCall &c, double *part, float *norm,
+                     cudaStream_t st);
+int launch_adamw(moonep_ctx *ctx, const AdamwCall &c, const moonep_adamw_config &h,
+                 cudaStream_t st);
+int launch_adamw_moments(moonep_ctx *ctx, int64_t n, const uint8_t *m8, const uint8_t *ms,
+                         const uint8_t *v8, const uint8_t *vs, int fp32, void *m, void *v,
+                         cudaStream_t st);
 // Raise a kernel's dynamic shared memory limit to at least `bytes` (never
 // lower it: contexts of different shapes, on different host threads, share the
 // kernels).

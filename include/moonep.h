@@ -488,6 +488,67 @@ int moonep_gated_act_backward(moonep_ctx *ctx, const int32_t *cu_seqlens,
                               const float *w_nvs, int F, uint16_t *d_gate,
                               uint16_t *d_up, float *d_w_nvs, void *stream);
 
+/* The norm of many gradients: norm[0] = sqrt(sum over all tensors of g^2), fp32
+ * in device memory.  g is a host array of n_tensors device pointers (fp32, or
+ * bf16 when g_bf16; any element alignment), sizes their elements.  Squares are
+ * taken in fp32 (below 2^-126 they lose bits, from 2^128 on they are
+ * infinite), sums of eight in fp32 and the rest in 64 bits, in a fixed order.
+ * workspace: moonep_grad_norm_workspace(ctx) bytes of device memory, 8-byte
+ * aligned, the call's own until it has run. */
+size_t moonep_grad_norm_workspace(const moonep_ctx *ctx);
+int moonep_grad_norm(moonep_ctx *ctx, int n_tensors, const void *const *g,
+                     const int64_t *sizes, int g_bf16, void *workspace,
+                     float *norm, void *stream);
+
+/* One AdamW step over many tensors, in place:
+ *   g' = g min(1, max_norm / norm[0])        (g without a norm)
+ *   m = beta1 m + (1 - beta1) g'    v = beta2 v + (1 - beta2) g'^2
+ *   p = p (1 - lr wd) - lr / (1 - beta1^step) m /
+ *                       (sqrt(v) / sqrt(1 - beta2^step) + eps)
+ * in fp32.  When norm[0] is not finite the call changes nothing.
+ *   p, g     n_tensors host arrays of device pointers, fp32 or bf16 (one type
+ *            per call each), any element alignment; sizes: elements, >= 0
+ *   m, v     bits 32: fp32; bits 8: codes, uint8, with ms, vs their scales;
+ *            16-byte aligned.  Of a tensor of n elements they hold n rounded up
+ *            to a multiple of 32 (8 bits: a scale byte for every 32), the ones
+ *            past n zero; a new state is all zero
+ *   w        NULL, or per tensor NULL or a bf16 tensor that receives p rounded
+ *            to nearest even (fp32 p only)
+ * Moments in 8 bits: every 32 values share the power 2^(s - 127), the smallest
+ * (s >= 0) under which none saturates; m is E4M3, v code c stands for c/8
+ * (c < 8) or (1 + (c & 7)/8) 2^(c/8 - 1).  A block with a NaN or an infinity gets
+ * the scale 255 and reads back as NaN.  Values round to nearest even; when
+ * seeded, up with the probability that makes them right on average, and so does
+ * a bf16 p, by 16 bits of a hash of (seed, step, tensor's place, element).  A v
+ * above zero keeps at least code 1.
+ *   lr_dev, step_dev   device scalars used in place of lr and step when given
+ *            (a captured step then goes on from replay to replay)
+ * 0 <= beta < 1, eps > 0, step >= 1, and max_norm > 0 with a norm. */
+typedef struct moonep_adamw_config {
+  double lr, beta1, beta2, eps, weight_decay;
+  const float *lr_dev;
+  const int32_t *step_dev;
+  const float *norm;
+  float max_norm;
+  int32_t step;
+  uint32_t seed;
+  int seeded;
+  int bits;   /* 32 or 8 */
+  int p_bf16, g_bf16;
+} moonep_adamw_config;
+int moonep_adamw(moonep_ctx *ctx, const moonep_adamw_config *config,
+                 int n_tensors, const int64_t *sizes, void *const *p,
+                 const void *const *g, void *const *m, void *const *v,
+                 uint8_t *const *ms, uint8_t *const *vs, uint16_t *const *w,
+                 void *stream);
+
+/* The values of n (a multiple of 32) moments in 8 bits, bf16 (fp32 when fp32);
+ * every pointer 16-byte aligned but the scales'. */
+int moonep_adamw_moments(moonep_ctx *ctx, int64_t n, const uint8_t *m8,
+                         const uint8_t *ms, const uint8_t *v8,
+                         const uint8_t *vs, int fp32, void *m, void *v,
+                         void *stream);
+
 /* Zero-copy aliases [API, Buffer.hidden_nvsh_buffer_view and
  * router_weight_buffer_view]: device address of rank `rank`'s [NvS, H] bf16
  * window (row rank*NvS of the context's hidden buffer) and of its [NvS] fp32
