@@ -111,6 +111,21 @@ def _check_rows(t, name, rows, cols):
     return t.data_ptr(), max(t.stride(0), cols) if rows > 1 else cols
 
 
+def _check_bf16_rows(t, name, rows):
+    """A bf16 [rows, cols] tensor whose rows may lie apart: (address, row
+    distance in bytes, cols)."""
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name}: expected torch.bfloat16, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a CUDA tensor")
+    if t.dim() != 2 or t.shape[0] != rows:
+        raise ValueError(f"{name}: expected {rows} rows, got shape {tuple(t.shape)}")
+    cols = t.shape[1]
+    if cols > 1 and t.stride(1) != 1 or rows > 1 and t.stride(0) < cols:
+        raise ValueError(f"{name}: rows must be contiguous and not overlap")
+    return t.data_ptr(), 2 * (max(t.stride(0), cols) if rows > 1 else cols), cols
+
+
 class CommPlan:
     """A communication plan [MoonEPCommPlan]: device arrays owned by libmoonep."""
 
@@ -669,6 +684,33 @@ class Buffer:
             self._ctx, self._segments(cu_seqlens), ap, lda, sap, lds, wp, swp, N, Kd,
             out.dtype == torch.float32, op, _stream()), "moonep_expert_product")
         return out
+
+    def expert_weight_grad(self, rows: torch.Tensor, d_out: torch.Tensor,
+                           cu_seqlens: torch.Tensor, out: tuple | None = None,
+                           accumulate: bool = False):
+        """Gradients of the experts' weights [N, Kd] from the rows that a product
+        read, `rows` [R*NvS, Kd] bf16, and its outputs' gradient, `d_out`
+        [R*NvS, N] bf16 (their rows may lie apart, by a multiple of 16 bytes):
+        (grad [E, N, Kd], slots [R, B, N, Kd]) fp32, as reduce_grad takes them.
+        Home experts without rows get zeros, slots without rows are not touched
+        (new ones are zero).  accumulate=True adds to both tensors of `out`."""
+        n_rows = self.R * self.NvS
+        xp, ldx, Kd = _check_bf16_rows(rows, "rows", n_rows)
+        dp, ldd, N = _check_bf16_rows(d_out, "d_out", n_rows)
+        if N % 8 or Kd % 8:
+            raise ValueError("rows, d_out: N and Kd must be multiples of 8")
+        if out is None:
+            if accumulate:
+                raise ValueError("accumulate needs out: the tensors to add to")
+            out = (torch.empty((self.E, N, Kd), dtype=torch.float32, device=rows.device),
+                   torch.zeros((self.R, self.B, N, Kd), dtype=torch.float32, device=rows.device))
+        grad, slots = out
+        gp = _check_tensor(grad, "grad", torch.float32, (self.E, N, Kd))
+        sp = _check_tensor(slots, "slots", torch.float32, (self.R, self.B, N, Kd))
+        check(_lib.load().moonep_expert_weight_grad(
+            self._ctx, self._segments(cu_seqlens), xp, ldx, dp, ldd, N, Kd, bool(accumulate), gp,
+            sp, _stream()), "moonep_expert_weight_grad")
+        return grad, slots
 
     def gated_act(self, gate: torch.Tensor, up: torch.Tensor, cu_seqlens: torch.Tensor,
                   route_weights_nvs: torch.Tensor | None = None, checkpoint: bool = False,

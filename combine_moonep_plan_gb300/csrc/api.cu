@@ -116,6 +116,7 @@ int moonep_ctx_create(const moonep_config *cfg, int alloc_views, moonep_ctx **ou
   ctx->blocks_expand = occupancy_dedup(false);
   ctx->blocks_fold = occupancy_dedup(true);
   ctx->product_clusters = product_clusters(ctx->sms);
+  ctx->wgrad_clusters = wgrad_clusters(ctx->sms);
   const size_t hist =
       (size_t)plan_scratch_words(c.R, c.E, ctx->C, c.K, ctx->sms_device) * sizeof(int32_t);
   const size_t ord = (size_t)c.R * ctx->C * sizeof(int32_t);
@@ -550,6 +551,34 @@ int moonep_expert_product(moonep_ctx *ctx, const int32_t *cu_seqlens, const uint
     return MOONEP_ERR_INVALID_ARG;
   return launch_product(ctx, cu_seqlens, a, row_bytes, a_scales, scale_row_bytes, w, w_scales, N,
                         Kd, out, out_fp32 != 0, (cudaStream_t)stream);
+}
+
+int moonep_expert_weight_grad(moonep_ctx *ctx, const int32_t *cu_seqlens, const uint16_t *x,
+                              int64_t x_row_bytes, const uint16_t *d, int64_t d_row_bytes, int N,
+                              int Kd, int accumulate, float *grad, float *slots, void *stream) {
+  int st = check_ctx(ctx);
+  if (st) return st;
+  const int64_t groups = (int64_t)ctx->cfg.E + (int64_t)ctx->cfg.R * ctx->cfg.B;
+  if (N < 0 || N % 8 != 0 || Kd < 0 || Kd % 8 != 0 || N > 1 << 20 || Kd > 1 << 20 ||
+      groups * ((N + 255) / 256) * ((Kd + 255) / 256) > INT32_MAX - (1 << 20))
+    return MOONEP_ERR_INVALID_ARG;
+  if (N == 0 || Kd == 0) return MOONEP_OK;
+  const bool extra = ctx->cfg.B > 0;
+  if (!grad || !aligned16(grad) || (extra && (!slots || !aligned16(slots))))
+    return MOONEP_ERR_INVALID_ARG;
+  if (!cu_seqlens || !aligned4(cu_seqlens) || x_row_bytes < 2 * (int64_t)Kd ||
+      x_row_bytes % 16 != 0 || d_row_bytes < 2 * (int64_t)N || d_row_bytes % 16 != 0 ||
+      x_row_bytes >= (int64_t)1 << 40 || d_row_bytes >= (int64_t)1 << 40)
+    return MOONEP_ERR_INVALID_ARG;
+  if (ctx->NvS == 0) {
+    // no rows: nothing to add, and zeros in their place otherwise
+    return accumulate ? MOONEP_OK
+                      : cuda_status(cudaMemsetAsync(grad, 0, (size_t)ctx->cfg.E * N * Kd * 4,
+                                                    (cudaStream_t)stream));
+  }
+  if (!x || !d || !aligned16(x) || !aligned16(d)) return MOONEP_ERR_INVALID_ARG;
+  return launch_wgrad(ctx, cu_seqlens, x, x_row_bytes, d, d_row_bytes, N, Kd, accumulate != 0,
+                      grad, slots, (cudaStream_t)stream);
 }
 
 int moonep_gated_act(moonep_ctx *ctx, const int32_t *cu_seqlens, const uint16_t *gate,

@@ -109,6 +109,7 @@ struct moonep_ctx {
   int32_t *d_route;         // moonep_route's per-block sums (route_scratch_words)
   unsigned long long *d_sync;  // [kSyncWords] the planner's counters (kSync*)
   int product_clusters;        // CTA pairs of the experts' product resident at once
+  int wgrad_clusters;          // and of their weight gradients
   int test_planner_timeout;    // test hook: the planner's arrival wait never completes
   int plan_cluster;            // blocks of the whole-problem planner launched as one
                                // cluster (0: a cooperative launch)
@@ -175,6 +176,11 @@ int product_clusters(int sms);  // CTA pairs resident at once on that many SMs (
 int launch_product(moonep_ctx *ctx, const int32_t *cu, const uint8_t *rows, int64_t lda,
                    const uint8_t *row_scales, int64_t lds, const uint8_t *w,
                    const uint8_t *w_scales, int N, int Kd, void *out, int fp32, cudaStream_t st);
+// The experts' weight gradients.
+int wgrad_clusters(int sms);  // CTA pairs resident at once on that many SMs (0: none)
+int launch_wgrad(moonep_ctx *ctx, const int32_t *cu, const uint16_t *x, int64_t x_pitch,
+                 const uint16_t *d, int64_t d_pitch, int N, int Kd, int add, float *grad,
+                 float *slots, cudaStream_t st);
 // The experts' gated activation.
 int launch_gated(moonep_ctx *ctx, const int32_t *cu, const uint16_t *gate, const uint16_t *up,
                  const float *w, int F, uint16_t *act, uint8_t *g8, uint8_t *u8, uint8_t *gs,

@@ -462,6 +462,29 @@ int moonep_expert_product(moonep_ctx *ctx, const int32_t *cu_seqlens,
                           const uint8_t *w, const uint8_t *w_scales, int N,
                           int Kd, int out_fp32, void *out, void *stream);
 
+/* The experts' weight gradients over the dispatched layout: for every segment,
+ * with g its weight row,
+ *   G[n, k] = sum over its rows of d[row, n] x[row, k]
+ * x the rows that a product with weights [N, Kd] read, d the gradient of what it
+ * gave.  bf16 in, fp32 sums.
+ *   cu_seqlens   device [R, E+B]: the plan's; segments outside [0, NvS) are taken
+ *                as empty and latch MOONEP_ERR_PLAN
+ *   x, d         R*NvS rows of Kd and N bf16 values, x_row_bytes and d_row_bytes
+ *                apart (multiples of 16), 16-byte aligned; rows outside every
+ *                segment may be read and never count, whatever they hold
+ *   grad         [E, N, Kd] fp32: home experts'; all written, zeros for one
+ *                without rows
+ *   slots        [R, B, N, Kd] fp32 (may be NULL when B = 0): the slots', those
+ *                without rows are not touched (moonep_reduce_redundant_grad's Gs)
+ * accumulate: both are added to instead (one addition per element).  N % 8 == 0,
+ * Kd % 8 == 0, each at most 2^20.  Runs on pairs of SMs: at least one pair,
+ * however few SMs the context may use. */
+int moonep_expert_weight_grad(moonep_ctx *ctx, const int32_t *cu_seqlens,
+                              const uint16_t *x, int64_t x_row_bytes,
+                              const uint16_t *d, int64_t d_row_bytes, int N,
+                              int Kd, int accumulate, float *grad,
+                              float *slots, void *stream);
+
 /* The experts' gated activation over the dispatched layout, times the route
  * weight (combine sums unweighted):
  *   act[row, f] = w[row] * gate * sigmoid(gate) * up
