@@ -24,7 +24,9 @@
 //   4-11   epilogue: accumulator (lane = n, TMEM column = k) through swizzled
 //          shared memory, 32 x 32 values per TMA store, or per TMA reduction
 //          where the gradients are added to (one addition per element, so the
-//          order of nothing changes a result)
+//          order of nothing changes a result).  The tensor cores' own sums drop
+//          bits at every addition, 2e-6 of the result over 2000 rows, so they
+//          end after 512 rows and the epilogue adds the parts up in registers
 // Home experts without rows get zeros unless gradients are added to; slots
 // without rows are not touched.  Every wait has a limit of one second, after
 // which the kernel latches MOONEP_ERR_TIMEOUT, drains and returns; every warp
@@ -42,6 +44,7 @@ constexpr int kDeep = 64;                  // rows of a stage
 constexpr int kChunkBytes = kDeep * 128;   // 64 columns of a stage
 constexpr int kSideBytes = 2 * kChunkBytes;
 constexpr int kStageBytes = 2 * kSideBytes;
+constexpr int kPart = 8;                   // stages summed in TMEM at a time
 constexpr int kEpilogueWarps = 8;
 constexpr int kTileReaders = 2 + kEpilogueWarps;  // and the leader's product warp
 constexpr int kEntries = 1024;
@@ -304,10 +307,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         int4 tile;
         if (!(ok = next_tile(sh, i, a.status, &tile))) break;
         const int stages = (tile.w + kDeep - 1) / kDeep;
-        if (stages == 0) continue;
-        const uint32_t d = tmem + (acc & 1) * kSide;
-        if (!(ok = wait(sh, &sh->acc_empty[acc & 1], ((acc >> 1) & 1) ^ 1, a.status))) break;
+        uint32_t d = 0;
         for (int k = 0; k < stages; k++) {
+          const int at = k % kPart;
+          if (at == 0) {
+            d = tmem + (acc & 1) * kSide;
+            if (!(ok = wait(sh, &sh->acc_empty[acc & 1], ((acc >> 1) & 1) ^ 1, a.status))) break;
+          }
           if (!(ok = wait(sh, &sh->full[s], phase, a.status))) break;
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
           const uint32_t base = stage0 + s * kStageBytes;
@@ -317,16 +323,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int q = 0; q < kDeep / 16; q++)
               // 16 rows: two groups of eight, 2 KB
-              if (q < steps) mma(d, da + 128 * q, db + 128 * q, k + q > 0);
+              if (q < steps) mma(d, da + 128 * q, db + 128 * q, at + q > 0);
             commit(&sh->empty[s]);
-            if (k == stages - 1) commit(&sh->acc_full[acc & 1]);
+            if (at == kPart - 1 || k == stages - 1) commit(&sh->acc_full[acc & 1]);
           }
+          if (at == kPart - 1 || k == stages - 1) acc++;
           if (++s == kStages) {
             s = 0;
             phase ^= 1;
           }
         }
-        acc++;
       }
     }
   } else if (warp == 2) {
@@ -369,43 +375,51 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int i = 0; i < mine; i++) {
       int4 tile;
       if (!next_tile(sh, i, a.status, &tile)) break;
-      const bool some = tile.w > 0;
-      if (some && !wait(sh, &sh->acc_full[acc & 1], (acc >> 1) & 1, a.status)) break;
-      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      const uint32_t d = tmem + (acc & 1) * kSide + ((uint32_t)(q * 32) << 16);
+      const int parts = (tile.w + kPart * kDeep - 1) / (kPart * kDeep);
+      float sum[4][32];
+#pragma unroll
+      for (int c = 0; c < 4; c++)
+#pragma unroll
+        for (int k = 0; k < 32; k++) sum[c][k] = 0.0f;
+      bool ok = true;
+      for (int p = 0; p < parts; p++, acc++) {
+        if (!(ok = wait(sh, &sh->acc_full[acc & 1], (acc >> 1) & 1, a.status))) break;
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        const uint32_t d = tmem + (acc & 1) * kSide + half * 32 + ((uint32_t)(q * 32) << 16);
+#pragma unroll
+        for (int c = 0; c < 4; c++) {
+          uint32_t v[32];
+          tmem_load(v, d + c * 64);
+          tmem_wait(v);
+#pragma unroll
+          for (int k = 0; k < 32; k++) sum[c][k] += __uint_as_float(v[k]);
+        }
+        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) arrive_leader(&sh->acc_empty[acc & 1], to_leader);
+      }
+      if (!ok) break;
       const int n = (tile.y & 0xffff) * kSide + (int)rank * 128 + q * 32;
-      const int k0 = (tile.y >> 16) * kSide;
+      const int k0 = (tile.y >> 16) * kSide + half * 32;
       const bool home = tile.x < a.E;
       const CUtensorMap *map = home ? &map_home : &map_slots;
       const int z = home ? tile.x : tile.x - a.E;
-      for (int c = half * 32; c < kSide; c += 64) {
-        if (n >= a.N || k0 + c >= a.Kd) break;
-        uint32_t v[32];
-        if (some) {
-          tmem_load(v, d + c);
-          tmem_wait(v);
-        } else {
 #pragma unroll
-          for (int k = 0; k < 32; k++) v[k] = 0;
-        }
+      for (int c = 0; c < 4; c++) {
+        if (n >= a.N || k0 + c * 64 >= a.Kd) break;
         // the buffer's last store has read it
         if (elect()) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
         __syncwarp();
 #pragma unroll
         for (int k = 0; k < 8; k++)
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+          asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(
                            buf + lane * 128 + ((k ^ (lane & 7)) * 16)),
-                       "r"(v[4 * k]), "r"(v[4 * k + 1]), "r"(v[4 * k + 2]), "r"(v[4 * k + 3])
+                       "f"(sum[c][4 * k]), "f"(sum[c][4 * k + 1]), "f"(sum[c][4 * k + 2]),
+                       "f"(sum[c][4 * k + 3])
                        : "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (elect()) tma_out(map, buf, k0 + c, n, z, a.add);
-      }
-      if (some) {
-        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) arrive_leader(&sh->acc_empty[acc & 1], to_leader);
-        acc++;
+        if (elect()) tma_out(map, buf, k0 + c * 64, n, z, a.add);
       }
     }
     if (elect()) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
