@@ -68,6 +68,7 @@ struct GradArgs {
   int E, B, L, EB, NvS, N, Kd, nb, kb;  // nb, kb: tiles of n and of k
   int groups, per;    // groups, groups per table entry
   int add;
+  int whole_d, whole_x;  // columns in whole blocks of 64
   int32_t *status;
 };
 
@@ -176,6 +177,22 @@ __device__ __noinline__ int build_table(const GradArgs &a, Shared *sh) {
   return sh->last[kEntries - 1];
 }
 
+// 128 columns from column c on of a stage's rows; whole: in one box, of a map
+// that has the columns as blocks of 64.
+__device__ __forceinline__ void load_side(uint32_t dst, const CUtensorMap *map, int c, int row,
+                                          uint32_t bar, int whole) {
+  if (whole) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(map), "r"(0), "r"(row), "r"(c >> 6), "r"(bar)
+        : "memory");
+  } else {
+    tma_load(dst, map, c, row, bar);
+    tma_load(dst + kChunkBytes, map, c + 64, row, bar);
+  }
+}
+
 // 32 x 32 values of shared memory to a gradient, or added to it.
 __device__ __forceinline__ void tma_out(const CUtensorMap *map, uint32_t src, int x, int y, int z,
                                         bool add) {
@@ -268,10 +285,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                          : "memory");
           else
             arrive_leader(&sh->full[s], to_leader);
-          tma_load(base, &map_d, n0, row, bar);
-          tma_load(base + kChunkBytes, &map_d, n0 + 64, row, bar);
-          tma_load(base + kSideBytes, &map_x, k0, row, bar);
-          tma_load(base + kSideBytes + kChunkBytes, &map_x, k0 + 64, row, bar);
+          load_side(base, &map_d, n0, row, bar, a.whole_d);
+          load_side(base + kSideBytes, &map_x, k0, row, bar, a.whole_x);
         }
         pending |= 1u << s;
         tails = ragged ? tails | 1u << s : tails & ~(1u << s);
@@ -376,51 +391,56 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int4 tile;
       if (!next_tile(sh, i, a.status, &tile)) break;
       const int parts = (tile.w + kPart * kDeep - 1) / (kPart * kDeep);
+      const int n = (tile.y & 0xffff) * kSide + (int)rank * 128 + q * 32;
+      const int k0 = (tile.y >> 16) * kSide + half * 128;
+      const bool home = tile.x < a.E;
+      const CUtensorMap *map = home ? &map_home : &map_slots;
+      const int z = home ? tile.x : tile.x - a.E;
       float sum[4][32];
 #pragma unroll
       for (int c = 0; c < 4; c++)
 #pragma unroll
         for (int k = 0; k < 32; k++) sum[c][k] = 0.0f;
       bool ok = true;
-      for (int p = 0; p < parts; p++, acc++) {
-        if (!(ok = wait(sh, &sh->acc_full[acc & 1], (acc >> 1) & 1, a.status))) break;
+      // the last part's columns go out as they come, so that stores are under
+      // way while the next ones are read
+      for (int p = 0; p < max(parts, 1); p++) {
+        const bool some = parts > 0, end = p >= parts - 1;
+        if (some && !(ok = wait(sh, &sh->acc_full[acc & 1], (acc >> 1) & 1, a.status))) break;
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        const uint32_t d = tmem + (acc & 1) * kSide + half * 32 + ((uint32_t)(q * 32) << 16);
+        const uint32_t d = tmem + (acc & 1) * kSide + half * 128 + ((uint32_t)(q * 32) << 16);
 #pragma unroll
         for (int c = 0; c < 4; c++) {
-          uint32_t v[32];
-          tmem_load(v, d + c * 64);
-          tmem_wait(v);
+          if (some) {
+            uint32_t v[32];
+            tmem_load(v, d + c * 32);
+            tmem_wait(v);
 #pragma unroll
-          for (int k = 0; k < 32; k++) sum[c][k] += __uint_as_float(v[k]);
+            for (int k = 0; k < 32; k++) sum[c][k] += __uint_as_float(v[k]);
+            if (c == 3) {
+              asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+              __syncwarp();
+              if (lane == 0) arrive_leader(&sh->acc_empty[acc & 1], to_leader);
+              acc++;
+            }
+          }
+          if (!end || n >= a.N || k0 + c * 32 >= a.Kd) continue;
+          // the buffer's last store has read it
+          if (elect()) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 8; k++)
+            asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(
+                             buf + lane * 128 + ((k ^ (lane & 7)) * 16)),
+                         "f"(sum[c][4 * k]), "f"(sum[c][4 * k + 1]), "f"(sum[c][4 * k + 2]),
+                         "f"(sum[c][4 * k + 3])
+                         : "memory");
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (elect()) tma_out(map, buf, k0 + c * 32, n, z, a.add);
         }
-        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) arrive_leader(&sh->acc_empty[acc & 1], to_leader);
       }
       if (!ok) break;
-      const int n = (tile.y & 0xffff) * kSide + (int)rank * 128 + q * 32;
-      const int k0 = (tile.y >> 16) * kSide + half * 32;
-      const bool home = tile.x < a.E;
-      const CUtensorMap *map = home ? &map_home : &map_slots;
-      const int z = home ? tile.x : tile.x - a.E;
-#pragma unroll
-      for (int c = 0; c < 4; c++) {
-        if (n >= a.N || k0 + c * 64 >= a.Kd) break;
-        // the buffer's last store has read it
-        if (elect()) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-        __syncwarp();
-#pragma unroll
-        for (int k = 0; k < 8; k++)
-          asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(
-                           buf + lane * 128 + ((k ^ (lane & 7)) * 16)),
-                       "f"(sum[c][4 * k]), "f"(sum[c][4 * k + 1]), "f"(sum[c][4 * k + 2]),
-                       "f"(sum[c][4 * k + 3])
-                       : "memory");
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (elect()) tma_out(map, buf, k0 + c * 64, n, z, a.add);
-      }
     }
     if (elect()) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
@@ -437,13 +457,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 constexpr size_t kSmem = sizeof(Shared) + 1024;
 static_assert(kSmem <= 227 * 1024, "shared memory");
 
-// bf16 rows `pitch` bytes apart, in boxes of 64 columns x kDeep rows.
+// bf16 rows `pitch` bytes apart, in boxes of kDeep rows x 64 columns, or where
+// the columns are whole blocks of 64 (the third dimension) x two of these.
 bool rows_map(CUtensorMap *m, const void *p, int cols, int64_t rows, int64_t pitch) {
-  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-  const cuuint64_t strides[1] = {(cuuint64_t)pitch};
-  const cuuint32_t box[2] = {64, kDeep}, one[2] = {1, 1};
+  const bool whole = cols % 64 == 0;
+  const cuuint64_t dims[3] = {(cuuint64_t)(whole ? 64 : cols), (cuuint64_t)rows,
+                              (cuuint64_t)(cols / 64)};
+  const cuuint64_t strides[2] = {(cuuint64_t)pitch, 128};
+  const cuuint32_t box[3] = {64, kDeep, 2}, one[3] = {1, 1, 1};
   return encoder() &&
-         encoder()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, (void *)p, dims, strides, box, one,
+         encoder()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, whole ? 3 : 2, (void *)p, dims, strides, box, one,
                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -512,6 +535,8 @@ int launch_wgrad(moonep_ctx *ctx, const int32_t *cu, const uint16_t *x, int64_t 
   a.groups = (int)(c.E + extra);
   a.per = (a.groups + kEntries - 1) / kEntries;
   a.add = add;
+  a.whole_d = N % 64 == 0;
+  a.whole_x = Kd % 64 == 0;
   a.status = ctx->d_status;
   return cuda_status(launch_pdl(wgrad_kernel, dim3(2 * ctx->wgrad_clusters), dim3(kThreads), kSmem,
                                 st, false, md, mx, mh, ms, a));
