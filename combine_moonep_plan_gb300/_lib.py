@@ -25,6 +25,7 @@ ERR_TIMEOUT = -9
 PLAN_DUP_RECORDS = 1
 SCORINGS = {"softmax": 0, "sigmoid": 1}
 SCOPES = {"rank": 0, "global": 1}
+GROUP_SCORES = {"max": 0, "top2": 1}
 
 #: every symbol include/moonep.h declares
 EXPORTS = (
@@ -39,6 +40,7 @@ EXPORTS = (
     "moonep_dequantize_mx", "moonep_expert_product", "moonep_gated_act",
     "moonep_gated_act_backward", "moonep_grad_norm_workspace", "moonep_grad_norm",
     "moonep_adamw", "moonep_adamw_moments", "moonep_expert_weight_grad",
+    "moonep_route_select", "moonep_route_select_backward", "moonep_update_route_bias",
 )
 
 
@@ -59,6 +61,12 @@ class MoonepCommPlan(ctypes.Structure):
                 ("E", ctypes.c_int), ("B", ctypes.c_int), ("K", ctypes.c_int),
                 ("S", ctypes.c_int), ("NvS", ctypes.c_int), ("NvS_padded", ctypes.c_int),
                 ("flags", ctypes.c_int), ("internal_bytes", ctypes.c_size_t)]
+
+
+class MoonepRouteSelection(ctypes.Structure):
+    _fields_ = [("bias", ctypes.c_void_p), ("groups", ctypes.c_int), ("top_groups", ctypes.c_int),
+                ("group_score", ctypes.c_int), ("renormalize", ctypes.c_int),
+                ("scale", ctypes.c_float)]
 
 
 class MoonepAdamwConfig(ctypes.Structure):
@@ -127,6 +135,12 @@ def load(path: str = LIB_PATH):
                                      vp, vp, vp]),
         "moonep_route": (ci, [vp, vp, ci, ci, ctypes.c_float, ci, i32p, vp, vp, vp, vp, vp, vp]),
         "moonep_route_backward": (ci, [vp, vp, ci, ci, i32p, vp, vp, vp, vp, vp, vp, vp]),
+        "moonep_route_select": (ci, [vp, vp, ci, ci, ctypes.POINTER(MoonepRouteSelection),
+                                     ctypes.c_float, ci, i32p, vp, vp, vp, vp, vp, vp]),
+        "moonep_route_select_backward": (ci, [vp, vp, ci, ci,
+                                              ctypes.POINTER(MoonepRouteSelection), i32p, vp, vp,
+                                              vp, vp, vp, vp, vp]),
+        "moonep_update_route_bias": (ci, [vp, vp, i32p, ctypes.c_float, vp, vp]),
         "moonep_quantize_mx": (ci, [vp, vp, ci, i64, i64, vp, vp, vp, vp]),
         "moonep_dequantize_mx": (ci, [vp, vp, vp, ci, i64, i64, vp, vp]),
         "moonep_expert_product": (ci, [vp, vp, vp, i64, vp, i64, vp, vp, ci, ci, ci, vp, vp]),

@@ -177,11 +177,11 @@ class Route:
     [R, S, K] int32, weights [R, S, K] fp32, tokens_per_expert [R, E] int32,
     and with a balance loss loss [1] fp32 and coef [R, E] fp32 (None without)."""
 
-    __slots__ = ("_tensors", "scoring", "num_tokens", "_ptrs", "_dims")
+    __slots__ = ("_tensors", "scoring", "num_tokens", "_ptrs", "_dims", "_selection")
 
-    def __init__(self, tensors, scoring, num_tokens, ptrs, dims):
+    def __init__(self, tensors, scoring, num_tokens, ptrs, dims, selection=None):
         self._tensors, self.scoring, self.num_tokens = tensors, scoring, num_tokens
-        self._ptrs, self._dims = ptrs, dims
+        self._ptrs, self._dims, self._selection = ptrs, dims, selection
 
     topk = property(lambda self: self._tensors[0])
     weights = property(lambda self: self._tensors[1])
@@ -543,7 +543,9 @@ class Buffer:
 
     # ------------------------------------------------------------ router
     def route(self, logits: torch.Tensor, scoring: str = "softmax", balance: float = 0.0,
-              scope: str = "rank", num_tokens=None) -> Route:
+              scope: str = "rank", num_tokens=None, bias: torch.Tensor | None = None,
+              groups: int = 1, top_groups: int | None = None, group_score: str = "top2",
+              renormalize: bool = True, scale: float = 1.0) -> Route:
         """Top-K routing of logits [R, S, E] (fp32 or bf16): the picks (largest
         logits, equal ones by lowest index), their weights (scores normalised
         over the picks; scoring "softmax" or "sigmoid"), tokens_per_expert for
@@ -551,8 +553,21 @@ class Buffer:
         per rank ("rank", averaged over the ranks that hold tokens) or over
         all ranks' tokens ("global").  num_tokens: valid tokens of each rank
         (host values); later rows get id 0 and weight 0 and stay out of the
-        loss."""
+        loss.
+
+        With bias [E] fp32 the picks are those of the largest score + bias
+        (softmax: share + bias), with groups > 1 among the top_groups groups
+        (default: all) of neighbouring experts whose largest such value ("max")
+        or sum of the two largest ("top2") is best.  Weights are made of the
+        scores alone and times `scale`: normalised over the picks, or with
+        renormalize=False as they are (softmax: the shares among all
+        experts)."""
         R, S, K, E = dims = self._dims
+        select = None
+        if bias is not None or groups != 1 or not renormalize or scale != 1.0:
+            select = self._selection(bias, groups, top_groups, group_score, renormalize, scale)
+        elif top_groups not in (None, 1):
+            raise ValueError("top_groups: at most groups")
         try:
             score, group = _lib.SCORINGS[scoring], _lib.SCOPES[scope]
         except KeyError as e:
@@ -570,10 +585,45 @@ class Buffer:
             coef_p = store.data_ptr()
             loss_p = coef_p + 4 * R * E
         topk_p, w_p = topk.data_ptr(), weights.data_ptr()
+        if select is not None:
+            check(_lib.load().moonep_route_select(
+                self._ctx, lp, logits.dtype is torch.bfloat16, score, ctypes.byref(select),
+                balance, group, nt, topk_p, w_p, tpe.data_ptr(), coef_p, loss_p, _stream()),
+                "moonep_route_select")
+            select.bias = None  # the route does not keep the tensor
+            return Route((topk, weights, tpe, store), scoring, nt, (topk_p, w_p, coef_p), dims,
+                         select)
         check(_lib.load().moonep_route(
             self._ctx, lp, logits.dtype is torch.bfloat16, score, balance, group, nt, topk_p, w_p,
             tpe.data_ptr(), coef_p, loss_p, _stream()), "moonep_route")
         return Route((topk, weights, tpe, store), scoring, nt, (topk_p, w_p, coef_p), dims)
+
+    def _selection(self, bias, groups, top_groups, group_score, renormalize, scale):
+        try:
+            by = _lib.GROUP_SCORES[group_score]
+        except KeyError:
+            raise ValueError(f"group_score: {group_score!r} is not one of "
+                             f"{sorted(_lib.GROUP_SCORES)}") from None
+        top = groups if top_groups is None else top_groups
+        if groups < 1 or self.E % groups or not 1 <= top <= groups:
+            raise ValueError(f"groups: {groups} of {self.E} experts, {top} of them kept")
+        if self.K > top * (self.E // groups):
+            raise ValueError(f"top_groups: {top} groups of {self.E // groups} experts hold fewer "
+                             f"than {self.K} picks")
+        bp = None if bias is None else _check_tensor(bias, "bias", torch.float32, (self.E,))
+        return _lib.MoonepRouteSelection(bp, groups, top, by, bool(renormalize), scale)
+
+    def update_route_bias(self, bias: torch.Tensor, route: Route, rate: float) -> torch.Tensor:
+        """One step of the selection bias [E] fp32, in place: + rate for experts
+        with fewer picks than the mean over all experts in `route`, - rate for
+        those with more.  Returns the bias."""
+        if route._dims != self._dims:
+            raise ValueError(f"route: made for (R, S, K, E) = {route._dims}, not {self._dims}")
+        bp = _check_tensor(bias, "bias", torch.float32, (self.E,))
+        check(_lib.load().moonep_update_route_bias(
+            self._ctx, route.tokens_per_expert.data_ptr(), route.num_tokens, rate, bp, _stream()),
+            "moonep_update_route_bias")
+        return bias
 
     def route_backward(self, route: Route, logits: torch.Tensor,
                        d_weights: torch.Tensor | None = None,
@@ -597,6 +647,12 @@ class Buffer:
         else:
             op = _check_tensor(out, "d_logits", logits.dtype, (R, S, E))
         topk_p, w_p, coef_p = route._ptrs
+        if route._selection is not None:
+            check(_lib.load().moonep_route_select_backward(
+                self._ctx, lp, logits.dtype is torch.bfloat16, _lib.SCORINGS[route.scoring],
+                ctypes.byref(route._selection), route.num_tokens, topk_p, w_p, dw, coef_p, dl, op,
+                _stream()), "moonep_route_select_backward")
+            return out
         check(_lib.load().moonep_route_backward(
             self._ctx, lp, logits.dtype is torch.bfloat16, _lib.SCORINGS[route.scoring],
             route.num_tokens, topk_p, w_p, dw, coef_p, dl, op, _stream()), "moonep_route_backward")

@@ -497,7 +497,70 @@ int moonep_route_backward(moonep_ctx *ctx, const void *logits, int logits_bf16, 
       !aligned4(d_w_sk) || !aligned4(coef) || !aligned4(d_loss))
     return MOONEP_ERR_INVALID_ARG;
   return launch_route_backward(ctx, logits, logits_bf16 != 0, scoring, num_tokens, topk, w_sk,
-                               d_w_sk, coef, d_loss, d_logits, (cudaStream_t)stream);
+                               d_w_sk, coef, d_loss, d_logits, nullptr, (cudaStream_t)stream);
+}
+
+// A selection that fits the context's experts; the backward pass reads none of
+// its bias and groups.
+static bool selection_ok(const moonep_config &c, const moonep_route_selection *s, bool whole) {
+  if (!s || !(s->scale - s->scale == 0.0f)) return false;
+  if (!whole) return true;
+  return s->groups >= 1 && c.E % s->groups == 0 && s->top_groups >= 1 &&
+         s->top_groups <= s->groups && c.K <= s->top_groups * (c.E / s->groups) &&
+         (s->group_score == MOONEP_GROUP_MAX || s->group_score == MOONEP_GROUP_TOP2) &&
+         aligned4(s->bias);
+}
+
+int moonep_route_select(moonep_ctx *ctx, const void *logits, int logits_bf16, int scoring,
+                        const moonep_route_selection *selection, float balance, int scope,
+                        const int32_t *num_tokens, int32_t *topk, float *w_sk,
+                        int32_t *tokens_per_expert, float *coef, float *loss, void *stream) {
+  int st = check_ctx(ctx);
+  if (st) return st;
+  const moonep_config &c = ctx->cfg;
+  if ((scoring != MOONEP_SCORE_SOFTMAX && scoring != MOONEP_SCORE_SIGMOID) ||
+      (scope != MOONEP_SCOPE_RANK && scope != MOONEP_SCOPE_GLOBAL) || c.K > c.E ||
+      !selection_ok(c, selection, true))
+    return MOONEP_ERR_INVALID_ARG;
+  if (!tokens_per_expert || (c.S > 0 && (!logits || !topk || !w_sk)) ||
+      (coef == nullptr) != (loss == nullptr) || !tokens_ok(c, num_tokens))
+    return MOONEP_ERR_INVALID_ARG;
+  if (!aligned16(logits) || !aligned4(topk) || !aligned4(w_sk) || !aligned4(tokens_per_expert) ||
+      !aligned4(coef) || !aligned4(loss))
+    return MOONEP_ERR_INVALID_ARG;
+  return launch_select(ctx, logits, logits_bf16 != 0, scoring, *selection, balance, scope,
+                       num_tokens, topk, w_sk, tokens_per_expert, coef, loss,
+                       (cudaStream_t)stream);
+}
+
+int moonep_route_select_backward(moonep_ctx *ctx, const void *logits, int logits_bf16, int scoring,
+                                 const moonep_route_selection *selection,
+                                 const int32_t *num_tokens, const int32_t *topk,
+                                 const float *w_sk, const float *d_w_sk, const float *coef,
+                                 const float *d_loss, void *d_logits, void *stream) {
+  int st = check_ctx(ctx);
+  if (st) return st;
+  const moonep_config &c = ctx->cfg;
+  if ((scoring != MOONEP_SCORE_SOFTMAX && scoring != MOONEP_SCORE_SIGMOID) || c.K > c.E ||
+      !tokens_ok(c, num_tokens) || !selection_ok(c, selection, false))
+    return MOONEP_ERR_INVALID_ARG;
+  if (c.S == 0) return MOONEP_OK;
+  if (!logits || !topk || !w_sk || !d_logits) return MOONEP_ERR_INVALID_ARG;
+  if (!aligned16(logits) || !aligned16(d_logits) || !aligned4(topk) || !aligned4(w_sk) ||
+      !aligned4(d_w_sk) || !aligned4(coef) || !aligned4(d_loss))
+    return MOONEP_ERR_INVALID_ARG;
+  return launch_route_backward(ctx, logits, logits_bf16 != 0, scoring, num_tokens, topk, w_sk,
+                               d_w_sk, coef, d_loss, d_logits, selection, (cudaStream_t)stream);
+}
+
+int moonep_update_route_bias(moonep_ctx *ctx, const int32_t *tokens_per_expert,
+                             const int32_t *num_tokens, float rate, float *bias, void *stream) {
+  int st = check_ctx(ctx);
+  if (st) return st;
+  if (!tokens_per_expert || !bias || !aligned4(tokens_per_expert) || !aligned4(bias) ||
+      !tokens_ok(ctx->cfg, num_tokens) || !(rate - rate == 0.0f))
+    return MOONEP_ERR_INVALID_ARG;
+  return launch_route_bias(ctx, tokens_per_expert, num_tokens, rate, bias, (cudaStream_t)stream);
 }
 
 // Sizes of a microscaled tensor: whole blocks, and offsets that fit.

@@ -166,7 +166,14 @@ int launch_route(moonep_ctx *ctx, const void *logits, int bf16, int scoring, flo
 int launch_route_backward(moonep_ctx *ctx, const void *logits, int bf16, int scoring,
                           const int32_t *num_tokens, const int32_t *topk, const float *w,
                           const float *dw, const float *coef, const float *dloss, void *dz,
-                          cudaStream_t st);
+                          const moonep_route_selection *sel, cudaStream_t st);
+// The router with a bias and groups, and the bias's step.
+int launch_select(moonep_ctx *ctx, const void *logits, int bf16, int scoring,
+                  const moonep_route_selection &sel, float alpha, int global,
+                  const int32_t *num_tokens, int32_t *topk, float *w, int32_t *tpe, float *coef,
+                  float *loss, cudaStream_t st);
+int launch_route_bias(moonep_ctx *ctx, const int32_t *tpe, const int32_t *num_tokens, float rate,
+                      float *bias, cudaStream_t st);
 // Microscaled 4-bit tensors and the experts' product of two of them.
 int launch_quantize_mx(moonep_ctx *ctx, const void *x, int fp32, int64_t rows, int64_t cols,
                        const int32_t *cu, uint8_t *packed, uint8_t *scales, cudaStream_t st);

@@ -17,271 +17,12 @@
 // A row whose scores sum to zero (every logit -inf) has p = w = 0 and no
 // gradient; its picks are the lowest indices.  A NaN logit ranks first and
 // makes its row's weights NaN; the ids stay in [0, E).
-#include <cuda_bf16.h>
-
-#include "moonep_internal.cuh"
-#include "mx_common.cuh"
+#include "route_common.cuh"
 
 namespace moonep {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kCluster = 8;  // blocks that add up their sums before they leave
-
-struct RouteArgs {
-  const void *logits;  // [R, S, E] fp32 or bf16
-  int32_t *topk;       // [R, S, K]
-  float *w;            // [R, S, K]
-  float *part_p;       // [R, parts, E] sums of p of one cluster's tokens, or null
-  int32_t *part_c;     // [R, parts, E] picks of one cluster's tokens
-  int32_t *tpe;        // [R, E], written here when a rank has one cluster and no loss
-  int R, S, E, K, sigmoid, cluster;
-  int32_t ntok[kMaxRanks];
-};
-
-// Order-preserving bits: a larger logit has a larger key, -0 equals +0 and NaN
-// is largest (adding +0 turns -0 into +0 and every NaN into 0x7fffffff); 0 is
-// below every logit.
-__device__ __forceinline__ uint32_t order_key(float v) {
-  const uint32_t b = __float_as_uint(__fadd_rn(v, 0.0f));
-  return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
-}
-
-// The logit of a key (NaN for the NaN key).
-__device__ __forceinline__ float key_value(uint32_t k) {
-  return __uint_as_float((k & 0x80000000u) ? k & 0x7fffffffu : ~k);
-}
-
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
-
-// Sum over the LP lanes that share a token.
-template <int LP>
-__device__ __forceinline__ float group_sum(float v) {
-#pragma unroll
-  for (int o = LP / 2; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
-
-// exp(x) as a power of two: two parts in 2^23, and the rounding of x log2(e)
-// (|x| parts in 2^24); below 2^-126 zero.  1/x within an ulp.
-__device__ __forceinline__ float exp_fast(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
-  return r;
-}
-__device__ __forceinline__ float inverse(float x) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-
-// Score of one logit; m is the row's maximum (softmax).  exp(-z) may be
-// infinite, its inverse is then zero.
-__device__ __forceinline__ float score(float z, float m, bool sigmoid) {
-  if (sigmoid) return inverse(1.0f + exp_fast(-z));
-  return m == -INFINITY ? 0.0f : exp_fast(z - m);
-}
-
-__device__ __forceinline__ float to_f(float v) { return v; }
-__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
-
-// V logits of a row from column c on; -inf past the row's end.  `vec`: rows
-// are whole aligned vectors.
-template <int V>
-__device__ __forceinline__ void load_row(const float *z, int c, int E, bool vec, float f[V]) {
-  if (V % 4 == 0 && vec) {
-#pragma unroll
-    for (int i = 0; i < V; i += 4) {
-      const float4 v = c + i < E ? __ldg((const float4 *)(z + c + i))
-                                 : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-      f[i] = v.x;
-      f[i + 1] = v.y;
-      f[i + 2] = v.z;
-      f[i + 3] = v.w;
-    }
-    return;
-  }
-  if (V == 2 && vec) {
-    const float2 v = c < E ? __ldg((const float2 *)(z + c)) : make_float2(-INFINITY, -INFINITY);
-    f[0] = v.x;
-    f[V - 1] = v.y;
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < V; i++) f[i] = c + i < E ? __ldg(z + c + i) : -INFINITY;
-}
-template <int V>
-__device__ __forceinline__ void load_row(const __nv_bfloat16 *z, int c, int E, bool vec,
-                                         float f[V]) {
-  if (V % 8 == 0 && vec) {
-#pragma unroll
-    for (int i = 0; i < V; i += 8) {
-      if (c + i < E) {
-        bf16x8(__ldg((const uint4 *)(z + c + i)), f + i);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; j++) f[i + j] = -INFINITY;
-      }
-    }
-    return;
-  }
-  if (V % 4 == 0 && vec) {
-#pragma unroll
-    for (int i = 0; i < V; i += 4) {
-      const uint2 v = c + i < E ? __ldg((const uint2 *)(z + c + i))
-                                : make_uint2(0xff80ff80u, 0xff80ff80u);
-      f[i] = __uint_as_float(v.x << 16);
-      f[i + 1] = __uint_as_float(v.x & 0xffff0000u);
-      f[i + 2] = __uint_as_float(v.y << 16);
-      f[i + 3] = __uint_as_float(v.y & 0xffff0000u);
-    }
-    return;
-  }
-  if (V == 2 && vec) {
-    const uint32_t v = c < E ? __ldg((const uint32_t *)(z + c)) : 0xff80ff80u;
-    f[0] = __uint_as_float(v << 16);
-    f[V - 1] = __uint_as_float(v & 0xffff0000u);
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < V; i++) f[i] = c + i < E ? to_f(z[c + i]) : -INFINITY;
-}
-
-template <int V>
-__device__ __forceinline__ void store_row(float *z, int c, int E, bool vec, const float f[V]) {
-  if (V % 4 == 0 && vec) {
-#pragma unroll
-    for (int i = 0; i < V; i += 4)
-      if (c + i < E) *(float4 *)(z + c + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
-    return;
-  }
-  if (V == 2 && vec) {
-    if (c < E) *(float2 *)(z + c) = make_float2(f[0], f[V - 1]);
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < V; i++)
-    if (c + i < E) z[c + i] = f[i];
-}
-template <int V>
-__device__ __forceinline__ void store_row(__nv_bfloat16 *z, int c, int E, bool vec,
-                                          const float f[V]) {
-  if (V % 8 == 0 && vec) {
-#pragma unroll
-    for (int i = 0; i < V; i += 8)
-      if (c + i < E) *(uint4 *)(z + c + i) = to_bf16x8(f + i);
-    return;
-  }
-  if (V % 2 == 0 && vec) {
-#pragma unroll
-    for (int i = 0; i < V; i += 2)
-      if (c + i < E) *(__nv_bfloat162 *)(z + c + i) = __floats2bfloat162_rn(f[i], f[i + 1]);
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < V; i++)
-    if (c + i < E) z[c + i] = __float2bfloat16_rn(f[i]);
-}
-
-// Adds up the blocks' sums cnt[E] and acc[E] (acc: `warps` rows of E, one per
-// warp) over the cluster, in a fixed order, and writes them.
-__device__ void finish_block(const RouteArgs &a, int32_t *cnt, float *acc, int warps) {
-  const int r = blockIdx.y;
-  __syncthreads();
-  if (a.part_p) {
-    for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
-      float v = acc[e];
-      for (int i = 1; i < warps; i++) v += acc[(size_t)i * a.E + e];
-      acc[e] = v;
-    }
-  }
-  const int n = a.cluster, me = blockIdx.x % n, parts = gridDim.x / n;
-  const int64_t o = ((int64_t)r * parts + blockIdx.x / n) * a.E;
-  if (n > 1)
-    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;"
-                 ::: "memory");
-  else
-    __syncthreads();
-  const uint32_t c0 = (uint32_t)__cvta_generic_to_shared(cnt);
-  const uint32_t a0 = (uint32_t)__cvta_generic_to_shared(acc);
-  for (int e = me * blockDim.x + threadIdx.x; e < a.E; e += n * blockDim.x) {
-    int c = 0;
-    float p = 0.0f;
-    for (int b = 0; b < n; b++) {
-      uint32_t ca, pa;
-      int cv;
-      float pv;
-      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ca) : "r"(c0 + 4 * e), "r"(b));
-      asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(cv) : "r"(ca) : "memory");
-      c += cv;
-      if (!a.part_p) continue;
-      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(pa) : "r"(a0 + 4 * e), "r"(b));
-      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(pv) : "r"(pa) : "memory");
-      p += pv;
-    }
-    if (a.tpe) {
-      a.tpe[(int64_t)r * a.E + e] = c + (e == 0 ? (a.S - a.ntok[r]) * a.K : 0);
-    } else {
-      a.part_c[o + e] = c;
-      if (a.part_p) a.part_p[o + e] = p;
-    }
-  }
-  // no block leaves before the others have read its sums
-  if (n > 1)
-    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;"
-                 ::: "memory");
-}
-
-// The K largest of a warp's keys (V per lane, index col + i), in order, into
-// stage[0..K): the K-th largest of the lanes' maxima is at most the K-th
-// largest key, so the few keys at or above it (usually K to K + 4 of 256)
-// move to one per lane, through buf, and the rounds work on a single register:
-// 170 instructions for K = 8, V = 8, against 400 over all keys.  False, with
-// nothing written, when more than a warp's worth of keys qualify (equal
-// logits).
-template <int V>
-__device__ __forceinline__ bool pick_few(const uint32_t key[V], int col, int K, int lane,
-                                         uint2 *buf, uint2 *stage) {
-  uint32_t best = key[0];
-#pragma unroll
-  for (int i = 1; i < V; i++) best = max(best, key[i]);
-  uint32_t least = 0;
-  for (int k = 0; k < K; k++) {
-    least = __reduce_max_sync(0xffffffffu, best);
-    if (best == least) best = 0;  // equal maxima together: only more keys qualify
-  }
-  if (least == 0) least = 1;  // fewer lanes than picks hold logits
-  int n = 0;
-  unsigned in[V];
-#pragma unroll
-  for (int i = 0; i < V; i++) {
-    in[i] = __ballot_sync(0xffffffffu, key[i] >= least);
-    n += __popc(in[i]);
-  }
-  if (n > 32) return false;
-  const unsigned before = (1u << lane) - 1;
-  int at = 0;
-#pragma unroll
-  for (int i = 0; i < V; i++) {
-    if (key[i] >= least) buf[at + __popc(in[i] & before)] = make_uint2(key[i], col + i);
-    at += __popc(in[i]);
-  }
-  __syncwarp();
-  uint2 c = lane < n ? buf[lane] : make_uint2(0u, 0xffffffffu);
-  for (int k = 0; k < K; k++) {
-    const uint32_t top = __reduce_max_sync(0xffffffffu, c.x);
-    const uint32_t id = __reduce_min_sync(0xffffffffu, c.x == top ? c.y : 0xffffffffu);
-    if (c.y == id) {
-      stage[k] = c;
-      c.x = 0;
-    }
-  }
-  return true;
-}
+constexpr int kWarps = kRouteWarps;
 
 // Rows of at most LP * V logits in registers, LP lanes to a token, lane l
 // holding columns l*V .. l*V + V - 1 (so the lowest lane and the lowest of its
@@ -468,17 +209,6 @@ __global__ void __launch_bounds__(kWarps * 32) route_long_kernel(RouteArgs a) {
   finish_block(a, cnt, sh, warps);
 }
 
-struct FinishArgs {
-  float *part_p;
-  const int32_t *part_c;
-  int32_t *tpe;  // [R, E]
-  float *coef;   // [R, E] or null
-  float *loss;   // [1] or null
-  float alpha;
-  int R, S, E, K, parts, global;
-  int32_t ntok[kMaxRanks];
-};
-
 constexpr int kFinishBlocks = 8;
 
 __device__ __forceinline__ void finish_arrive() {
@@ -582,6 +312,10 @@ struct RouteBwdArgs {
   const float *dloss;  // [1] or null (1)
   void *dz;            // [R, S, E] in the logits' type
   int R, S, E, K, sigmoid;
+  // of weights that are not the picks' shares alone (kForm): their scale's
+  // inverse, and whether they are normalised
+  float unscale;
+  int renormalize;
   int32_t ntok[kMaxRanks];
 };
 
@@ -592,10 +326,15 @@ __device__ __forceinline__ float one_minus_sigmoid(float z) { return inverse(1.0
 // then ordinary numbers, as the shares that they stand for are.
 constexpr float kCoefScale = 0x1p40f, kCoefUnscale = 0x1p-40f;
 
+// With kForm weights are w = scale a / sum a (renormalize) or scale a, a the
+// shares (softmax) or scores (sigmoid): a pick's term is w (dw - sum w dw /
+// scale) in the first case, w dw in the second, where the shares' common
+// denominator adds -p sum w dw to every expert.
+//
 // The same layout of rows in registers; blockIdx.y is the rank, whose
 // coefficients stay in registers too.  A pick's term reaches the lane of its
 // column through a zeroed row of shared memory.
-template <typename T, int LP, int V>
+template <typename T, int LP, int V, bool kForm>
 __global__ void __launch_bounds__(kWarps * 32) route_backward_kernel(RouteBwdArgs a, bool vec) {
   pdl_wait();
   pdl_launch_dependents();
@@ -650,11 +389,16 @@ __global__ void __launch_bounds__(kWarps * 32) route_backward_kernel(RouteBwdArg
     float z[V], g[V];
 #pragma unroll
     for (int i = 0; i < V; i++) z[i] = ahead[i];
+    float all = 0.0f;  // what the picks' gradients take from every share
     if (a.dw) {
       float wd = 0.0f;
 #pragma unroll
       for (int i = 0; i < kPicks; i++) wd += pw[i] * pd[i];
       wd = group_sum<LP>(wd);
+      if (kForm) {
+        if (!a.renormalize && !a.sigmoid) all = wd;
+        wd = a.renormalize ? wd * a.unscale : 0.0f;
+      }
 #pragma unroll
       for (int i = 0; i < kPicks; i++)
         if (pid[i] >= 0 && pid[i] < a.E) row[pid[i]] = pw[i] * (pd[i] - wd);
@@ -666,7 +410,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_backward_kernel(RouteBwdArg
     float slope[V];  // d log(score) / d logit
 #pragma unroll
     for (int i = 0; i < V; i++) slope[i] = 1.0f;
-    if (a.coef || a.sigmoid) {
+    if (a.coef || a.sigmoid || (kForm && a.dw && !a.renormalize)) {
       float m = 0.0f;
       if (!a.sigmoid) {
         m = z[0];
@@ -697,7 +441,8 @@ __global__ void __launch_bounds__(kWarps * 32) route_backward_kernel(RouteBwdArg
       const float f = dl * kCoefUnscale;
 #pragma unroll
       for (int i = 0; i < V; i++)
-        g[i] = on ? (g[i] + p[i] * inv * (f * (cf[i] - pc))) * slope[i] : 0.0f;
+        g[i] = on ? (g[i] + p[i] * inv * (kForm ? f * (cf[i] - pc) - all : f * (cf[i] - pc))) *
+                        slope[i] : 0.0f;
     }
     if (s < a.S) store_row<V>((T *)a.dz + t * a.E, col, a.E, vec, g);
     __syncwarp();
@@ -713,7 +458,7 @@ __device__ __forceinline__ void put(float *p, float v) { *p = v; }
 __device__ __forceinline__ void put(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
 
 // Any E: one warp per token, several passes over its row.
-template <typename T>
+template <typename T, bool kForm>
 __global__ void __launch_bounds__(kWarps * 32) route_backward_long_kernel(RouteBwdArgs a) {
   pdl_wait();
   pdl_launch_dependents();
@@ -734,11 +479,13 @@ __global__ void __launch_bounds__(kWarps * 32) route_backward_long_kernel(RouteB
 #pragma unroll
     for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     float Z = 0.0f, pc = 0.0f;
-    if (cf) {
+    // shares that are not normalised over the picks lower each other
+    const bool shares = kForm && !a.renormalize && !a.sigmoid;
+    if (cf || shares) {
       for (int e = lane; e < a.E; e += 32) {
         const float s1 = score(to_f(z[e]), m, a.sigmoid);
         Z += s1;
-        pc += s1 * (cf[e] * kCoefScale);
+        if (cf) pc += s1 * (cf[e] * kCoefScale);
       }
       Z = warp_sum(Z);
       pc = warp_sum(pc);
@@ -753,11 +500,16 @@ __global__ void __launch_bounds__(kWarps * 32) route_backward_long_kernel(RouteB
       dk = a.dw ? a.dw[t * a.K + lane] : 0.0f;
       if (id < 0 || id >= a.E) id = -1;
     }
-    const float wd = warp_sum(wk * dk);
+    float wd = warp_sum(wk * dk), all = 0.0f;
+    if (kForm) {
+      if (shares) all = wd;
+      wd = a.renormalize ? wd * a.unscale : 0.0f;
+    }
     for (int e = lane; e < a.E; e += 32) {
       const float x = to_f(z[e]);
       float g = 0.0f;
       if (cf) g = score(x, m, a.sigmoid) * inv * (dl * (cf[e] - pc));
+      if (shares) g -= score(x, m, a.sigmoid) * inv * all;
       if (a.sigmoid) g *= one_minus_sigmoid(x);
       put(out + e, g);
     }
@@ -766,6 +518,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_backward_long_kernel(RouteB
       const float x = to_f(z[id]);
       float g = wk * (dk - wd);
       if (cf) g += score(x, m, a.sigmoid) * inv * (dl * (cf[id] - pc));
+      if (shares) g -= score(x, m, a.sigmoid) * inv * all;
       if (a.sigmoid) g *= one_minus_sigmoid(x);
       put(out + id, g);
     }
@@ -845,31 +598,31 @@ cudaError_t launch_forward(const RouteArgs &a, int bpr, cudaStream_t st) {
                        false, a.cluster, a, whole_vectors(a.E, sizeof(T) == 2));
 }
 
-template <typename T>
+template <typename T, bool kForm>
 auto route_backward_kernel_of(Form f) {
-  return f == kThread8 ? route_backward_kernel<T, 1, 8> : f == kFour8 ? route_backward_kernel<T, 4, 8>
-         : f == kWarp2 ? route_backward_kernel<T, 32, 2>
-         : f == kWarp4 ? route_backward_kernel<T, 32, 4>
-         : f == kWarp8 ? route_backward_kernel<T, 32, 8>
-         : f == kWarp12 ? route_backward_kernel<T, 32, 12>
-                        : route_backward_kernel<T, 32, 16>;
+  return f == kThread8 ? route_backward_kernel<T, 1, 8, kForm> : f == kFour8 ? route_backward_kernel<T, 4, 8, kForm>
+         : f == kWarp2 ? route_backward_kernel<T, 32, 2, kForm>
+         : f == kWarp4 ? route_backward_kernel<T, 32, 4, kForm>
+         : f == kWarp8 ? route_backward_kernel<T, 32, 8, kForm>
+         : f == kWarp12 ? route_backward_kernel<T, 32, 12, kForm>
+                        : route_backward_kernel<T, 32, 16, kForm>;
 }
 
-template <typename T>
+template <typename T, bool kForm>
 cudaError_t launch_backward(const moonep_ctx *ctx, const RouteBwdArgs &a, cudaStream_t st) {
   const Form f = form_of(a.E);
   const int per = kWarps * tokens_per_warp(f), threads = kWarps * 32;
   const int per_sm = f == kWarp16 ? 2 : 3;  // what the registers allow
   const int64_t held = f == kLong
-                           ? blocks_in_cap(ctx, route_backward_long_kernel<T>, threads, 0)
-                           : blocks_in_cap(ctx, route_backward_kernel_of<T>(f), threads, 0);
+                           ? blocks_in_cap(ctx, route_backward_long_kernel<T, kForm>, threads, 0)
+                           : blocks_in_cap(ctx, route_backward_kernel_of<T, kForm>(f), threads, 0);
   const int64_t need = ((int64_t)a.S + per - 1) / per;
   int64_t cap = ((int64_t)ctx->sms * per_sm + a.R - 1) / a.R;
   if (held / a.R < cap) cap = held / a.R > 0 ? held / a.R : 1;
   const dim3 grid((unsigned)(need < cap ? need : cap), a.R);
   if (f == kLong)
-    return launch_pdl(route_backward_long_kernel<T>, grid, dim3(threads), 0, st, false, a);
-  return launch_pdl(route_backward_kernel_of<T>(f), grid, dim3(threads), 0, st, false, a,
+    return launch_pdl(route_backward_long_kernel<T, kForm>, grid, dim3(threads), 0, st, false, a);
+  return launch_pdl(route_backward_kernel_of<T, kForm>(f), grid, dim3(threads), 0, st, false, a,
                     whole_vectors(a.E, sizeof(T) == 2));
 }
 
@@ -881,6 +634,10 @@ cudaError_t route_configure(int E) {
   if (e == cudaSuccess)
     e = raise_dyn_smem((const void *)route_long_kernel<__nv_bfloat16>, (int)long_smem(E));
   return e;
+}
+
+cudaError_t launch_route_finish(const FinishArgs &f, cudaStream_t st) {
+  return launch_pdl(route_finish_kernel, dim3(kFinishBlocks), dim3(256), 0, st, false, f);
 }
 
 int64_t route_scratch_words(int R, int E, int sms) {
@@ -920,14 +677,14 @@ int launch_route(moonep_ctx *ctx, const void *logits, int bf16, int scoring, flo
   for (int r = 0; r < c.R; r++) a.ntok[r] = f.ntok[r] = num_tokens ? num_tokens[r] : c.S;
   cudaError_t e = bf16 ? launch_forward<__nv_bfloat16>(a, bpr, st) : launch_forward<float>(a, bpr, st);
   if (e == cudaSuccess && !a.tpe)
-    e = launch_pdl(route_finish_kernel, dim3(kFinishBlocks), dim3(256), 0, st, false, f);
+    e = launch_route_finish(f, st);
   return cuda_status(e);
 }
 
 int launch_route_backward(moonep_ctx *ctx, const void *logits, int bf16, int scoring,
                           const int32_t *num_tokens, const int32_t *topk, const float *w,
                           const float *dw, const float *coef, const float *dloss, void *dz,
-                          cudaStream_t st) {
+                          const moonep_route_selection *sel, cudaStream_t st) {
   const moonep_config &c = ctx->cfg;
   RouteBwdArgs a{};
   a.logits = logits;
@@ -943,8 +700,15 @@ int launch_route_backward(moonep_ctx *ctx, const void *logits, int bf16, int sco
   a.K = c.K;
   a.sigmoid = scoring;
   for (int r = 0; r < c.R; r++) a.ntok[r] = num_tokens ? num_tokens[r] : c.S;
-  return cuda_status(bf16 ? launch_backward<__nv_bfloat16>(ctx, a, st)
-                          : launch_backward<float>(ctx, a, st));
+  if (sel) {
+    a.renormalize = sel->renormalize != 0;
+    // weights of scale 0 are 0, and so is their gradient
+    a.unscale = sel->scale == 0.0f ? 0.0f : 1.0f / sel->scale;
+    return cuda_status(bf16 ? launch_backward<__nv_bfloat16, true>(ctx, a, st)
+                            : launch_backward<float, true>(ctx, a, st));
+  }
+  return cuda_status(bf16 ? launch_backward<__nv_bfloat16, false>(ctx, a, st)
+                          : launch_backward<float, false>(ctx, a, st));
 }
 
 }  // namespace moonep

@@ -40,7 +40,8 @@
  *     buffers behind moonep_hidden_view / moonep_weight_view.
  *   - One context plans one batch at a time: its planner scratch (counters,
  *     per-rank totals) is shared by its moonep_plan calls, and its router
- *     scratch by its moonep_route calls, so two plans, or two routes, must not
+ *     scratch by its moonep_route and moonep_route_select calls, so two plans,
+ *     or two routes, must not
  *     overlap on the GPU (issue them on one stream, or order the streams); use
  *     one context per concurrent stream.  A plan and a route may overlap.  The
  *     other entry points keep no state between calls and may overlap freely.
@@ -421,6 +422,58 @@ int moonep_route_backward(moonep_ctx *ctx, const void *logits, int logits_bf16,
                           const int32_t *topk, const float *w_sk,
                           const float *d_w_sk, const float *coef,
                           const float *d_loss, void *d_logits, void *stream);
+
+/* The router with a bias that balances the experts' loads, and with expert
+ * groups.  Scores and shares as moonep_route's; a_e = p_e (softmax) or s_e
+ * (sigmoid), and in place of the logits
+ *   c_e = a_e + bias[e]
+ * selects: the E/groups neighbouring experts of a group score the largest c
+ * (MOONEP_GROUP_MAX) or the sum of the two largest (MOONEP_GROUP_TOP2; the one
+ * of a group of one), and the picks are the K largest c within the top_groups
+ * best groups; equal values by lowest index, a NaN first.  The order is that
+ * of c in 64 bits; without a bias that of the logits.
+ *   w_sk   scale a of the picks over their sum (renormalize; 0 when that is 0),
+ *          or scale a; the bias weighs nothing
+ * Everything else as moonep_route.  bias: [E] fp32 in device memory or NULL;
+ * E % groups == 0, 1 <= top_groups <= groups, K <= top_groups * (E / groups). */
+#define MOONEP_GROUP_MAX 0
+#define MOONEP_GROUP_TOP2 1
+typedef struct moonep_route_selection {
+  const float *bias;
+  int groups;      /* 1: no groups */
+  int top_groups;
+  int group_score;
+  int renormalize;
+  float scale;     /* finite */
+} moonep_route_selection;
+int moonep_route_select(moonep_ctx *ctx, const void *logits, int logits_bf16,
+                        int scoring, const moonep_route_selection *selection,
+                        float balance, int scope, const int32_t *num_tokens,
+                        int32_t *topk, float *w_sk, int32_t *tokens_per_expert,
+                        float *coef, float *loss, void *stream);
+
+/* moonep_route_backward for moonep_route_select's weights (selection's
+ * renormalize and scale; picks, bias and groups have no gradient):
+ *   g_e = d_loss p_e (coef_e - sum_j p_j coef_j) + [e picked] t_e - u p_e
+ *   renormalize   t_e = w_e (d_w_e - sum_k w_k d_w_k / scale), u = 0
+ *   otherwise     t_e = w_e d_w_e, u = sum_k w_k d_w_k (softmax) or 0 (sigmoid) */
+int moonep_route_select_backward(moonep_ctx *ctx, const void *logits,
+                                 int logits_bf16, int scoring,
+                                 const moonep_route_selection *selection,
+                                 const int32_t *num_tokens,
+                                 const int32_t *topk, const float *w_sk,
+                                 const float *d_w_sk, const float *coef,
+                                 const float *d_loss, void *d_logits,
+                                 void *stream);
+
+/* One step of the bias, in place: bias[e] += rate sign(mean load - load_e), the
+ * load of an expert its picks among the valid tokens of all ranks
+ * (tokens_per_expert [R, E] as the router wrote it, num_tokens as given to it);
+ * a load equal to the mean leaves the bias as it is.  Counts are compared as
+ * whole numbers. */
+int moonep_update_route_bias(moonep_ctx *ctx, const int32_t *tokens_per_expert,
+                             const int32_t *num_tokens, float rate,
+                             float *bias, void *stream);
 
 /* Microscaled 4-bit quantisation (OCP MX v1.0, MXFP4) of x [rows, cols] (bf16,
  * or fp32 when x_fp32), cols % 32 == 0: every 32 values of a row share the

@@ -57,3 +57,70 @@ def weight_grad(x, d, cu, E, R, B, NvS):
         out[g] = ds.T @ xs
         mag[g] = np.abs(ds).T @ np.abs(xs)
     return out, mag
+
+
+def select_values(z, scoring, bias):
+    """What selects, in 64 bits: the logits where there is no bias."""
+    if bias is None:
+        return np.asarray(z, np.float64)
+    s = ref.scores(np.asarray(z, np.float64), scoring)
+    return (ref.share(s) if scoring == "softmax" else s) + np.asarray(bias, np.float64)
+
+
+def select(z, K, scoring, bias, groups, top_groups, mode):
+    """Picks [R, S, K] in 64 bits."""
+    z = np.asarray(z, np.float64)
+    R, S, E = z.shape
+    c = select_values(z, scoring, bias)
+    out = np.zeros(z.shape, bool)
+    if top_groups < groups:
+        a = ref.scores(z, scoring)
+        by = c if bias is not None or mode == "max" else \
+            (ref.share(a) if scoring == "softmax" else a)
+        parts = -np.sort(-by.reshape(R, S, groups, -1), axis=-1)
+        value = parts[..., 0] + (parts[..., 1] if mode == "top2" and E > groups else 0)
+        kept = ref.picks(value, top_groups)
+        keep = np.zeros((R, S, groups), bool)
+        np.put_along_axis(keep, kept, True, -1)
+        out = np.repeat(~keep, E // groups, axis=-1)
+    # left-out experts behind everything else, by index among equals
+    idx = np.broadcast_to(np.arange(E), z.shape)
+    key = np.where(np.isnan(c), np.inf, c)
+    return np.lexsort((idx, -key, ~np.isnan(c), out), axis=-1)[..., :K]
+
+
+def select_weights(z, ids, scoring, renormalize, scale, ntok):
+    s = ref.scores(np.asarray(z, np.float64), scoring)
+    a = ref.share(s) if scoring == "softmax" else s
+    ak = np.take_along_axis(a, ids, -1)
+    if renormalize:
+        if scoring == "softmax":
+            # the picks' ratios, also where their shares are far below the rest
+            zk = np.take_along_axis(np.asarray(z, np.float64), ids, -1)
+            ak = ref.scores(zk, "softmax")
+        ak = ref.share(ak)
+    live = np.arange(z.shape[1])[None, :] < np.asarray(ntok)[:, None]
+    return scale * ak * live[..., None]
+
+
+def select_grad(z, ids, w, dw, coef, dl, scoring, ntok, renormalize, scale):
+    """(gradient, sum of its terms' magnitudes) in 64 bits."""
+    z = np.asarray(z, np.float64)
+    live = (np.arange(z.shape[1])[None, :] < np.asarray(ntok)[:, None])[..., None]
+    p = ref.share(ref.scores(z, scoring))
+    c = coef[:, None, :]
+    g = dl * p * (c - (p * c).sum(-1, keepdims=True))
+    mag = abs(dl) * p * (abs(c) + (p * abs(c)).sum(-1, keepdims=True))
+    wd, wm = (w * dw).sum(-1, keepdims=True), (w * abs(dw)).sum(-1, keepdims=True)
+    if renormalize:
+        t = w * (dw - (wd / scale if scale else 0))
+        tm = w * (abs(dw) + (wm / abs(scale) if scale else 0))
+    else:
+        t, tm = w * dw, w * abs(dw)
+        if scoring == "softmax":
+            g, mag = g - p * wd, mag + p * wm
+    add, addm = np.zeros_like(p), np.zeros_like(p)
+    np.put_along_axis(add, ids, t, -1)
+    np.put_along_axis(addm, ids, np.abs(tm), -1)
+    slope = ref.sigmoid(-z) if scoring == "sigmoid" else 1.0
+    return np.where(live, (g + add) * slope, 0), np.where(live, (mag + addm) * slope, 0)
