@@ -10,10 +10,11 @@
 //
 // The order of c is that of its value in 64 bits.  In fp32 two neighbours may
 // come out the wrong way round, so the picks are made in fp32 with a bound on
-// each value's error, and a row in which a comparison that mattered (neighbours
+// each value's error, and where a comparison that mattered (neighbours
 // among the picks, the last pick and the rest, the last group and the rest) is
-// closer than the bounds is done again in 64 bits by its warp: one row in a
-// thousand of 256 experts.  Two experts with the same logit and bias have the
+// closer than the bounds, 64 bits decide: among the picks of sigmoid scores the
+// few candidates alone, one row in a thousand of 256 experts, else the whole
+// row is done again.  Two experts with the same logit and bias have the
 // same c and need no second look.
 #include "route_common.cuh"
 
@@ -21,6 +22,7 @@ namespace moonep {
 namespace {
 
 constexpr int kWarps = kRouteWarps;
+constexpr int kScratch = 100;  // words of a warp: 36 candidates, their indices, the picks
 
 struct SelectArgs {
   RouteArgs r;
@@ -39,12 +41,11 @@ __device__ __forceinline__ double key_value64(uint64_t k) {
   return __longlong_as_double((int64_t)((k >> 63) ? k & 0x7fffffffffffffffull : ~k));
 }
 
-// A row's picks in 64 bits, by one warp: indices into stage[k].y, and the
-// logits' keys into stage[k].x.  row: E words of shared memory, of the warp's
-// own; best: one word per group.
+// A row's picks in 64 bits, by one warp, into index.  row: E words of shared
+// memory, of the warp's own; best: one word per group.
 template <typename T>
-__device__ __noinline__ void select_exact(const SelectArgs &a, const T *z, uint64_t *row,
-                                          uint64_t *best, uint2 *stage) {
+__device__ __forceinline__ void select_exact(const SelectArgs &a, const T *z, uint64_t *row,
+                                          uint64_t *best, int32_t *index) {
   const int lane = threadIdx.x & 31, E = a.r.E, gs = E / a.groups;
   const bool grouped = a.top_groups < a.groups;
   if (a.bias || grouped) {
@@ -118,20 +119,20 @@ __device__ __noinline__ void select_exact(const SelectArgs &a, const T *z, uint6
     }
     if (lane == 0) {
       row[at] = 0;
-      stage[k] = make_uint2(order_key(to_f(z[at])), at);
+      index[k] = at;
     }
     __syncwarp();
   }
 }
 
-// Weights, ids and counts of a row's picks (stage: the logits' keys and
-// indices); m and inv: the row's largest logit and 1 / sum of its scores, for
-// softmax weights that are not normalised.
-__device__ __forceinline__ void write_picks(const SelectArgs &a, const uint2 *stage, int64_t t,
+// Weights, ids and counts of a row's picks, one per lane (id, and logit z); m and
+// inv: the row's largest logit and 1 / sum of its scores, for softmax weights
+// that are not normalised.
+__device__ __forceinline__ void write_picks(const SelectArgs &a, int id, float z, int64_t t,
                                             bool on, float m, float inv, int32_t *cnt) {
   const int lane = threadIdx.x & 31, K = a.r.K;
   const bool mine = lane < K;
-  const float z = mine && on ? key_value(stage[lane].x) : -INFINITY;
+  if (!on || !mine) z = -INFINITY;
   float by = 1.0f, top = m;
   if (a.renormalize && !a.r.sigmoid) {
     top = z;
@@ -146,122 +147,292 @@ __device__ __forceinline__ void write_picks(const SelectArgs &a, const uint2 *st
     by = a.r.sigmoid ? a.scale : a.scale * inv;
   }
   if (mine) {
-    a.r.topk[t * K + lane] = on ? (int)stage[lane].y : 0;
+    a.r.topk[t * K + lane] = on ? id : 0;
     // no weight beside the smallest scores
     a.r.w[t * K + lane] = on && by != 0.0f ? v * by : 0.0f;
-    if (on) atomicAdd(&cnt[stage[lane].y], 1);
+    if (on) atomicAdd(&cnt[id], 1);
   }
 }
 
-// Bound on the error of a in fp32 where it is s and the logit x (sigmoid: two
-// parts in 2^23 of the exponential and |x| of 2^24 of its argument, halved, and
-// the inverse's; softmax: relative to the row's largest logit, and n roundings
-// of the sum), twice over, and of adding the bias.
-__device__ __forceinline__ float bound(float s, float x, float c, int n) {
-  return s * (fminf(fabsf(x), 104.0f) * 0x1p-23f + (float)n * 0x1p-24f) + fabsf(c) * 0x1p-23f;
+// Bounds on the error of c = a + b in fp32, twice what they have to be.
+//   sigmoid  of e = exp(-x): two parts in 2^23 and |x| parts in 2^24, of which
+//            s (1 - s) reaches s; the sum 1 + e, the inverse, and the addition of
+//            b.  s (1 - s) |x| is at most 0.28
+//   softmax  of exp(x - m): the same two; the sum of the row's in n roundings,
+//            and its terms' errors, which weighted by p are those of |x - m| = 7;
+//            p |x - m| is at most 0.4 times the largest p
+__device__ __forceinline__ float sigmoid_bound(float s, float x, float c) {
+  return s * ((1.0f - s) * (fminf(fabsf(x), 104.0f) * 0x1p-23f + 0x1p-21f) + 3 * 0x1p-23f) +
+         fabsf(c) * 0x1p-23f;
+}
+__device__ __forceinline__ float softmax_bound(float p, float d, float c, int n) {
+  return p * (fminf(fabsf(d), 104.0f) * 0x1p-23f + (float)(n + 30) * 0x1p-24f) +
+         fabsf(c) * 0x1p-23f;
+}
+
+// The values at or above `least` (V per lane, index col + i; NaN: none) side by
+// side, in the order of their indices; their count, of which more than 32 are
+// not written.
+template <int V>
+__device__ __forceinline__ int gather(const float c[V], int col, float least, int lane,
+                                      float *value, int32_t *index) {
+  int mine = 0;
+#pragma unroll
+  for (int i = 0; i < V; i++) mine += c[i] >= least;
+  int at = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, at, o);
+    if (lane >= o) at += u;
+  }
+  const int n = __shfl_sync(0xffffffffu, at, 31);
+  if (n > 32) return n;
+  at -= mine;
+#pragma unroll
+  for (int i = 0; i < V; i++)
+    if (c[i] >= least) {
+      value[at] = c[i];
+      index[at++] = col + i;
+    }
+  // what the comparisons by fours read behind them
+  if (lane < 4) value[n + lane] = __uint_as_float(0x7fffffffu);
+  __syncwarp();
+  return n;
+}
+
+// Places of a warp's n side-by-side values, largest first, equal ones in order:
+// each counts the ones before it.
+__device__ __forceinline__ int place(const float *value, int n, int lane, float mine) {
+  int rank = 0;
+  for (int j = 0; j < n; j += 4) {
+    const float4 o = *(const float4 *)(value + j);
+    rank += o.x > mine || (o.x == mine && j < lane);
+    rank += o.y > mine || (o.y == mine && j + 1 < lane);
+    rank += o.z > mine || (o.z == mine && j + 2 < lane);
+    rank += o.w > mine || (o.w == mine && j + 3 < lane);
+  }
+  return rank;
+}
+
+// The picks among n candidates by their values in 64 bits, into `index`; sigmoid
+// scores, which need no other logit.
+template <typename T>
+__device__ __noinline__ void refine_picks(const T *z, const float *bias, int K, int n,
+                                          const int32_t *from, uint64_t *keys, int32_t *index) {
+  const int lane = threadIdx.x & 31;
+  uint64_t mine = 0;
+  int id = 0;
+  if (lane < n) {
+    id = from[lane];
+    mine = order_key64(1.0 / (1.0 + exp(-(double)to_f(z[id]))) + (double)bias[id]);
+    keys[lane] = mine;
+  }
+  __syncwarp();
+  int rank = 0;
+  for (int j = 0; j < n; j++) {
+    const uint64_t o = keys[j];
+    rank += o > mine || (o == mine && j < lane);
+  }
+  if (lane < n && rank < K) index[rank] = id;
+  __syncwarp();
+}
+
+// The top groups where some values lie within `margin` of the last one's: those
+// groups by their values in 64 bits, from the elements that can be among a
+// group's two largest.  Lane g has group g's value and its second largest
+// element; line: the elements.  Returns the groups as bits.  Sigmoid scores.
+template <typename T>
+__device__ __noinline__ unsigned refine_groups(const SelectArgs &a, const T *z, const float *bias,
+                                               const float *line, uint64_t *best, float value,
+                                               float second, float last, float margin, float any) {
+  const int lane = threadIdx.x & 31, gs = a.r.E / a.groups;
+  const bool group = lane < a.groups, flagged = group && fabsf(value - last) <= margin;
+  const unsigned sure = __ballot_sync(0xffffffffu, group && value - last > margin);
+  uint64_t mine = 0;
+  if (flagged) {
+    uint64_t one = 0, two = 0;
+    const float least = second - 2.0f * any;
+    for (int i = 0; i < gs; i++) {
+      const int e = lane * gs + i;
+      if (!(line[e] >= least)) continue;
+      const uint64_t k =
+          order_key64(1.0 / (1.0 + exp(-(double)to_f(z[e]))) + (double)bias[e]);
+      if (k > one) {
+        two = one;
+        one = k;
+      } else if (k > two) {
+        two = k;
+      }
+    }
+    mine = a.sum_two && gs > 1 ? order_key64(key_value64(one) + key_value64(two)) : one;
+  }
+  if (group) best[lane] = mine;
+  __syncwarp();
+  int rank = __popc(sure);
+  for (int h = 0; h < a.groups; h++) {
+    const uint64_t o = best[h];
+    rank += o > mine || (o == mine && h < lane);
+  }
+  const unsigned in = __ballot_sync(0xffffffffu, flagged && rank < a.top_groups) | sure;
+  __syncwarp();
+  return in;
+}
+
+// A row's largest logit, and 1 / sum of its scores (0 where that is 0).
+template <typename T>
+__device__ __forceinline__ float row_max(const T *z, int E) {
+  float m = -INFINITY;
+  for (int e = threadIdx.x & 31; e < E; e += 32) m = fmaxf(m, to_f(z[e]));
+#pragma unroll
+  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  return m;
+}
+template <typename T>
+__device__ __forceinline__ float row_inverse(const T *z, int E, float m, bool sigmoid) {
+  float Z = 0.0f;
+  for (int e = threadIdx.x & 31; e < E; e += 32) Z += score(to_f(z[e]), m, sigmoid);
+  Z = warp_sum(Z);
+  return Z == 0.0f ? 0.0f : 1.0f / Z;
+}
+
+// A row's picks and weights, by 64-bit values.
+template <typename T>
+__device__ __noinline__ void again_exact(const SelectArgs &a, const T *z, uint64_t *row,
+                                         uint64_t *best, int32_t *index, int64_t t, int32_t *cnt) {
+  select_exact(a, z, row, best, index);
+  const float m = row_max(z, a.r.E);
+  const float inv = a.r.sigmoid || a.renormalize ? 0.0f : row_inverse(z, a.r.E, m, false);
+  const int id = (threadIdx.x & 31) < a.r.K ? index[threadIdx.x & 31] : 0;
+  write_picks(a, id, to_f(z[id]), t, true, m, inv, cnt);
+  __syncwarp();
 }
 
 // Rows of up to 32 V logits, a warp to a token, lane l holding columns l V to
-// l V + V - 1.
+// l V + V - 1.  A row to be done again gets the id -1 as its first pick and its
+// turn after the warp's last row: a call within the loop would take the
+// registers of half the warps.
 template <typename T, int V>
-__global__ void __launch_bounds__(kWarps * 32) select_kernel(SelectArgs a, bool vec) {
+__global__ void __launch_bounds__(kWarps * 32, V <= 8 ? 4 : 2) select_kernel(SelectArgs a, bool vec) {
   pdl_wait();
   pdl_launch_dependents();
   extern __shared__ __align__(16) uint64_t words[];
   const int E = a.r.E, K = a.r.K, G = a.groups;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, col = lane * V;
-  uint64_t *row = words + (size_t)warp * E;                         // [kWarps, E]
-  uint64_t *best = words + (size_t)kWarps * E + (size_t)warp * G;   // [kWarps, G]
-  uint2 *stage = (uint2 *)(words + (size_t)kWarps * (E + G)) + warp * 64;
-  uint2 *few = stage + 32;
-  int32_t *cnt = (int32_t *)(words + (size_t)kWarps * (E + G + 64));  // [E]
-  const int r = blockIdx.y, n = a.r.ntok[r];
+  uint64_t *row = words + (size_t)warp * (E + 32);                        // [kWarps, E + 32]
+  uint64_t *best = words + (size_t)kWarps * (E + 32) + (size_t)warp * G;  // [kWarps, G]
+  float *bias = (float *)(words + (size_t)kWarps * (E + 32 + G));         // [32 V], 0 past E
+  float *value = bias + 32 * V + warp * kScratch;                         // 36 candidates
+  int32_t *from = (int32_t *)(value + 36), *index = from + 32;            // theirs, the picks
+  int32_t *cnt = (int32_t *)(bias + 32 * V + kWarps * kScratch);          // [E]
+  const int r = blockIdx.y, n = min(a.r.ntok[r], a.r.S);
   const bool grouped = a.top_groups < G, sigmoid = a.r.sigmoid;
   const int gs = E / G;
+  const float none = __uint_as_float(0x7fffffffu);  // left out: no comparison holds
+  for (int e = threadIdx.x; e < 32 * V; e += blockDim.x)
+    bias[e] = a.bias && e < E ? __ldg(a.bias + e) : 0.0f;
   for (int e = threadIdx.x; e < E; e += blockDim.x) cnt[e] = 0;
   __syncthreads();
-  float sum[V], b[V];
+  float sum[V];
   float most = 0.0f;  // largest finite bias
 #pragma unroll
   for (int i = 0; i < V; i++) {
     sum[i] = 0.0f;
-    b[i] = a.bias && col + i < E ? __ldg(a.bias + col + i) : 0.0f;
-    if (fabsf(b[i]) < INFINITY) most = fmaxf(most, fabsf(b[i]));
+    const float b = fabsf(bias[col + i]);
+    if (b < INFINITY) most = fmaxf(most, b);
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-  // lanes of a group in the search for its best, a power of two
-  int per = 1;
-  while (2 * per * G <= 32) per *= 2;
-  int first[V];  // the first lane of a column's group
-#pragma unroll
-  for (int i = 0; i < V; i++) first[i] = ((col + i) / gs * per) & 31;
-  const int gl = lane / per, sub = lane & (per - 1), turns = (gs + per - 1) / per;
+  // Lanes that search a group for its best, a power of two: those that hold its
+  // columns where these are a lane's whole ones, else as many as there are, which
+  // read the columns from shared memory.
+  const int whole = gs % V == 0 ? gs / V : 0;
+  const bool held = whole && (whole & (whole - 1)) == 0 && whole <= 32;
+  int per = 0;  // its logarithm
+  while (held ? 1 << per < whole : 2 * G << per <= 32) per++;
+  const int gl = lane >> per, sub = lane & ((1 << per) - 1), turns = (gs + (1 << per) - 1) >> per;
   // whether the whole row's scores are wanted, or logits are enough
   const bool scores = a.r.part_p || a.bias || (grouped && a.sum_two) ||
                       (!sigmoid && !a.renormalize);
   const int need = a.bias ? K + 1 : K;  // the first that is not picked, too
-  const int roundings = sigmoid ? 8 : V + 30;
-  for (int s = blockIdx.x * kWarps + warp; s < a.r.S; s += gridDim.x * kWarps) {
+  const int step = gridDim.x * kWarps, begin = blockIdx.x * kWarps + warp;
+  for (int s = begin; s < a.r.S; s += step) {
     const int64_t t = (int64_t)r * a.r.S + s;
     if (s >= n) {
-      write_picks(a, stage, t, false, 0.0f, 0.0f, cnt);
+      write_picks(a, 0, 0.0f, t, false, 0.0f, 0.0f, cnt);
       continue;
     }
     const T *zt = (const T *)a.r.logits + t * E;
-    float z[V], p[V];
-    load_row<V>(zt, col, E, vec, z);
-    float m = z[0];
+    float c[V], p[V];
+    load_row<V>(zt, col, E, vec, c);
+    float m = 0.0f, inv = 0.0f;
+    if (!sigmoid) {
+      m = c[0];
 #pragma unroll
-    for (int i = 1; i < V; i++) m = fmaxf(m, z[i]);
+      for (int i = 1; i < V; i++) m = fmaxf(m, c[i]);
 #pragma unroll
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float inv = 0.0f;
+      for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    }
     if (scores) {
       float Z = 0.0f;
 #pragma unroll
       for (int i = 0; i < V; i++) {
-        p[i] = score(z[i], m, sigmoid);  // -inf past the row's end: 0
+        p[i] = score(c[i], m, sigmoid);  // -inf past the row's end: 0
         Z += p[i];
       }
-      Z = warp_sum(Z);
-      inv = Z == 0.0f ? 0.0f : 1.0f / Z;
+      if (a.r.part_p || !sigmoid) {
+        Z = warp_sum(Z);
+        inv = Z == 0.0f ? 0.0f : 1.0f / Z;
+      }
+    }
+    if (a.r.part_p) {
+#pragma unroll
+      for (int i = 0; i < V; i++) sum[i] += p[i] * inv;
     }
     const float unit = sigmoid ? 1.0f : inv;  // from scores to what selects
-    uint32_t key[V];
+    bool nan = false;
 #pragma unroll
-    for (int i = 0; i < V; i++)
-      key[i] = col + i >= E ? 0u : order_key(a.bias ? __fadd_rn(p[i] * unit, b[i]) : z[i]);
+    for (int i = 0; i < V; i++) {
+      if (a.bias) c[i] = __fadd_rn(p[i] * unit, bias[col + i]);
+      if (col + i < E)
+        nan |= c[i] != c[i];
+      else
+        c[i] = none;
+    }
+    bool again = need > 32 || (grouped && G > 32) || __any_sync(0xffffffffu, nan);
     // a bound for every value of the row
-    const float any = bound(unit, sigmoid ? fmaxf(m, 0.3f) : 0.4f, 1.0f + most, roundings);
-    bool again = need > 32 || G > 32;
+    const float any = sigmoid ? 5.0f * 0x1p-23f + most * 0x1p-23f + 0x1p-23f
+                              : softmax_bound(unit, 0.4f, 1.0f + most, V);
     if (grouped && !again) {
       // groups are compared by logits where these are what selects
-      const bool exact = !a.bias && !a.sum_two;
-      float *line = (float *)row;
-      bool nan = false;
-#pragma unroll
-      for (int i = 0; i < V; i++)
-        if (col + i < E) {
-          const float c = a.bias ? key_value(key[i]) : exact ? z[i] : p[i] * unit;
-          nan |= c != c;
-          line[col + i] = c;
-        }
-      __syncwarp();
+      const bool logits = !a.bias && !a.sum_two, shares = !a.bias && a.sum_two;
       float one = -INFINITY, two = -INFINITY;
-      if (gl < G)
-        for (int i = 0; i < turns; i++) {
-          // every group starts elsewhere, on banks of its own
-          int q = i + gl % turns;
-          if (q >= turns) q -= turns;
-          const int e = q * per + sub;
-          if (e < gs) {
-            const float c = line[gl * gs + e];
-            two = fmaxf(two, fminf(one, c));
-            one = fmaxf(one, c);
+      auto take = [&](float x) {
+        two = fmaxf(two, fminf(one, x));
+        one = fmaxf(one, x);
+      };
+      float *line = (float *)row;
+      auto spread = [&] {
+#pragma unroll
+        for (int i = 0; i < V; i++)
+          if (col + i < E) line[col + i] = shares ? p[i] * unit : c[i];
+        __syncwarp();
+      };
+      if (held) {
+#pragma unroll
+        for (int i = 0; i < V; i++) take(shares ? p[i] * unit : c[i]);
+      } else {
+        spread();
+        if (gl < G)
+          for (int i = 0; i < turns; i++) {
+            // every group starts elsewhere, on banks of its own
+            int q = i + gl % turns;
+            if (q >= turns) q -= turns;
+            q = (q << per) + sub;
+            if (q < gs) take(line[gl * gs + q]);
           }
-        }
-      for (int o = 1; o < per; o <<= 1) {
+        __syncwarp();
+      }
+      for (int o = 1; o < 1 << per; o <<= 1) {
         const float x = __shfl_xor_sync(0xffffffffu, one, o);
         const float y = __shfl_xor_sync(0xffffffffu, two, o);
         two = fmaxf(fmaxf(two, y), fminf(one, x));
@@ -269,72 +440,138 @@ __global__ void __launch_bounds__(kWarps * 32) select_kernel(SelectArgs a, bool 
       }
       const float v = a.sum_two && gs > 1 ? one + two : one;
       uint32_t left = gl < G && sub == 0 ? order_key(v) : 0u, last = 0u;
-      unsigned in = 0;  // the chosen groups' lanes
+      unsigned in = 0;  // the chosen groups
       for (int k = 0; k < a.top_groups; k++) {
         last = __reduce_max_sync(0xffffffffu, left);
         const int src = __ffs(__ballot_sync(0xffffffffu, left == last)) - 1;
-        in |= 1u << src;
+        in |= 1u << (src >> per);
         if (lane == src) left = 0u;
       }
       const float lowest = key_value(last);
       const float rest = key_value(__reduce_max_sync(0xffffffffu, left));
-      again = __any_sync(0xffffffffu, nan) ||
-              (!exact && !(lowest - rest > 4.0f * any + fabsf(lowest) * 0x1p-22f));
+      const float margin = 4.0f * any + fabsf(lowest) * 0x1p-21f;
+      if (!logits && !(lowest - rest > margin)) {
+        again = true;
+        if (sigmoid && fabsf(lowest) < INFINITY && !__any_sync(0xffffffffu, v != v)) {
+          if (held) spread();
+          const int src = lane << per & 31;
+          in = refine_groups(a, zt, bias, line, best, __shfl_sync(0xffffffffu, v, src),
+                             __shfl_sync(0xffffffffu, gs > 1 ? two : one, src), lowest, margin,
+                             any);
+          again = false;
+        }
+      }
+      if (held) {
+        const bool mine = in >> gl & 1u;
 #pragma unroll
-      for (int i = 0; i < V; i++)
-        if (!(in >> first[i] & 1u)) key[i] = 0u;
-      __syncwarp();
+        for (int i = 0; i < V; i++) c[i] = mine ? c[i] : none;
+      } else {
+        int g = col / gs, at = col - g * gs;  // the column's group and place in it
+#pragma unroll
+        for (int i = 0; i < V; i++) {
+          if (!(in >> (g & 31) & 1u)) c[i] = none;
+          if (++at == gs) {
+            at = 0;
+            g++;
+          }
+        }
+      }
     }
     if (!again) {
-      bool done = V >= 4 && pick_few<V>(key, col, need, lane, few, stage);
-      for (int k = 0; k < need && !done; k++) {
-        uint32_t top = key[0];
+      // The need-th largest of the lanes' largest is at most the need-th largest
+      // value, so the few at or above it hold the picks.
+      float top = c[0];
 #pragma unroll
-        for (int i = 1; i < V; i++) top = max(top, key[i]);
-        const uint32_t all = __reduce_max_sync(0xffffffffu, top);
-        const int src = __ffs(__ballot_sync(0xffffffffu, top == all)) - 1;
-        bool look = lane == src;
-#pragma unroll
-        for (int i = 0; i < V; i++)
-          if (look && key[i] == all) {
-            key[i] = 0u;
-            stage[k] = make_uint2(all, col + i);
-            look = false;
-          }
-        // fewer candidates than picks and one: nothing is left out
-        if (all == 0u && lane == 0) stage[k] = make_uint2(0u, 0u);
+      for (int i = 1; i < V; i++) top = fmaxf(top, c[i]);
+      uint32_t lead = top == top ? order_key(top) : 0u, least = 0u;
+      for (int k = 0; k < need; k++) {
+        least = __reduce_max_sync(0xffffffffu, lead);
+        if (lead == least) lead = 0u;  // equal ones together: only more qualify
       }
-      __syncwarp();
+      const int count = gather<V>(c, col, least ? key_value(least) : -INFINITY, lane, value, from);
+      int id = 0;
+      float own = none;  // this lane's pick's value
+      if (count <= 32) {
+        const float mine = lane < count ? value[lane] : none;
+        const int rank = place(value, count, lane, mine), of = lane < count ? from[lane] : 0;
+        __syncwarp();
+        if (lane >= count && lane < need) value[lane] = none;
+        if (lane < count && rank < need) {
+          value[rank] = mine;
+          index[rank] = of;
+        }
+        __syncwarp();
+        if (lane < need) {
+          own = value[lane];
+          id = own == own ? index[lane] : 0;
+        }
+      } else {
+        for (int k = 0; k < need; k++) {
+          float x = none;
+          int at = 0;
+#pragma unroll
+          for (int i = V - 1; i >= 0; i--)
+            if (c[i] == c[i] && !(c[i] < x)) {
+              x = c[i];
+              at = col + i;
+            }
+          const uint32_t key = x == x ? order_key(x) : 0u;
+          const uint32_t all = __reduce_max_sync(0xffffffffu, key);
+          const int src = __ffs(__ballot_sync(0xffffffffu, key == all)) - 1;
+          const float xs = __shfl_sync(0xffffffffu, x, src);
+          const int is = __shfl_sync(0xffffffffu, at, src);
+          if (lane == k && all) {
+            own = xs;
+            id = is;
+          }
+#pragma unroll
+          for (int i = 0; i < V; i++)
+            if (all && col + i == is) c[i] = none;
+        }
+      }
+      float x = to_f(zt[id]);
       if (a.bias) {
-        // from the keys of c to those of the logits; neighbours further apart
-        // than their errors
-        const uint2 q = lane < need ? stage[lane] : make_uint2(0u, 0u);
-        const bool there = q.x != 0u;
-        const int id = there && q.y < (uint32_t)E ? (int)q.y : 0;
-        const float c = key_value(q.x), x = to_f(zt[id]), bx = __ldg(a.bias + id);
-        const float as = score(x, m, sigmoid) * unit;
-        const float d = bound(as, sigmoid ? x : x - m, c, roundings);
-        const float cn = __shfl_down_sync(0xffffffffu, c, 1), dn = __shfl_down_sync(0xffffffffu, d, 1);
-        const float xn = __shfl_down_sync(0xffffffffu, x, 1), bn = __shfl_down_sync(0xffffffffu, bx, 1);
-        const bool next = __shfl_down_sync(0xffffffffu, there, 1);
+        // neighbours have to lie further apart than their errors
+        const float bx = bias[id], as = score(x, m, sigmoid) * unit;
+        const float d = sigmoid ? sigmoid_bound(as, x, own) : softmax_bound(as, x - m, own, V);
+        const float cn = __shfl_down_sync(0xffffffffu, own, 1);
+        const float dn = __shfl_down_sync(0xffffffffu, d, 1);
+        const float xn = __shfl_down_sync(0xffffffffu, x, 1);
+        const float bn = __shfl_down_sync(0xffffffffu, bx, 1);
         bool close = false;
         if (lane < K - 1)
-          close = !(c - cn > d + dn) && !(x == xn && bx == bn);
+          close = !(own - cn > d + dn) && !(x == xn && bx == bn);
         else if (lane == K - 1)
-          close = next && !(c - cn > d + any);
+          close = cn == cn && !(own - cn > d + any);
         again = __any_sync(0xffffffffu, close);
-        __syncwarp();
-        if (lane < K) stage[lane] = make_uint2(order_key(x), q.y);
-        __syncwarp();
+        if (again && count <= 32 && sigmoid) {
+          // what may be a pick lies at most twice the bound below the last one
+          const float last = __shfl_sync(0xffffffffu, own, K - 1);
+          const float low = last - 2.0f * any - fabsf(last) * 0x1p-22f;
+          if (fabsf(low) < INFINITY) {
+            const int more = gather<V>(c, col, low, lane, value, from);
+            if (more <= 32) {
+              refine_picks(zt, bias, K, more, from, row, index);
+              id = lane < K ? index[lane] : 0;
+              x = to_f(zt[id]);
+              again = false;
+            }
+          }
+        }
       }
+      if (!again) write_picks(a, id, x, t, true, m, inv, cnt);
     }
-    if (again) select_exact(a, zt, row, best, stage);
-    write_picks(a, stage, t, true, m, inv, cnt);
-    if (a.r.part_p) {
-#pragma unroll
-      for (int i = 0; i < V; i++) sum[i] += p[i] * inv;
-    }
+    if (again && lane == 0) a.r.topk[t * K] = -1;
     __syncwarp();
+  }
+  // the rows to be done again, found 32 at a time
+  for (int s0 = begin; s0 < n; s0 += 32 * step) {
+    const int64_t mine = (int64_t)s0 + (int64_t)lane * step;
+    const bool again = mine < n && __ldcg(a.r.topk + ((int64_t)r * a.r.S + mine) * K) < 0;
+    for (unsigned todo = __ballot_sync(0xffffffffu, again); todo; todo &= todo - 1) {
+      const int64_t t = (int64_t)r * a.r.S + s0 + (int64_t)(__ffs(todo) - 1) * step;
+      again_exact<T>(a, (const T *)a.r.logits + t * E, row, best, index, t, cnt);
+    }
   }
   __syncthreads();
   float *acc = (float *)words;  // [kWarps, E], over the rows
@@ -356,8 +593,8 @@ __global__ void __launch_bounds__(kWarps * 32) select_long_kernel(SelectArgs a) 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint64_t *row = words + (size_t)warp * E;
   uint64_t *best = words + (size_t)warps * E + (size_t)warp * G;
-  uint2 *stage = (uint2 *)(words + (size_t)warps * (E + G)) + warp * 32;
-  float *acc = (float *)(words + (size_t)warps * (E + G + 32));  // [warps, E]
+  int32_t *index = (int32_t *)(words + (size_t)warps * (E + G)) + warp * 32;
+  float *acc = (float *)(words + (size_t)warps * (E + G + 16));  // [warps, E]
   int32_t *cnt = (int32_t *)(acc + (size_t)warps * E);           // [E]
   float *mine = acc + (size_t)warp * E;
   const int r = blockIdx.y, n = a.r.ntok[r];
@@ -367,19 +604,14 @@ __global__ void __launch_bounds__(kWarps * 32) select_long_kernel(SelectArgs a) 
   for (int s = blockIdx.x * warps + warp; s < a.r.S; s += gridDim.x * warps) {
     const int64_t t = (int64_t)r * a.r.S + s;
     if (s >= n) {
-      write_picks(a, stage, t, false, 0.0f, 0.0f, cnt);
+      write_picks(a, 0, 0.0f, t, false, 0.0f, 0.0f, cnt);
       continue;
     }
     const T *z = (const T *)a.r.logits + t * E;
-    select_exact(a, z, row, best, stage);
-    float m = -INFINITY, Z = 0.0f;
-    for (int e = lane; e < E; e += 32) m = fmaxf(m, to_f(z[e]));
-#pragma unroll
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    for (int e = lane; e < E; e += 32) Z += score(to_f(z[e]), m, a.r.sigmoid);
-    Z = warp_sum(Z);
-    const float inv = Z == 0.0f ? 0.0f : 1.0f / Z;
-    write_picks(a, stage, t, true, m, inv, cnt);
+    select_exact(a, z, row, best, index);
+    const int id = lane < a.r.K ? index[lane] : 0;
+    const float m = row_max(z, E), inv = row_inverse(z, E, m, a.r.sigmoid);
+    write_picks(a, id, to_f(z[id]), t, true, m, inv, cnt);
     if (a.r.part_p)
       for (int e = lane; e < E; e += 32) mine[e] += score(to_f(z[e]), m, a.r.sigmoid) * inv;
     __syncwarp();
@@ -415,9 +647,11 @@ constexpr int kInRegisters = 512;  // longest row in registers
 int long_warps(int E) { return E <= 1024 ? 8 : E <= 2048 ? 4 : 2; }
 
 size_t select_smem(int E, int G) {
-  if (E <= kInRegisters) return ((size_t)kWarps * (E + G + 64)) * 8 + (size_t)E * 4;
+  if (E <= kInRegisters)  // the bias in whole lanes' columns, at most 512
+    return ((size_t)kWarps * (E + 32 + G)) * 8 +
+           (size_t)(E + kInRegisters + kWarps * kScratch) * 4;
   const size_t w = long_warps(E);
-  return w * (E + G + 32) * 8 + (w + 1) * E * 4;
+  return w * (E + G + 16) * 8 + (w + 1) * E * 4;
 }
 
 template <typename T>
