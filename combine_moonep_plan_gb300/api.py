@@ -12,7 +12,9 @@ every step runs in libmoonep's kernels.
 """
 from __future__ import annotations
 
+import array
 import ctypes
+import operator
 
 import torch
 
@@ -77,22 +79,31 @@ def _one_of(t, name, dtypes):
     return t.dtype
 
 
+_kind, _place = operator.attrgetter("dtype"), torch.Tensor.get_device
+_ptr, _numel, _whole = torch.Tensor.data_ptr, torch.Tensor.numel, torch.Tensor.is_contiguous
+
+
 def _check_list(tensors, name, dtypes, sizes):
-    """Contiguous CUDA tensors of one type out of `dtypes` (returned), of `sizes`
-    elements where given."""
-    if sizes is not None and len(tensors) != len(sizes):
-        raise ValueError(f"{name}: expected {len(sizes)} tensors, got {len(tensors)}")
-    dtype = _one_of(tensors[0], f"{name}[0]", dtypes) if tensors else dtypes[0]
-    for t in tensors:
-        if t.dtype is not dtype:
-            raise TypeError(f"{name}: expected all {dtype}, got {t.dtype}")
-        if not (t.is_cuda and t.is_contiguous()):
-            raise ValueError(f"{name}: must be contiguous CUDA tensors")
-    if sizes is not None:
-        for t, n in zip(tensors, sizes):
-            if t.numel() != n:
-                raise ValueError(f"{name}: expected a tensor of {n} elements, got {t.numel()}")
-    return dtype
+    """Contiguous CUDA tensors of one type out of `dtypes`, of `sizes` elements
+    where given: (type, addresses, sizes).  Every look at a tensor costs a
+    twentieth of a microsecond and there may be hundreds, so each property is
+    asked of all of them at a time."""
+    count = list(map(_numel, tensors))
+    if sizes is not None and (len(count) != len(sizes) or count != list(sizes)):
+        raise ValueError(f"{name}: expected tensors of {list(sizes)[:8]}... elements, got "
+                         f"{count[:8]}...")
+    kinds = set(map(_kind, tensors)) or {dtypes[0]}
+    if len(kinds) > 1:
+        raise TypeError(f"{name}: expected one type for all, got {sorted(map(str, kinds))}")
+    dtype = kinds.pop()
+    if dtype not in dtypes:
+        raise TypeError(f"{name}: expected one of {dtypes}, got {dtype}")
+    places = set(map(_place, tensors))
+    if len(places) > 1 or -1 in places:
+        raise ValueError(f"{name}: must be CUDA tensors of one device")
+    if not all(map(_whole, tensors)):
+        raise ValueError(f"{name}: must be contiguous")
+    return dtype, list(map(_ptr, tensors)), count
 
 
 def _check_rows(t, name, rows, cols):
@@ -223,6 +234,13 @@ class GatedCheckpoint:
         views = tuple(self._store[at[k]:at[k + 1]].view(rows, F if k < 2 else F // 32)
                       for k in range(4))
         return views[i]
+
+
+def _words(ctype, values):
+    """Host array of 64-bit words for the C ABI."""
+    if not values:
+        return (ctype * 0)()
+    return (ctype * len(values)).from_buffer(array.array("q", values))
 
 
 class AdamWState:
@@ -842,26 +860,27 @@ class Buffer:
         params = list(params)
         if bits not in (32, 8):
             raise ValueError(f"bits: expected 32 or 8, got {bits}")
-        _check_list(params, "params", _FLOATS, None)
+        _, _, sizes = _check_list(params, "params", _FLOATS, None)
         device = params[0].device if params else torch.device("cuda", torch.cuda.current_device())
-        return AdamWState(self, [t.numel() for t in params], bits, device)
+        return AdamWState(self, sizes, bits, device)
 
     def grad_norm(self, grads, out: torch.Tensor | None = None) -> torch.Tensor:
         """The 2-norm [1] fp32 of all tensors in `grads` together (all fp32 or
         all bf16), summed in a fixed order."""
         grads = list(grads)
-        dtype = _check_list(grads, "grads", _FLOATS, None)
+        dtype, ptrs, sizes = _check_list(grads, "grads", _FLOATS, None)
         lib = _lib.load()
         n = lib.moonep_grad_norm_workspace(self._ctx)
         dev = grads[0].device if grads else torch.device("cuda", torch.cuda.current_device())
         if out is None:
             out = torch.empty(1, dtype=torch.float32, device=dev)
-        op = _check_tensor(out, "norm", torch.float32, (1,))
+            op = out.data_ptr()
+        else:
+            op = _check_tensor(out, "norm", torch.float32, (1,))
         work = torch.empty(n // 8, dtype=torch.float64, device=dev)
         check(lib.moonep_grad_norm(
-            self._ctx, len(grads), _lib.ptr_array([t.data_ptr() for t in grads]),
-            (ctypes.c_int64 * len(grads))(*[t.numel() for t in grads]), dtype == torch.bfloat16,
-            work.data_ptr(), op, _stream()), "moonep_grad_norm")
+            self._ctx, len(grads), _words(ctypes.c_void_p, ptrs), _words(ctypes.c_int64, sizes),
+            dtype == torch.bfloat16, work.data_ptr(), op, _stream()), "moonep_grad_norm")
         return out
 
     def adamw(self, params, grads, state: AdamWState, lr, step, betas=(0.9, 0.999),
@@ -879,8 +898,8 @@ class Buffer:
           weights    for fp32 params: bf16 tensors (or None) that receive the
                      rounded parameters, e.g. the experts' rows W[:E]"""
         params, grads = list(params), list(grads)
-        pt = _check_list(params, "params", _FLOATS, state.sizes)
-        gt = _check_list(grads, "grads", _FLOATS, state.sizes)
+        pt, pp, _ = _check_list(params, "params", _FLOATS, state.sizes)
+        gt, gp, _ = _check_list(grads, "grads", _FLOATS, state.sizes)
         wp = None
         if weights is not None:
             if pt != torch.float32:
@@ -888,14 +907,15 @@ class Buffer:
             weights = list(weights)
             if len(weights) != len(params):
                 raise ValueError(f"weights: expected {len(params)} tensors")
-            for t, n in zip(weights, state.sizes):
-                if t is not None:
-                    _check_list([t], "weights", (torch.bfloat16,), (n,))
-            wp = _lib.ptr_array([0 if t is None else t.data_ptr() for t in weights])
-        pp = [t.data_ptr() for t in params]
-        if len(set(pp)) < len(pp) and len({p for p, n in zip(pp, state.sizes) if n}) < \
-                sum(n > 0 for n in state.sizes):
-            raise ValueError("params: a tensor is given twice")
+            given = [(t, n) for t, n in zip(weights, state.sizes) if t is not None]
+            _, to, _ = _check_list([t for t, _ in given], "weights", (torch.bfloat16,),
+                                   [n for _, n in given])
+            to = iter(to)
+            wp = _words(ctypes.c_void_p, [0 if t is None else next(to) for t in weights])
+        if len(set(pp)) < len(pp):
+            used = [p for p, n in zip(pp, state.sizes) if n]
+            if len(set(used)) < len(used):
+                raise ValueError("params: a tensor is given twice")
         if (norm is None) != (max_norm is None):
             raise ValueError("norm and max_norm go together")
         cfg = _lib.MoonepAdamwConfig(
@@ -918,8 +938,8 @@ class Buffer:
         m, v, ms, vs = state._pointers()
         check(_lib.load().moonep_adamw(
             self._ctx, ctypes.byref(cfg), len(params), state._c_sizes,
-            _lib.ptr_array(pp), _lib.ptr_array([t.data_ptr() for t in grads]), m, v, ms, vs, wp,
-            _stream()), "moonep_adamw")
+            _words(ctypes.c_void_p, pp), _words(ctypes.c_void_p, gp), m, v, ms, vs, wp, _stream()),
+            "moonep_adamw")
 
     # ------------------------------------------------- rank-local forms
     # The per-rank shape of the path when each EP rank is its own GPU: one

@@ -568,7 +568,8 @@ int moonep_gated_act_backward(moonep_ctx *ctx, const int32_t *cu_seqlens,
  * in device memory.  g is a host array of n_tensors device pointers (fp32, or
  * bf16 when g_bf16; any element alignment), sizes their elements.  Squares are
  * taken in fp32 (below 2^-126 they lose bits, from 2^128 on they are
- * infinite), sums of eight in fp32 and the rest in 64 bits, in a fixed order.
+ * infinite), sums of eight in fp32 and the rest in 45 bits or more, in a fixed
+ * order.
  * workspace: moonep_grad_norm_workspace(ctx) bytes of device memory, 8-byte
  * aligned, the call's own until it has run. */
 size_t moonep_grad_norm_workspace(const moonep_ctx *ctx);
@@ -581,7 +582,8 @@ int moonep_grad_norm(moonep_ctx *ctx, int n_tensors, const void *const *g,
  *   m = beta1 m + (1 - beta1) g'    v = beta2 v + (1 - beta2) g'^2
  *   p = p (1 - lr wd) - lr / (1 - beta1^step) m /
  *                       (sqrt(v) / sqrt(1 - beta2^step) + eps)
- * in fp32.  When norm[0] is not finite the call changes nothing.
+ * in fp32 (a v below 2^-126 counts as 0 beside eps).  When norm[0] is not finite
+ * the call changes nothing.  No two tensors overlap.
  *   p, g     n_tensors host arrays of device pointers, fp32 or bf16 (one type
  *            per call each), any element alignment; sizes: elements, >= 0
  *   m, v     bits 32: fp32; bits 8: codes, uint8, with ms, vs their scales;
