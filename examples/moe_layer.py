@@ -33,6 +33,7 @@ class MoELayer:
         self.buf = Buffer(H=H, **kw)
         self.R, self.S, self.H, self.F, self.E, self.K = R, S, H, F, E, K
         self.scoring = scoring
+        self.selection = {}  # the router's bias, groups and weights' form, where not plain
         # a token's record: its codes, its scales, up to whole 16-byte vectors.
         # The second Buffer moves records as rows of bf16-sized elements; plans
         # do not depend on the row length, so both share one.
@@ -54,7 +55,7 @@ class MoELayer:
         s = SimpleNamespace(hidden=hidden)
         s.logits = hidden.float() @ self.router.T
         s.route = buf.route(s.logits, scoring=self.scoring, balance=balance,
-                            num_tokens=num_tokens)
+                            num_tokens=num_tokens, **self.selection)
         s.plan = buf.plan(s.route.topk, s.route.tokens_per_expert)
         s.cu = s.plan.cu_seqlens
         weights = (self.gate, self.up, self.down)
@@ -100,7 +101,7 @@ class MoELayer:
     def backward(self, s, d_out, d_loss=None):
         """d_out [R, S, H] bf16 -> (d_router [E, H], d_hidden [R, S, H] fp32)."""
         buf, n = self.buf, self.R * self.buf.NvS
-        d_y, _, _, _ = buf.dispatch(d_out, plan=s.plan)
+        s.d_y = d_y = buf.dispatch(d_out, plan=s.plan)[0]
         zeros = lambda c: torch.zeros(n, c, device="cuda")  # noqa: E731
         s.d_act = self._back_product(d_y, self.down, s.cu, zeros(self.F)).bfloat16()
         s.d_gate, s.d_up, s.d_weights_nvs = buf.gated_act_backward(s.checkpoint, s.d_act, s.cu,
