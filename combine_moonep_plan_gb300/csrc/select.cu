@@ -312,7 +312,7 @@ __device__ __noinline__ void again_exact(const SelectArgs &a, const T *z, uint64
 // turn after the warp's last row: a call within the loop would take the
 // registers of half the warps.
 template <typename T, int V>
-__global__ void __launch_bounds__(kWarps * 32, V <= 8 ? 4 : 2) select_kernel(SelectArgs a, bool vec) {
+__global__ void __launch_bounds__(kWarps * 32, V <= 12 ? 4 : 2) select_kernel(SelectArgs a, bool vec) {
   pdl_wait();
   pdl_launch_dependents();
   extern __shared__ __align__(16) uint64_t words[];
@@ -334,11 +334,13 @@ __global__ void __launch_bounds__(kWarps * 32, V <= 8 ? 4 : 2) select_kernel(Sel
   __syncthreads();
   float sum[V];
   float most = 0.0f;  // largest finite bias
+  bool odd = false;   // one is a NaN
 #pragma unroll
   for (int i = 0; i < V; i++) {
     sum[i] = 0.0f;
     const float b = fabsf(bias[col + i]);
     if (b < INFINITY) most = fmaxf(most, b);
+    odd |= b != b;
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
@@ -354,6 +356,7 @@ __global__ void __launch_bounds__(kWarps * 32, V <= 8 ? 4 : 2) select_kernel(Sel
   const bool scores = a.r.part_p || a.bias || (grouped && a.sum_two) ||
                       (!sigmoid && !a.renormalize);
   const int need = a.bias ? K + 1 : K;  // the first that is not picked, too
+  const bool full = E == 32 * V;
   const int step = gridDim.x * kWarps, begin = blockIdx.x * kWarps + warp;
   for (int s = begin; s < a.r.S; s += step) {
     const int64_t t = (int64_t)r * a.r.S + s;
@@ -364,7 +367,7 @@ __global__ void __launch_bounds__(kWarps * 32, V <= 8 ? 4 : 2) select_kernel(Sel
     const T *zt = (const T *)a.r.logits + t * E;
     float c[V], p[V];
     load_row<V>(zt, col, E, vec, c);
-    float m = 0.0f, inv = 0.0f;
+    float m = 0.0f, inv = 0.0f, Z = 0.0f;
     if (!sigmoid) {
       m = c[0];
 #pragma unroll
@@ -372,13 +375,14 @@ __global__ void __launch_bounds__(kWarps * 32, V <= 8 ? 4 : 2) select_kernel(Sel
 #pragma unroll
       for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     }
+    bool nan = false;
     if (scores) {
-      float Z = 0.0f;
 #pragma unroll
       for (int i = 0; i < V; i++) {
         p[i] = score(c[i], m, sigmoid);  // -inf past the row's end: 0
         Z += p[i];
       }
+      nan = Z != Z || odd;  // a NaN among the lane's scores, or its biases
       if (a.r.part_p || !sigmoid) {
         Z = warp_sum(Z);
         inv = Z == 0.0f ? 0.0f : 1.0f / Z;
@@ -389,14 +393,17 @@ __global__ void __launch_bounds__(kWarps * 32, V <= 8 ? 4 : 2) select_kernel(Sel
       for (int i = 0; i < V; i++) sum[i] += p[i] * inv;
     }
     const float unit = sigmoid ? 1.0f : inv;  // from scores to what selects
-    bool nan = false;
+    if (a.bias) {
 #pragma unroll
-    for (int i = 0; i < V; i++) {
-      if (a.bias) c[i] = __fadd_rn(p[i] * unit, bias[col + i]);
-      if (col + i < E)
-        nan |= c[i] != c[i];
-      else
-        c[i] = none;
+      for (int i = 0; i < V; i++) c[i] = __fmaf_rn(p[i], unit, bias[col + i]);
+    } else if (!scores) {
+#pragma unroll
+      for (int i = 0; i < V; i++) nan |= c[i] != c[i];
+    }
+    if (!full) {
+#pragma unroll
+      for (int i = 0; i < V; i++)
+        if (col + i >= E) c[i] = none;
     }
     bool again = need > 32 || (grouped && G > 32) || __any_sync(0xffffffffu, nan);
     // a bound for every value of the row
@@ -417,9 +424,12 @@ __global__ void __launch_bounds__(kWarps * 32, V <= 8 ? 4 : 2) select_kernel(Sel
           if (col + i < E) line[col + i] = shares ? p[i] * unit : c[i];
         __syncwarp();
       };
-      if (held) {
+      if (held && !shares) {
 #pragma unroll
-        for (int i = 0; i < V; i++) take(shares ? p[i] * unit : c[i]);
+        for (int i = 0; i < V; i++) take(c[i]);
+      } else if (held) {
+#pragma unroll
+        for (int i = 0; i < V; i++) take(p[i] * unit);
       } else {
         spread();
         if (gl < G)
@@ -439,13 +449,24 @@ __global__ void __launch_bounds__(kWarps * 32, V <= 8 ? 4 : 2) select_kernel(Sel
         one = fmaxf(one, x);
       }
       const float v = a.sum_two && gs > 1 ? one + two : one;
-      uint32_t left = gl < G && sub == 0 ? order_key(v) : 0u, last = 0u;
-      unsigned in = 0;  // the chosen groups
+      const uint32_t mine = gl < G && sub == 0 ? order_key(v) : 0u;
+      uint32_t left = mine, last = 0u;
       for (int k = 0; k < a.top_groups; k++) {
         last = __reduce_max_sync(0xffffffffu, left);
-        const int src = __ffs(__ballot_sync(0xffffffffu, left == last)) - 1;
-        in |= 1u << (src >> per);
-        if (lane == src) left = 0u;
+        if (left == last) left = 0u;  // equal ones together
+      }
+      // the chosen groups, by their lanes, the first of equal ones
+      unsigned in = __ballot_sync(0xffffffffu, mine && mine >= last);
+      const bool ties = __popc(in) != a.top_groups;
+      if (ties) {
+        left = mine;
+        in = 0;
+        for (int k = 0; k < a.top_groups; k++) {
+          last = __reduce_max_sync(0xffffffffu, left);
+          const int src = __ffs(__ballot_sync(0xffffffffu, left == last)) - 1;
+          in |= 1u << src;
+          if (lane == src) left = 0u;
+        }
       }
       const float lowest = key_value(last);
       const float rest = key_value(__reduce_max_sync(0xffffffffu, left));
@@ -455,21 +476,22 @@ __global__ void __launch_bounds__(kWarps * 32, V <= 8 ? 4 : 2) select_kernel(Sel
         if (sigmoid && fabsf(lowest) < INFINITY && !__any_sync(0xffffffffu, v != v)) {
           if (held) spread();
           const int src = lane << per & 31;
-          in = refine_groups(a, zt, bias, line, best, __shfl_sync(0xffffffffu, v, src),
-                             __shfl_sync(0xffffffffu, gs > 1 ? two : one, src), lowest, margin,
-                             any);
+          const unsigned groups = refine_groups(
+              a, zt, bias, line, best, __shfl_sync(0xffffffffu, v, src),
+              __shfl_sync(0xffffffffu, gs > 1 ? two : one, src), lowest, margin, any);
+          in = __ballot_sync(0xffffffffu, sub == 0 && gl < G && (groups >> gl & 1u));
           again = false;
         }
       }
       if (held) {
-        const bool mine = in >> gl & 1u;
+        const bool kept = in >> (lane - sub) & 1u;
 #pragma unroll
-        for (int i = 0; i < V; i++) c[i] = mine ? c[i] : none;
+        for (int i = 0; i < V; i++) c[i] = kept ? c[i] : none;
       } else {
         int g = col / gs, at = col - g * gs;  // the column's group and place in it
 #pragma unroll
         for (int i = 0; i < V; i++) {
-          if (!(in >> (g & 31) & 1u)) c[i] = none;
+          if (!(in >> (g << per & 31) & 1u)) c[i] = none;
           if (++at == gs) {
             at = 0;
             g++;
