@@ -10,12 +10,12 @@
 //
 // The order of c is that of its value in 64 bits.  In fp32 two neighbours may
 // come out the wrong way round, so the picks are made in fp32 with a bound on
-// each value's error, and where a comparison that mattered (neighbours
-// among the picks, the last pick and the rest, the last group and the rest) is
-// closer than the bounds, 64 bits decide: among the picks of sigmoid scores the
-// few candidates alone, one row in a thousand of 256 experts, else the whole
-// row is done again.  Two experts with the same logit and bias have the
-// same c and need no second look.
+// each value's error, and where a comparison that mattered (neighbours among the
+// picks, the last pick and the rest, the last group and the rest) is closer than
+// the bounds, 64 bits decide, of the few candidates alone (one row in a thousand
+// of 256 experts).  Rows with values that are not finite, or with too many
+// candidates, are done again as a whole.  Two experts with the same logit and
+// bias have the same c and need no second look.
 #include "route_common.cuh"
 
 namespace moonep {
@@ -128,23 +128,24 @@ __device__ __forceinline__ void select_exact(const SelectArgs &a, const T *z, ui
 // Weights, ids and counts of a row's picks, one per lane (id, and logit z); m and
 // inv: the row's largest logit and 1 / sum of its scores, for softmax weights
 // that are not normalised.
-__device__ __forceinline__ void write_picks(const SelectArgs &a, int id, float z, int64_t t,
-                                            bool on, float m, float inv, int32_t *cnt) {
+__device__ __forceinline__ void write_picks(const SelectArgs &a, bool sigmoid, int id, float z,
+                                            int64_t t, bool on, float m, float inv,
+                                            int32_t *cnt) {
   const int lane = threadIdx.x & 31, K = a.r.K;
   const bool mine = lane < K;
   if (!on || !mine) z = -INFINITY;
   float by = 1.0f, top = m;
-  if (a.renormalize && !a.r.sigmoid) {
+  if (a.renormalize && !sigmoid) {
     top = z;
 #pragma unroll
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   }
-  const float v = mine ? score(z, top, a.r.sigmoid) : 0.0f;
+  const float v = mine ? score(z, top, sigmoid) : 0.0f;
   if (a.renormalize) {
     const float sum = warp_sum(v);
     by = sum == 0.0f ? 0.0f : a.scale / sum;
   } else {
-    by = a.r.sigmoid ? a.scale : a.scale * inv;
+    by = sigmoid ? a.scale : a.scale * inv;
   }
   if (mine) {
     a.r.topk[t * K + lane] = on ? id : 0;
@@ -214,17 +215,34 @@ __device__ __forceinline__ int place(const float *value, int n, int lane, float 
   return rank;
 }
 
-// The picks among n candidates by their values in 64 bits, into `index`; sigmoid
-// scores, which need no other logit.
-template <typename T>
-__device__ __noinline__ void refine_picks(const T *z, const float *bias, int K, int n,
-                                          const int32_t *from, uint64_t *keys, int32_t *index) {
-  const int lane = threadIdx.x & 31;
+// What selects, in 64 bits: a score, or a share of a row whose largest logit is m
+// and whose scores' sum Z is.
+__device__ __forceinline__ double exact_value(double x, double m, double Z, bool sigmoid) {
+  return sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - m) / Z;
+}
+template <bool kSigmoid, typename T>
+__device__ __forceinline__ double exact_sum(const SelectArgs &a, const T *z, float m) {
+  double Z = 0.0;
+  if (!kSigmoid) {
+    for (int e = threadIdx.x & 31; e < a.r.E; e += 32) Z += exp((double)to_f(z[e]) - (double)m);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) Z += __shfl_xor_sync(0xffffffffu, Z, o);
+  }
+  return Z;
+}
+
+// The picks among n candidates by their values in 64 bits, into `index`.
+template <bool kSigmoid, typename T>
+__device__ __noinline__ void refine_picks(const SelectArgs &a, const T *z, const float *bias,
+                                          float m, int n, const int32_t *from, uint64_t *keys,
+                                          int32_t *index) {
+  const int lane = threadIdx.x & 31, K = a.r.K;
+  const double Z = exact_sum<kSigmoid>(a, z, m);
   uint64_t mine = 0;
   int id = 0;
   if (lane < n) {
     id = from[lane];
-    mine = order_key64(1.0 / (1.0 + exp(-(double)to_f(z[id]))) + (double)bias[id]);
+    mine = order_key64(exact_value(to_f(z[id]), m, Z, kSigmoid) + (double)bias[id]);
     keys[lane] = mine;
   }
   __syncwarp();
@@ -240,11 +258,13 @@ __device__ __noinline__ void refine_picks(const T *z, const float *bias, int K, 
 // The top groups where some values lie within `margin` of the last one's: those
 // groups by their values in 64 bits, from the elements that can be among a
 // group's two largest.  Lane g has group g's value and its second largest
-// element; line: the elements.  Returns the groups as bits.  Sigmoid scores.
-template <typename T>
+// element; line: the elements.  Returns the groups as bits.
+template <bool kSigmoid, typename T>
 __device__ __noinline__ unsigned refine_groups(const SelectArgs &a, const T *z, const float *bias,
-                                               const float *line, uint64_t *best, float value,
-                                               float second, float last, float margin, float any) {
+                                               float m, const float *line, uint64_t *best,
+                                               float value, float second, float last,
+                                               float margin, float any) {
+  const double Z = exact_sum<kSigmoid>(a, z, m);
   const int lane = threadIdx.x & 31, gs = a.r.E / a.groups;
   const bool group = lane < a.groups, flagged = group && fabsf(value - last) <= margin;
   const unsigned sure = __ballot_sync(0xffffffffu, group && value - last > margin);
@@ -256,7 +276,7 @@ __device__ __noinline__ unsigned refine_groups(const SelectArgs &a, const T *z, 
       const int e = lane * gs + i;
       if (!(line[e] >= least)) continue;
       const uint64_t k =
-          order_key64(1.0 / (1.0 + exp(-(double)to_f(z[e]))) + (double)bias[e]);
+          order_key64(exact_value(to_f(z[e]), m, Z, kSigmoid) + (double)bias[e]);
       if (k > one) {
         two = one;
         one = k;
@@ -303,16 +323,22 @@ __device__ __noinline__ void again_exact(const SelectArgs &a, const T *z, uint64
   const float m = row_max(z, a.r.E);
   const float inv = a.r.sigmoid || a.renormalize ? 0.0f : row_inverse(z, a.r.E, m, false);
   const int id = (threadIdx.x & 31) < a.r.K ? index[threadIdx.x & 31] : 0;
-  write_picks(a, id, to_f(z[id]), t, true, m, inv, cnt);
+  write_picks(a, a.r.sigmoid, id, to_f(z[id]), t, true, m, inv, cnt);
   __syncwarp();
 }
 
 // Rows of up to 32 V logits, a warp to a token, lane l holding columns l V to
 // l V + V - 1.  A row to be done again gets the id -1 as its first pick and its
-// turn after the warp's last row: a call within the loop would take the
-// registers of half the warps.
-template <typename T, int V>
-__global__ void __launch_bounds__(kWarps * 32, V <= 12 ? 4 : 2) select_kernel(SelectArgs a, bool vec) {
+// turn after the warp's last row.
+//
+// Bound by instructions, some 900 a row, and the chains between them: with four
+// blocks per SM (64 registers, a few of them spilled) 32768 rows of 256 in 8
+// groups take 41 us, without groups 34, 65536 bf16 rows of 384 66 us, where two or
+// three blocks without spills took 52 to 62, 62 and 77; loading the next row ahead
+// took 5 us more, sorting the candidates by warp-wide maxima 7.
+template <typename T, int V, bool kSigmoid>
+__global__ void __launch_bounds__(kWarps * 32, V <= 12 ? 4 : 2)
+    select_kernel(SelectArgs a, bool vec) {
   pdl_wait();
   pdl_launch_dependents();
   extern __shared__ __align__(16) uint64_t words[];
@@ -325,7 +351,8 @@ __global__ void __launch_bounds__(kWarps * 32, V <= 12 ? 4 : 2) select_kernel(Se
   int32_t *from = (int32_t *)(value + 36), *index = from + 32;            // theirs, the picks
   int32_t *cnt = (int32_t *)(bias + 32 * V + kWarps * kScratch);          // [E]
   const int r = blockIdx.y, n = min(a.r.ntok[r], a.r.S);
-  const bool grouped = a.top_groups < G, sigmoid = a.r.sigmoid;
+  const bool grouped = a.top_groups < G;
+  constexpr bool sigmoid = kSigmoid;
   const int gs = E / G;
   const float none = __uint_as_float(0x7fffffffu);  // left out: no comparison holds
   for (int e = threadIdx.x; e < 32 * V; e += blockDim.x)
@@ -361,7 +388,7 @@ __global__ void __launch_bounds__(kWarps * 32, V <= 12 ? 4 : 2) select_kernel(Se
   for (int s = begin; s < a.r.S; s += step) {
     const int64_t t = (int64_t)r * a.r.S + s;
     if (s >= n) {
-      write_picks(a, 0, 0.0f, t, false, 0.0f, 0.0f, cnt);
+      write_picks(a, true, 0, 0.0f, t, false, 0.0f, 0.0f, cnt);
       continue;
     }
     const T *zt = (const T *)a.r.logits + t * E;
@@ -473,12 +500,13 @@ __global__ void __launch_bounds__(kWarps * 32, V <= 12 ? 4 : 2) select_kernel(Se
       const float margin = 4.0f * any + fabsf(lowest) * 0x1p-21f;
       if (!logits && !(lowest - rest > margin)) {
         again = true;
-        if (sigmoid && fabsf(lowest) < INFINITY && !__any_sync(0xffffffffu, v != v)) {
+        if (fabsf(lowest) < INFINITY && m > -INFINITY && !__any_sync(0xffffffffu, v != v)) {
           if (held) spread();
           const int src = lane << per & 31;
-          const unsigned groups = refine_groups(
-              a, zt, bias, line, best, __shfl_sync(0xffffffffu, v, src),
-              __shfl_sync(0xffffffffu, gs > 1 ? two : one, src), lowest, margin, any);
+          const float gv = __shfl_sync(0xffffffffu, v, src);
+          const float g2 = __shfl_sync(0xffffffffu, gs > 1 ? two : one, src);
+          const unsigned groups =
+              refine_groups<kSigmoid>(a, zt, bias, m, line, best, gv, g2, lowest, margin, any);
           in = __ballot_sync(0xffffffffu, sub == 0 && gl < G && (groups >> gl & 1u));
           again = false;
         }
@@ -566,14 +594,14 @@ __global__ void __launch_bounds__(kWarps * 32, V <= 12 ? 4 : 2) select_kernel(Se
         else if (lane == K - 1)
           close = cn == cn && !(own - cn > d + any);
         again = __any_sync(0xffffffffu, close);
-        if (again && count <= 32 && sigmoid) {
+        if (again && count <= 32 && m > -INFINITY) {
           // what may be a pick lies at most twice the bound below the last one
           const float last = __shfl_sync(0xffffffffu, own, K - 1);
           const float low = last - 2.0f * any - fabsf(last) * 0x1p-22f;
           if (fabsf(low) < INFINITY) {
             const int more = gather<V>(c, col, low, lane, value, from);
             if (more <= 32) {
-              refine_picks(zt, bias, K, more, from, row, index);
+              refine_picks<kSigmoid>(a, zt, bias, m, more, from, row, index);
               id = lane < K ? index[lane] : 0;
               x = to_f(zt[id]);
               again = false;
@@ -581,7 +609,7 @@ __global__ void __launch_bounds__(kWarps * 32, V <= 12 ? 4 : 2) select_kernel(Se
           }
         }
       }
-      if (!again) write_picks(a, id, x, t, true, m, inv, cnt);
+      if (!again) write_picks(a, kSigmoid, id, x, t, true, m, inv, cnt);
     }
     if (again && lane == 0) a.r.topk[t * K] = -1;
     __syncwarp();
@@ -626,14 +654,14 @@ __global__ void __launch_bounds__(kWarps * 32) select_long_kernel(SelectArgs a) 
   for (int s = blockIdx.x * warps + warp; s < a.r.S; s += gridDim.x * warps) {
     const int64_t t = (int64_t)r * a.r.S + s;
     if (s >= n) {
-      write_picks(a, 0, 0.0f, t, false, 0.0f, 0.0f, cnt);
+      write_picks(a, true, 0, 0.0f, t, false, 0.0f, 0.0f, cnt);
       continue;
     }
     const T *z = (const T *)a.r.logits + t * E;
     select_exact(a, z, row, best, index);
     const int id = lane < a.r.K ? index[lane] : 0;
     const float m = row_max(z, E), inv = row_inverse(z, E, m, a.r.sigmoid);
-    write_picks(a, id, to_f(z[id]), t, true, m, inv, cnt);
+    write_picks(a, a.r.sigmoid, id, to_f(z[id]), t, true, m, inv, cnt);
     if (a.r.part_p)
       for (int e = lane; e < E; e += 32) mine[e] += score(to_f(z[e]), m, a.r.sigmoid) * inv;
     __syncwarp();
@@ -676,11 +704,15 @@ size_t select_smem(int E, int G) {
   return w * (E + G + 16) * 8 + (w + 1) * E * 4;
 }
 
+template <typename T, bool kSigmoid>
+auto select_kernel_for(int E) {
+  return E <= 32 ? select_kernel<T, 1, kSigmoid> : E <= 64 ? select_kernel<T, 2, kSigmoid>
+         : E <= 128 ? select_kernel<T, 4, kSigmoid> : E <= 256 ? select_kernel<T, 8, kSigmoid>
+         : E <= 384 ? select_kernel<T, 12, kSigmoid> : select_kernel<T, 16, kSigmoid>;
+}
 template <typename T>
-auto select_kernel_of(int E) {
-  return E <= 32 ? select_kernel<T, 1> : E <= 64 ? select_kernel<T, 2>
-         : E <= 128 ? select_kernel<T, 4> : E <= 256 ? select_kernel<T, 8>
-         : E <= 384 ? select_kernel<T, 12> : select_kernel<T, 16>;
+auto select_kernel_of(int E, bool sigmoid) {
+  return sigmoid ? select_kernel_for<T, true>(E) : select_kernel_for<T, false>(E);
 }
 
 template <typename T>
@@ -690,12 +722,13 @@ int run_select(moonep_ctx *ctx, SelectArgs &a, FinishArgs &f, int32_t *tpe, bool
   const bool reg = c.E <= kInRegisters;
   const int warps = reg ? kWarps : long_warps(c.E);
   const size_t smem = select_smem(c.E, a.groups);
-  const void *fn = reg ? (const void *)select_kernel_of<T>(c.E) : (const void *)select_long_kernel<T>;
+  const auto kernel = select_kernel_of<T>(c.E, a.r.sigmoid);
+  const void *fn = reg ? (const void *)kernel : (const void *)select_long_kernel<T>;
   cudaError_t e = smem > 48 * 1024 ? raise_dyn_smem(fn, (int)smem) : cudaSuccess;
   if (e != cudaSuccess) return cuda_status(e);
   // as the plain router: at most four blocks per SM, no more than num_sms SMs
   // hold, but one per rank; a power of two up to the cluster, then a multiple
-  const int64_t held = reg ? blocks_in_cap(ctx, select_kernel_of<T>(c.E), warps * 32, smem)
+  const int64_t held = reg ? blocks_in_cap(ctx, kernel, warps * 32, smem)
                            : blocks_in_cap(ctx, select_long_kernel<T>, warps * 32, smem);
   const int64_t need = ((int64_t)c.S + warps - 1) / warps;
   int64_t cap = (4 * ctx->sms + c.R - 1) / c.R;
@@ -716,7 +749,7 @@ int run_select(moonep_ctx *ctx, SelectArgs &a, FinishArgs &f, int32_t *tpe, bool
   f.part_p = a.r.part_p;
   const dim3 grid(bpr, c.R), block(warps * 32);
   if (reg)
-    e = launch_pdl_ex(select_kernel_of<T>(c.E), grid, block, smem, st, false, a.r.cluster, a,
+    e = launch_pdl_ex(kernel, grid, block, smem, st, false, a.r.cluster, a,
                       c.E % (sizeof(T) == 2 ? 8 : 4) == 0);
   else
     e = launch_pdl_ex(select_long_kernel<T>, grid, block, smem, st, false, a.r.cluster, a);
