@@ -237,7 +237,7 @@ __device__ __forceinline__ uint2 encode_m(const float2 f[4], const uint32_t word
   uint32_t top = 0;
 #pragma unroll
   for (int i = 0; i < 4; i++)
-    top = max(top, max(__float_as_uint(f[i].x) & 0x7fffffffu, __float_as_uint(f[i].y) & 0x7fffffffu));
+    top = max(top, max(__float_as_uint(fabsf(f[i].x)), __float_as_uint(fabsf(f[i].y))));
   const uint32_t s = block_scale<8, 0x600000u>(block_max(top));
   const float2 inv = both(mx_inverse(s)), down = both(0x1p-120f);
   *scale = s;
@@ -285,8 +285,8 @@ __device__ void device_scalars(const StepArgs &a, Scalars *s) {
 }
 
 template <typename P, typename G, int BITS, int N>
-__global__ void __launch_bounds__(kThreads, BITS == 32 ? 6 : 4) adamw_kernel(const __grid_constant__ Table<N> tab,
-                                                         const __grid_constant__ StepArgs a) {
+__global__ void __launch_bounds__(kThreads, BITS == 32 ? 6 : 4)
+    adamw_kernel(const __grid_constant__ Table<N> tab, const __grid_constant__ StepArgs a) {
   pdl_wait();
   pdl_launch_dependents();
   __shared__ Scalars sh;
