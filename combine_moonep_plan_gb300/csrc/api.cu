@@ -503,7 +503,9 @@ int moonep_route_backward(moonep_ctx *ctx, const void *logits, int logits_bf16, 
 // A selection that fits the context's experts; the backward pass reads none of
 // its bias and groups.
 static bool selection_ok(const moonep_config &c, const moonep_route_selection *s, bool whole) {
-  if (!s || !(s->scale - s->scale == 0.0f)) return false;
+  if (!s || !(s->scale - s->scale == 0.0f) ||
+      (s->scale != 0.0f && s->scale < FLT_MIN && s->scale > -FLT_MIN))
+    return false;
   if (!whole) return true;
   return s->groups >= 1 && c.E % s->groups == 0 && s->top_groups >= 1 &&
          s->top_groups <= s->groups && c.K <= s->top_groups * (c.E / s->groups) &&

@@ -277,7 +277,7 @@ __device__ __forceinline__ uint2 encode_v(const float2 f[4], const uint32_t word
 // The scalars of a step whose rate or number lies in device memory.
 __device__ void device_scalars(const StepArgs &a, Scalars *s) {
   const float lr = a.lr_dev ? *a.lr_dev : a.lr;
-  const int32_t t = a.step_dev ? *a.step_dev : a.step;
+  const int32_t t = a.step_dev ? max(*a.step_dev, 1) : a.step;
   s->decay = 1.0f - lr * a.wd;
   s->rate = lr / -expm1f((float)t * a.log_b1);
   s->root = 1.0f / sqrtf(-expm1f((float)t * a.log_b2));

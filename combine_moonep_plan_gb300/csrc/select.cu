@@ -803,8 +803,9 @@ int launch_route_bias(moonep_ctx *ctx, const int32_t *tpe, const int32_t *num_to
   a.K = c.K;
   for (int r = 0; r < c.R; r++) a.ntok[r] = num_tokens ? num_tokens[r] : c.S;
   const int threads = c.E < 1024 ? (c.E + 31) / 32 * 32 : 1024;
-  return cuda_status(launch_pdl(bias_kernel, dim3((c.E + threads - 1) / threads), dim3(threads), 0,
-                                st, false, a));
+  const int blocks = (c.E + threads - 1) / threads;
+  return cuda_status(launch_pdl(bias_kernel, dim3(blocks < ctx->sms ? blocks : ctx->sms),
+                                dim3(threads), 0, st, false, a));
 }
 
 }  // namespace moonep

@@ -444,7 +444,7 @@ typedef struct moonep_route_selection {
   int top_groups;
   int group_score;
   int renormalize;
-  float scale;     /* finite */
+  float scale;     /* finite, 0 or at least 2^-126 in size */
 } moonep_route_selection;
 int moonep_route_select(moonep_ctx *ctx, const void *logits, int logits_bf16,
                         int scoring, const moonep_route_selection *selection,
@@ -600,7 +600,8 @@ int moonep_grad_norm(moonep_ctx *ctx, int n_tensors, const void *const *g,
  * a bf16 p, by 16 bits of a hash of (seed, step, tensor's place, element).  A v
  * above zero keeps at least code 1.
  *   lr_dev, step_dev   device scalars used in place of lr and step when given
- *            (a captured step then goes on from replay to replay)
+ *            (a captured step then goes on from replay to replay); a step below
+ *            1 there counts as 1
  * 0 <= beta < 1, eps > 0, step >= 1, and max_norm > 0 with a norm. */
 typedef struct moonep_adamw_config {
   double lr, beta1, beta2, eps, weight_decay;

@@ -301,6 +301,40 @@ def test_captured_step_with_device_scalars(buf):
     assert step.item() == 5 and buf.get_status() == 0
 
 
+def test_few_sms(buf):
+    """A context of one SM takes the same steps."""
+    from combine_moonep_plan_gb300 import Buffer
+    one = Buffer(S=1, H=8, K=1, E=1, num_ep_ranks=1, zero_copy_views=False, num_sms=1)
+    for bits, dtype in ((32, torch.float32), (8, torch.float32), (8, torch.bfloat16)):
+        p = _tensors([100000, 33, 4097], dtype, 1, 1.0, 0)
+        g = _tensors([100000, 33, 4097], torch.float32, 2, 1.0, 0)
+        got = []
+        for b in (buf, one):
+            q = [t.clone() for t in p]
+            state = b.adamw_state(q, bits=bits)
+            norm = b.grad_norm(g)
+            b.adamw(q, g, state, step=1, seed=3, norm=norm, max_norm=1.0, **HYPER)
+            got.append((*q, *state.tensors, *state.moments()))
+            full = np.sqrt(sum((_f64(t) ** 2).sum() for t in g))
+            assert abs(norm.item() - full) <= 6 * U * full
+        # the norm's sums are split over the blocks, so its last bit may differ, which
+        # may move a clipped value by one, and a rounded one by a step in a million
+        for x, y in zip(*got):
+            assert (x != y).float().mean().item() <= (1.0 if x.dtype == torch.float32 else 1e-3)
+            if x.dtype == torch.float32:
+                assert torch.allclose(x, y, rtol=2.0 ** -20, atol=2.0 ** -20)
+
+
+def test_device_step_below_one_counts_as_one(buf):
+    p, g = torch.ones(100, device="cuda"), torch.randn(100, device="cuda")
+    q = p.clone()
+    zero = torch.zeros(1, dtype=torch.int32, device="cuda")
+    a, b = buf.adamw_state([p]), buf.adamw_state([q])
+    buf.adamw([p], [g], a, lr=0.1, step=zero)
+    buf.adamw([q], [g], b, lr=0.1, step=1)
+    assert torch.allclose(p, q, rtol=2.0 ** -20) and torch.equal(a.tensors[0], b.tensors[0])
+
+
 def test_past_two_to_31_elements(buf):
     n = (1 << 31) + 1000
     p = torch.zeros(n, dtype=torch.bfloat16, device="cuda")

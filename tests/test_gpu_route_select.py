@@ -104,7 +104,8 @@ def test_select_and_gradient(R, S, E, K, groups, top, mode, scoring, renorm, kin
     assert np.array_equal(out.tokens_per_expert.cpu().numpy(), tpe)
     w = ref.select_weights(zn, picks, scoring, renorm, scale, n)
     span = float(min(100.0, np.ptp(zn[np.isfinite(zn)])))
-    assert np.all(np.abs(out.weights.cpu().numpy() - w) <= (span + E / 16 + K + 16) * EPS * w + 1e-30)
+    tol = (span + E / 16 + K + 16) * EPS * w + 1e-30
+    assert np.all(np.abs(out.weights.cpu().numpy() - w) <= tol)
     assert np.all(np.abs(out.coef.cpu().numpy() - coef) <= 8 * EPS * coef)
     assert abs(out.loss.item() - loss) <= (span + S + R * E + 32) * EPS * loss + 1e-30
     rng = np.random.default_rng(5)
@@ -263,6 +264,38 @@ def test_captured_with_its_bias_step():
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("E,groups", [(640, 8), (512, 512), (4096, 4)])
+def test_captured_long_rows(E, groups):
+    """Rows and groups whose kernels need more shared memory than a launch has by
+    itself, first called within a capture."""
+    z, bias = _inputs(1, 20, E, "bias", "sigmoid", "float32", E)
+    kw = dict(scoring="sigmoid", bias=bias, groups=groups, top_groups=max(2, groups // 2))
+    buf = _buffer(1, 20, 4, E)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = buf.route(z, **kw)
+    graph.replay()
+    want = ref.select(z.cpu().numpy(), 4, "sigmoid", bias.cpu().numpy(), groups,
+                      max(2, groups // 2), "top2")
+    assert np.array_equal(out.topk.cpu().numpy(), want)
+
+
+def test_no_tokens_and_no_weight():
+    buf = _buffer(2, 0, 2, 8)
+    z, bias = torch.zeros(2, 0, 8, device="cuda"), torch.zeros(8, device="cuda")
+    out = buf.route(z, bias=bias, balance=0.1)
+    assert out.topk.numel() == 0 and not out.tokens_per_expert.any() and out.loss.item() == 0
+    assert buf.route_backward(out, z).numel() == 0
+    buf.update_route_bias(bias, out, 0.1)
+    assert not bias.any()
+    # a scale of zero: no weights, no gradient of them
+    z, buf = torch.randn(2, 5, 8, device="cuda"), _buffer(2, 5, 2, 8)
+    for renorm in (True, False):
+        out = buf.route(z, scale=0.0, renormalize=renorm)
+        assert out.topk.max() > 0 and not out.weights.any()
+        assert not buf.route_backward(out, z, torch.ones_like(out.weights)).any()
+
+
 def test_few_sms():
     z, bias = _inputs(4, 500, 256, "bias", "sigmoid", "float32", 1)
     kw = dict(scoring="sigmoid", bias=bias, groups=8, top_groups=4, balance=0.1)
@@ -285,7 +318,7 @@ def test_refusals():
             buf.route(z, **kw)
     with pytest.raises(TypeError):
         buf.route(z, bias=bias.double())
-    for scale in (float("nan"), float("inf")):
+    for scale in (float("nan"), float("inf"), 1e-40, -1e-40):
         with pytest.raises(MoonepError):
             buf.route(z, scale=scale)
     out = buf.route(z, bias=bias)

@@ -84,7 +84,8 @@ def _check(buf, cu, N, Kd, seed=0, accumulate=False, pad=0, garbage=True):
 LENGTHS = [0, 1, 15, 16, 17, 63, 64, 65, 127, 128, 129, 320, 333]
 
 
-@pytest.mark.parametrize("N,Kd", [(8, 8), (256, 256), (264, 72), (512, 1000), (1000, 520)])
+@pytest.mark.parametrize("N,Kd", [(8, 8), (256, 256), (264, 72), (512, 1000), (1000, 520),
+                                  (64, 64), (192, 8), (320, 448)])
 @pytest.mark.parametrize("accumulate", [False, True])
 def test_lengths(N, Kd, accumulate):
     buf = _buffer(2, 8, 3, 2000)
@@ -128,7 +129,7 @@ def test_repeats_bit_for_bit_and_overlaps_itself():
     buf = _buffer(2, 8, 2, 1500)
     cu = torch.from_numpy(_cu(2, 8, 2, [300, 77, 0, 150], buf.NvS)).cuda()
     n = 2 * buf.NvS
-    x, d = torch.randn(n, 512, device="cuda").bfloat16(), torch.randn(n, 768, device="cuda").bfloat16()
+    x, d = (torch.randn(n, c, device="cuda").bfloat16() for c in (512, 768))
     first = [t.clone() for t in buf.expert_weight_grad(x, d, cu)]
     streams = [torch.cuda.Stream() for _ in range(2)]
     outs = []
@@ -154,6 +155,43 @@ def test_repeats_bit_for_bit_and_overlaps_itself():
     assert buf.get_status() == 0
 
 
+def test_no_rows_at_all():
+    """A context without tokens: zeros for the home experts, or nothing added."""
+    buf = _buffer(1, 3, 0, 0)
+    assert buf.NvS == 0
+    x, d = (torch.zeros(0, c, device="cuda").bfloat16() for c in (16, 8))
+    cu = torch.zeros(1, 3, dtype=torch.int32, device="cuda")
+    grad, slots = torch.ones(3, 8, 16, device="cuda"), torch.ones(1, 0, 8, 16, device="cuda")
+    buf.expert_weight_grad(x, d, cu, out=(grad, slots), accumulate=True)
+    assert grad.eq(1).all()
+    buf.expert_weight_grad(x, d, cu, out=(grad, slots))
+    assert not grad.any()
+
+
+def test_beside_a_product_on_another_stream():
+    """Two kernels that each want whole SMs take turns."""
+    buf = _buffer(2, 8, 2, 3000)
+    cu = torch.from_numpy(_cu(2, 8, 2, [500, 77, 0, 450], buf.NvS)).cuda()
+    n = 2 * buf.NvS
+    x, d = (torch.randn(n, c, device="cuda").bfloat16() for c in (512, 768))
+    x4 = buf.quantize_mx(x)
+    w4 = buf.quantize_mx(torch.randn(8 + 4, 768, 512, device="cuda").bfloat16())
+    grad, _ = buf.expert_weight_grad(x, d, cu)
+    y = torch.zeros(n, 768, device="cuda")
+    buf.expert_product(x4, w4, cu, out=y)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(5):
+        y2 = torch.zeros_like(y)
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            buf.expert_product(x4, w4, cu, out=y2)
+        again, _ = buf.expert_weight_grad(x, d, cu)
+        torch.cuda.synchronize()
+        assert torch.equal(again, grad) and torch.equal(y2, y)
+    assert buf.get_status() == 0
+
+
 def test_against_differences():
     """sum(c * (x W^T)) moves by h times the gradient, with c as d_out: linear, so
     the difference is exact but for 64-bit rounding; the kernel's part is that of
@@ -167,7 +205,8 @@ def test_against_differences():
     W = np.random.default_rng(0).standard_normal((2, 8, 16))
 
     def value(W):
-        return sum((cn[a:b] * (xn[a:b] @ W[e].T)).sum() for e, (a, b) in enumerate(((0, 19), (19, 40))))
+        return sum((cn[rows] * (xn[rows] @ W[e].T)).sum()
+                   for e, rows in enumerate((slice(0, 19), slice(19, 40))))
 
     for i in np.ndindex(2, 8, 16):
         up = W.copy()
@@ -181,7 +220,7 @@ def test_against_differences():
 def test_reported_segments_count_as_empty():
     from combine_moonep_plan_gb300._lib import ERR_PLAN
     buf = _buffer(1, 4, 0, 100)
-    x, d = torch.ones(buf.NvS, 16, device="cuda").bfloat16(), torch.ones(buf.NvS, 8, device="cuda").bfloat16()
+    x, d = (torch.ones(buf.NvS, c, device="cuda").bfloat16() for c in (16, 8))
     cu = torch.tensor([[10, 5, 30, 1 << 20]], dtype=torch.int32, device="cuda")
     grad, _ = buf.expert_weight_grad(x, d, cu)
     assert grad[0].eq(10).all() and not grad[1].any() and grad[2].eq(25).all() and not grad[3].any()
@@ -209,14 +248,15 @@ def test_past_two_to_31_values():
         a = slice(20 * e, 20 * e + 20)
         for n0, k0 in ((0, 0), (N - 8, Kd - 8), (12000, 5000)):
             want = d[a, n0:n0 + 8].double().T @ x[a, k0:k0 + 8].double()
-            assert (grad[e, n0:n0 + 8, k0:k0 + 8].double() - want).abs().max() <= 4 * 2.0 ** -22 * 20 * 25
+            got = grad[e, n0:n0 + 8, k0:k0 + 8].double()
+            assert (got - want).abs().max() <= 4 * 2.0 ** -22 * 20 * 25
     assert buf.get_status() == 0
 
 
 def test_refusals():
     from combine_moonep_plan_gb300._lib import MoonepError
     buf = _buffer(1, 2, 1, 64)
-    x, d = torch.zeros(64, 16, device="cuda").bfloat16(), torch.zeros(64, 8, device="cuda").bfloat16()
+    x, d = (torch.zeros(64, c, device="cuda").bfloat16() for c in (16, 8))
     cu = torch.zeros(1, 3, dtype=torch.int32, device="cuda")
     assert buf.NvS == 64
     ok = buf.expert_weight_grad(x, d, cu)
