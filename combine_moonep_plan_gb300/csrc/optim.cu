@@ -285,7 +285,7 @@ __device__ void device_scalars(const StepArgs &a, Scalars *s) {
 }
 
 template <typename P, typename G, int BITS, int N>
-__global__ void __launch_bounds__(kThreads, BITS == 32 ? 6 : 4)
+__global__ void __launch_bounds__(kThreads, BITS == 8 && sizeof(P) == 4 ? 5 : 6)
     adamw_kernel(const __grid_constant__ Table<N> tab, const __grid_constant__ StepArgs a) {
   pdl_wait();
   pdl_launch_dependents();
