@@ -155,19 +155,21 @@ __device__ __forceinline__ void write_picks(const SelectArgs &a, bool sigmoid, i
   }
 }
 
-// Bounds on the error of c = a + b in fp32, twice what they have to be.
-//   sigmoid  of e = exp(-x): two parts in 2^23 and |x| parts in 2^24, of which
-//            s (1 - s) reaches s; the sum 1 + e, the inverse, and the addition of
-//            b.  s (1 - s) |x| is at most 0.28
-//   softmax  of exp(x - m): the same two; the sum of the row's in n roundings,
-//            and its terms' errors, which weighted by p are those of |x - m| = 7;
-//            p |x - m| is at most 0.4 times the largest p
+// Bounds on the error of c = a + b in fp32, some one and a half times what they
+// have to be.
+//   sigmoid  of e = exp(-x): four parts in 2^24, and |x| parts of its argument's
+//            rounding, of which s (1 - s) reaches s; the sum 1 + e, the inverse,
+//            and the addition of b.  s (1 - s) |x| is at most 0.28
+//   softmax  of exp(x - m): the same, and |x - m| parts of the difference's
+//            rounding; the sum of the row's in n + 5 roundings, its terms' errors,
+//            which weighted by p are those of |x - m| = 7 (the entropy of 512
+//            experts), and its inverse.  p |x - m| is at most 0.4 times the largest p
 __device__ __forceinline__ float sigmoid_bound(float s, float x, float c) {
   return s * ((1.0f - s) * (fminf(fabsf(x), 104.0f) * 0x1p-23f + 0x1p-21f) + 3 * 0x1p-23f) +
          fabsf(c) * 0x1p-23f;
 }
 __device__ __forceinline__ float softmax_bound(float p, float d, float c, int n) {
-  return p * (fminf(fabsf(d), 104.0f) * 0x1p-23f + (float)(n + 30) * 0x1p-24f) +
+  return p * (fminf(fabsf(d), 104.0f) * 0x1p-22f + (float)(n + 60) * 0x1p-24f) +
          fabsf(c) * 0x1p-23f;
 }
 

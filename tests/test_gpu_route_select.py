@@ -141,6 +141,21 @@ def test_long_batches_pick_exactly():
         assert np.array_equal(out.topk.cpu().numpy(), want)
 
 
+def test_long_batches_of_shares_pick_exactly():
+    """Shares of the row, under biases of their size."""
+    for E, K, groups, top, mode in ((160, 6, 8, 3, "top2"), (64, 6, 1, 1, "max"),
+                                    (384, 8, 16, 6, "max")):
+        R, S = 4, 8192
+        g = torch.Generator(device="cuda").manual_seed(E)
+        z = torch.randn(R, S, E, generator=g, device="cuda") * 2
+        bias = torch.round(torch.randn(E, generator=g, device="cuda") * 10) * (0.1 / E)
+        buf = _buffer(R, S, K, E)
+        out = buf.route(z, scoring="softmax", bias=bias, groups=groups, top_groups=top,
+                        group_score=mode)
+        want = ref.select(z.cpu().numpy(), K, "softmax", bias.cpu().numpy(), groups, top, mode)
+        assert np.array_equal(out.topk.cpu().numpy(), want)
+
+
 def test_without_bias_and_groups_it_is_the_plain_router():
     R, S, E, K = 4, 300, 256, 8
     z = torch.randn(R, S, E, device="cuda")
