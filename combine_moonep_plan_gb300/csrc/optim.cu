@@ -23,13 +23,15 @@
 //
 // Measured (the kernels alone, 704 million parameters in three tensors): fp32
 // moments, parameters and gradients with bf16 copies 2.98 ms, 7.09 TB/s, above
-// the plain copy's 6.79, bound by memory; 8-bit moments, rounded at random, 1.85
-// ms, 6.9 TB/s; bf16 parameters and gradients with 8-bit moments 2.10 ms, 3.4
-// TB/s, bound by its instructions (the words for p's rounding are a fifth of
-// them), with fp32 moments 2.24 ms, 6.9 TB/s.  Pairs of products and sums in one
-// instruction, rounding in whole numbers and a hash whose first shift the eight
-// values of a thread share took 8-bit moments from 2.44 to 1.85 ms.  The norm
-// reads at 7.3 TB/s (fp32) and 6.3 (bf16).
+// the plain copy's 6.79, bound by memory; 8-bit moments, rounded at random, 1.81
+// ms, 7.0 TB/s; bf16 parameters and gradients with fp32 moments 2.24 ms, 6.9
+// TB/s, with 8-bit ones 1.87 ms, 3.8 TB/s, bound by 86 instructions per value (60
+// to nearest: a fifth of them are the words for p's rounding).  Pairs of products
+// in one instruction, rounding in whole numbers and a hash whose first shift the
+// eight values of a thread share took 8-bit moments from 2.44 to 1.86 ms; five
+// blocks per SM in place of four (a few registers spilled) to 1.81, bf16
+// parameters with six from 2.10 to 1.87.  The norm reads at 7.3 TB/s (fp32) and
+// 6.3 (bf16).
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -496,8 +498,9 @@ int resident(const moonep_ctx *ctx, K kernel, int64_t chunks) {
 // hardware handing blocks out as others end: 704 million fp32 parameters with
 // fp32 moments took 2.98 ms, with as many blocks as are resident and many chunks
 // to each 3.56.  Moments in 8 bits have more to work out before a block's first
-// load: four chunks 1.84 ms, one 2.00, all resident 2.09; bf16 parameters, bound
-// by instructions, sixteen 2.13, four 2.30, one 2.51.
+// load: four chunks 1.81 ms, two 1.84, eight 1.86 (at four blocks per SM one chunk
+// took 8 % more than four, all resident 13 %); bf16 parameters, bound by
+// instructions, sixteen or more 1.94 ms, eight 1.96 (and 9 % more with four).
 // Where blocks take several chunks their count is a multiple of the resident
 // ones, so that no wave of them is all but empty.
 template <typename K>
