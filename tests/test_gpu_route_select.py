@@ -39,6 +39,11 @@ def _inputs(R, S, E, kind, scoring, dtype, seed):
     elif kind == "masked":     # experts and logits shut out
         z[rng.random(z.shape) < 0.5] = -np.inf
         b[rng.random(E) < 0.2] = -np.inf
+    elif kind == "lowest":     # logits at the type's lowest value, whole rows of them
+        z[rng.random(z.shape) < 0.7] = -3e38
+        z[:, ::5] = -3e38
+    elif kind == "shut":       # fewer experts are open than are picked
+        b[3:] = -np.inf
     elif kind == "large":      # the bias decides, scores are a rounding beside it
         b = np.round(rng.standard_normal(E)) * 1e4
     t = torch.from_numpy(z).float().to(getattr(torch, dtype))
@@ -76,6 +81,11 @@ CASES = [
     (2, 64, 256, 31, 1, 1, "top2", "softmax", True, "close", "float32", None),
     (8, 41, 384, 8, 1, 1, "max", "sigmoid", True, "close", "bfloat16", None),
     (3, 41, 384, 8, 16, 7, "top2", "sigmoid", True, "bias", "float32", None),
+    (2, 33, 96, 5, 4, 2, "top2", "sigmoid", True, "lowest", "float32", None),
+    (2, 33, 96, 5, 4, 2, "top2", "softmax", False, "lowest", "bfloat16", [33, 4]),
+    (1, 17, 256, 8, 8, 4, "top2", "sigmoid", True, "shut", "float32", None),
+    (1, 17, 40, 8, 1, 1, "max", "softmax", True, "shut", "float32", None),
+    (1, 17, 700, 8, 7, 2, "max", "sigmoid", False, "shut", "float32", None),
     (1, 50, 500, 9, 50, 20, "top2", "sigmoid", True, "bias", "float32", None),
     (2, 9, 512, 8, 16, 3, "max", "softmax", False, "bias", "float32", None),
     (2, 9, 640, 8, 8, 4, "top2", "sigmoid", True, "close", "float32", [9, 5]),
@@ -103,7 +113,7 @@ def test_select_and_gradient(R, S, E, K, groups, top, mode, scoring, renorm, kin
     _, _, tpe, loss, coef, P = base.route(zn, K, scoring, n, alpha, "rank", ids=picks)
     assert np.array_equal(out.tokens_per_expert.cpu().numpy(), tpe)
     w = ref.select_weights(zn, picks, scoring, renorm, scale, n)
-    span = float(min(100.0, np.ptp(zn[np.isfinite(zn)])))
+    span = float(min(100.0, np.ptp(zn[zn > -1e30])))
     tol = (span + E / 16 + K + 16) * EPS * w + 1e-30
     assert np.all(np.abs(out.weights.cpu().numpy() - w) <= tol)
     assert np.all(np.abs(out.coef.cpu().numpy() - coef) <= 8 * EPS * coef)
