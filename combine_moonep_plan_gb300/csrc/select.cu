@@ -22,7 +22,8 @@ namespace moonep {
 namespace {
 
 constexpr int kWarps = kRouteWarps;
-constexpr int kScratch = 100;  // words of a warp: 36 candidates, their indices, the picks
+constexpr int kCandidates = 36;  // one per lane, and what is read behind them
+constexpr int kScratch = 2 * (kCandidates + 32);  // words of a warp: candidates and picks
 
 struct SelectArgs {
   RouteArgs r;
@@ -143,7 +144,7 @@ __device__ __forceinline__ void write_picks(const SelectArgs &a, bool sigmoid, i
   const float v = mine ? score(z, top, sigmoid) : 0.0f;
   if (a.renormalize) {
     const float sum = warp_sum(v);
-    by = sum == 0.0f ? 0.0f : a.scale / sum;
+    by = sum == 0.0f ? 0.0f : a.scale * inverse(sum);
   } else {
     by = sigmoid ? a.scale : a.scale * inv;
   }
@@ -174,14 +175,18 @@ __device__ __forceinline__ float softmax_bound(float p, float d, float c, int n)
 }
 
 // The values at or above `least` (V per lane, index col + i; NaN: none) side by
-// side, in the order of their indices; their count, of which more than 32 are
-// not written.
+// side with their indices, in the order of these; their count, of which more than
+// 32 are not written.  By predicates: as branches they were twice the
+// instructions.
 template <int V>
 __device__ __forceinline__ int gather(const float c[V], int col, float least, int lane,
-                                      float *value, int32_t *index) {
+                                      uint2 *list) {
   int mine = 0;
 #pragma unroll
-  for (int i = 0; i < V; i++) mine += c[i] >= least;
+  for (int i = 0; i < V; i++)
+    asm("{\n .reg .pred p;\n setp.ge.f32 p, %1, %2;\n @p add.s32 %0, %0, 1;\n}"
+        : "+r"(mine)
+        : "f"(c[i]), "f"(least));
   int at = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -190,30 +195,35 @@ __device__ __forceinline__ int gather(const float c[V], int col, float least, in
   }
   const int n = __shfl_sync(0xffffffffu, at, 31);
   if (n > 32) return n;
-  at -= mine;
+  uint32_t to = (uint32_t)__cvta_generic_to_shared(list + at - mine);
 #pragma unroll
   for (int i = 0; i < V; i++)
-    if (c[i] >= least) {
-      value[at] = c[i];
-      index[at++] = col + i;
-    }
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ge.f32 p, %1, %2;\n @p st.shared.v2.b32 [%0], {%3, %4};\n"
+        " @p add.u32 %0, %0, 8;\n}"
+        : "+r"(to)
+        : "f"(c[i]), "f"(least), "r"(__float_as_uint(c[i])), "r"(col + i)
+        : "memory");
   // what the comparisons by fours read behind them
-  if (lane < 4) value[n + lane] = __uint_as_float(0x7fffffffu);
+  if (lane < 4) list[n + lane].x = 0x7fffffffu;
   __syncwarp();
   return n;
 }
 
 // Places of a warp's n side-by-side values, largest first, equal ones in order:
-// each counts the ones before it.
-__device__ __forceinline__ int place(const float *value, int n, int lane, float mine) {
+// each counts the larger ones, and where that does not tell all apart the equal
+// ones before it.
+__device__ __forceinline__ int place(const uint2 *list, int n, int lane, float mine) {
   int rank = 0;
   for (int j = 0; j < n; j += 4) {
-    const float4 o = *(const float4 *)(value + j);
-    rank += o.x > mine || (o.x == mine && j < lane);
-    rank += o.y > mine || (o.y == mine && j + 1 < lane);
-    rank += o.z > mine || (o.z == mine && j + 2 < lane);
-    rank += o.w > mine || (o.w == mine && j + 3 < lane);
+    const uint4 a = *(const uint4 *)(list + j), b = *(const uint4 *)(list + j + 2);
+    rank += __uint_as_float(a.x) > mine;
+    rank += __uint_as_float(a.z) > mine;
+    rank += __uint_as_float(b.x) > mine;
+    rank += __uint_as_float(b.z) > mine;
   }
+  if ((int)__reduce_add_sync(0xffffffffu, lane < n ? rank : 0) != n * (n - 1) / 2)
+    for (int j = 0; j < n; j++) rank += j < lane && __uint_as_float(list[j].x) == mine;
   return rank;
 }
 
@@ -233,17 +243,17 @@ __device__ __forceinline__ double exact_sum(const SelectArgs &a, const T *z, flo
   return Z;
 }
 
-// The picks among n candidates by their values in 64 bits, into `index`.
+// The picks among n candidates by their values in 64 bits, into picks[..].y.
 template <bool kSigmoid, typename T>
 __device__ __noinline__ void refine_picks(const SelectArgs &a, const T *z, const float *bias,
-                                          float m, int n, const int32_t *from, uint64_t *keys,
-                                          int32_t *index) {
+                                          float m, int n, const uint2 *list, uint64_t *keys,
+                                          uint2 *picks) {
   const int lane = threadIdx.x & 31, K = a.r.K;
   const double Z = exact_sum<kSigmoid>(a, z, m);
   uint64_t mine = 0;
   int id = 0;
   if (lane < n) {
-    id = from[lane];
+    id = (int)list[lane].y;
     mine = order_key64(exact_value(to_f(z[id]), m, Z, kSigmoid) + (double)bias[id]);
     keys[lane] = mine;
   }
@@ -253,7 +263,7 @@ __device__ __noinline__ void refine_picks(const SelectArgs &a, const T *z, const
     const uint64_t o = keys[j];
     rank += o > mine || (o == mine && j < lane);
   }
-  if (lane < n && rank < K) index[rank] = id;
+  if (lane < n && rank < K) picks[rank].y = (uint32_t)id;
   __syncwarp();
 }
 
@@ -349,8 +359,8 @@ __global__ void __launch_bounds__(kWarps * 32, V <= 12 ? 4 : 2)
   uint64_t *row = words + (size_t)warp * (E + 32);                        // [kWarps, E + 32]
   uint64_t *best = words + (size_t)kWarps * (E + 32) + (size_t)warp * G;  // [kWarps, G]
   float *bias = (float *)(words + (size_t)kWarps * (E + 32 + G));         // [32 V], 0 past E
-  float *value = bias + 32 * V + warp * kScratch;                         // 36 candidates
-  int32_t *from = (int32_t *)(value + 36), *index = from + 32;            // theirs, the picks
+  uint2 *list = (uint2 *)(bias + 32 * V + warp * kScratch);               // candidates: value,
+  uint2 *picks = list + kCandidates;                                      // index; the picks
   int32_t *cnt = (int32_t *)(bias + 32 * V + kWarps * kScratch);          // [E]
   const int r = blockIdx.y, n = min(a.r.ntok[r], a.r.S);
   const bool grouped = a.top_groups < G;
@@ -540,22 +550,23 @@ __global__ void __launch_bounds__(kWarps * 32, V <= 12 ? 4 : 2)
         least = __reduce_max_sync(0xffffffffu, lead);
         if (lead == least) lead = 0u;  // equal ones together: only more qualify
       }
-      const int count = gather<V>(c, col, least ? key_value(least) : -INFINITY, lane, value, from);
+      const int count = gather<V>(c, col, least ? key_value(least) : -INFINITY, lane, list);
       int id = 0;
       float own = none;  // this lane's pick's value
       if (count <= 32) {
-        const float mine = lane < count ? value[lane] : none;
-        const int rank = place(value, count, lane, mine), of = lane < count ? from[lane] : 0;
-        __syncwarp();
-        if (lane >= count && lane < need) value[lane] = none;
-        if (lane < count && rank < need) {
-          value[rank] = mine;
-          index[rank] = of;
+        const uint2 mine = lane < count ? list[lane] : make_uint2(0x7fffffffu, 0u);
+        const int rank = place(list, count, lane, __uint_as_float(mine.x));
+        if (lane >= count) {
+          picks[lane].x = 0x7fffffffu;  // fewer candidates than picks and one
+          picks[lane].y = 0u;
+        } else if (rank < need) {
+          picks[rank] = mine;
         }
         __syncwarp();
         if (lane < need) {
-          own = value[lane];
-          id = own == own ? index[lane] : 0;
+          const uint2 q = picks[lane];
+          own = __uint_as_float(q.x);
+          id = (int)q.y;
         }
       } else {
         for (int k = 0; k < need; k++) {
@@ -601,10 +612,10 @@ __global__ void __launch_bounds__(kWarps * 32, V <= 12 ? 4 : 2)
           const float last = __shfl_sync(0xffffffffu, own, K - 1);
           const float low = last - 2.0f * any - fabsf(last) * 0x1p-22f;
           if (fabsf(low) < INFINITY) {
-            const int more = gather<V>(c, col, low, lane, value, from);
+            const int more = gather<V>(c, col, low, lane, list);
             if (more <= 32) {
-              refine_picks<kSigmoid>(a, zt, bias, m, more, from, row, index);
-              id = lane < K ? index[lane] : 0;
+              refine_picks<kSigmoid>(a, zt, bias, m, more, list, row, picks);
+              id = lane < K ? (int)picks[lane].y : 0;
               x = to_f(zt[id]);
               again = false;
             }
@@ -622,7 +633,7 @@ __global__ void __launch_bounds__(kWarps * 32, V <= 12 ? 4 : 2)
     const bool again = mine < n && __ldcg(a.r.topk + ((int64_t)r * a.r.S + mine) * K) < 0;
     for (unsigned todo = __ballot_sync(0xffffffffu, again); todo; todo &= todo - 1) {
       const int64_t t = (int64_t)r * a.r.S + s0 + (int64_t)(__ffs(todo) - 1) * step;
-      again_exact<T>(a, (const T *)a.r.logits + t * E, row, best, index, t, cnt);
+      again_exact<T>(a, (const T *)a.r.logits + t * E, row, best, (int32_t *)list, t, cnt);
     }
   }
   __syncthreads();
