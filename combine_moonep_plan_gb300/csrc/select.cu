@@ -30,6 +30,11 @@ struct SelectArgs {
   const float *bias;  // [E] or null
   int groups, top_groups, sum_two, renormalize;
   float scale;
+  // Of the search for a group's best: its size; whether it is lanes' whole columns
+  // (a power of two of lanes), which then hold it in registers, or read from shared
+  // memory by as many lanes as there are for each; the logarithm of the lanes, and
+  // the turns they take.
+  int size, held, lanes_log, turns;
 };
 
 __device__ __forceinline__ uint64_t order_key64(double v) {
@@ -343,11 +348,11 @@ __device__ __noinline__ void again_exact(const SelectArgs &a, const T *z, uint64
 // l V + V - 1.  A row to be done again gets the id -1 as its first pick and its
 // turn after the warp's last row.
 //
-// Bound by instructions, some 900 a row, and the chains between them: with four
+// Bound by instructions, some 800 a row, and the chains between them: with four
 // blocks per SM (64 registers, a few of them spilled) 32768 rows of 256 in 8
-// groups take 41 us, without groups 34, 65536 bf16 rows of 384 66 us, where two or
-// three blocks without spills took 52 to 62, 62 and 77; loading the next row ahead
-// took 5 us more, sorting the candidates by warp-wide maxima 7.
+// groups take 41 us, without groups 32, 65536 bf16 rows of 384 61 us.  Two or three
+// blocks without spills took a quarter more; loading the next row ahead took 5 us
+// more, sorting the candidates by warp-wide maxima 7.
 template <typename T, int V, bool kSigmoid>
 __global__ void __launch_bounds__(kWarps * 32, V <= 12 ? 4 : 2)
     select_kernel(SelectArgs a, bool vec) {
@@ -365,7 +370,7 @@ __global__ void __launch_bounds__(kWarps * 32, V <= 12 ? 4 : 2)
   const int r = blockIdx.y, n = min(a.r.ntok[r], a.r.S);
   const bool grouped = a.top_groups < G;
   constexpr bool sigmoid = kSigmoid;
-  const int gs = E / G;
+  const int gs = a.size;
   const float none = __uint_as_float(0x7fffffffu);  // left out: no comparison holds
   for (int e = threadIdx.x; e < 32 * V; e += blockDim.x)
     bias[e] = a.bias && e < E ? __ldg(a.bias + e) : 0.0f;
@@ -383,14 +388,8 @@ __global__ void __launch_bounds__(kWarps * 32, V <= 12 ? 4 : 2)
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-  // Lanes that search a group for its best, a power of two: those that hold its
-  // columns where these are a lane's whole ones, else as many as there are, which
-  // read the columns from shared memory.
-  const int whole = gs % V == 0 ? gs / V : 0;
-  const bool held = whole && (whole & (whole - 1)) == 0 && whole <= 32;
-  int per = 0;  // its logarithm
-  while (held ? 1 << per < whole : 2 * G << per <= 32) per++;
-  const int gl = lane >> per, sub = lane & ((1 << per) - 1), turns = (gs + (1 << per) - 1) >> per;
+  const bool held = a.held;
+  const int per = a.lanes_log, gl = lane >> per, sub = lane & ((1 << per) - 1), turns = a.turns;
   // whether the whole row's scores are wanted, or logits are enough
   const bool scores = a.r.part_p || a.bias || (grouped && a.sum_two) ||
                       (!sigmoid && !a.renormalize);
@@ -717,15 +716,25 @@ size_t select_smem(int E, int G) {
   return w * (E + G + 16) * 8 + (w + 1) * E * 4;
 }
 
+// Logits of a lane in the kernel of rows in registers: no more than need be (160
+// experts in 8 groups of 20 take 27 us with five, whose lanes hold whole groups, and
+// 33 with eight).
+int per_lane(int E) {
+  return E <= 32 ? 1 : E <= 64 ? 2 : E <= 128 ? 4 : E <= 160 ? 5 : E <= 192 ? 6
+         : E <= 256 ? 8 : E <= 384 ? 12 : 16;
+}
+
 template <typename T, bool kSigmoid>
-auto select_kernel_for(int E) {
-  return E <= 32 ? select_kernel<T, 1, kSigmoid> : E <= 64 ? select_kernel<T, 2, kSigmoid>
-         : E <= 128 ? select_kernel<T, 4, kSigmoid> : E <= 256 ? select_kernel<T, 8, kSigmoid>
-         : E <= 384 ? select_kernel<T, 12, kSigmoid> : select_kernel<T, 16, kSigmoid>;
+auto select_kernel_for(int V) {
+  return V == 1 ? select_kernel<T, 1, kSigmoid> : V == 2 ? select_kernel<T, 2, kSigmoid>
+         : V == 4 ? select_kernel<T, 4, kSigmoid> : V == 5 ? select_kernel<T, 5, kSigmoid>
+         : V == 6 ? select_kernel<T, 6, kSigmoid> : V == 8 ? select_kernel<T, 8, kSigmoid>
+         : V == 12 ? select_kernel<T, 12, kSigmoid> : select_kernel<T, 16, kSigmoid>;
 }
 template <typename T>
 auto select_kernel_of(int E, bool sigmoid) {
-  return sigmoid ? select_kernel_for<T, true>(E) : select_kernel_for<T, false>(E);
+  const int V = per_lane(E);
+  return sigmoid ? select_kernel_for<T, true>(V) : select_kernel_for<T, false>(V);
 }
 
 template <typename T>
@@ -793,6 +802,11 @@ int launch_select(moonep_ctx *ctx, const void *logits, int bf16, int scoring,
   a.sum_two = sel.group_score == MOONEP_GROUP_TOP2;
   a.renormalize = sel.renormalize;
   a.scale = sel.scale;
+  a.size = c.E / sel.groups;
+  const int V = per_lane(c.E), whole = a.size % V == 0 ? a.size / V : 0;
+  a.held = whole > 0 && whole <= 32 && (whole & (whole - 1)) == 0;
+  while (a.held ? 1 << a.lanes_log < whole : 2 * sel.groups << a.lanes_log <= 32) a.lanes_log++;
+  a.turns = (a.size + (1 << a.lanes_log) - 1) >> a.lanes_log;
   f.tpe = tpe;
   f.coef = coef;
   f.loss = loss;

@@ -72,6 +72,10 @@ CASES = [
     (2, 64, 128, 8, 1, 1, "top2", "softmax", True, "bias", "bfloat16", None),
     (5, 33, 160, 6, 8, 3, "max", "softmax", False, "plain", "bfloat16", [33, 2, 0, 32, 9]),
     (5, 33, 160, 6, 8, 3, "top2", "softmax", True, "plain", "float32", None),
+    (3, 33, 132, 6, 4, 2, "top2", "sigmoid", True, "close", "float32", None),
+    (2, 33, 160, 6, 8, 3, "top2", "sigmoid", True, "ties", "float32", [33, 2]),
+    (4, 33, 192, 6, 8, 3, "max", "sigmoid", True, "close", "bfloat16", None),
+    (2, 33, 176, 9, 8, 5, "top2", "softmax", True, "masked", "float32", None),
     (8, 64, 256, 8, 8, 4, "top2", "sigmoid", True, "bias", "float32", None),
     (8, 64, 256, 8, 8, 4, "top2", "sigmoid", True, "close", "float32", None),
     (8, 33, 256, 8, 8, 4, "max", "sigmoid", False, "ties", "bfloat16", None),
