@@ -887,7 +887,8 @@ class Buffer:
               eps: float = 1e-8, weight_decay: float = 0.01, norm: torch.Tensor | None = None,
               max_norm: float | None = None, seed: int | None = None, weights=None) -> None:
         """One AdamW step, in place on `params` (all fp32 or all bf16) and on
-        their `state`; grads: matching tensors (all fp32 or all bf16).
+        their `state`; grads: matching tensors (all fp32 or all bf16).  Autograd
+        is not told: a graph that saved a parameter sees its new values.
           lr, step   host numbers, or tensors [1] (fp32, int32) in device memory,
                      which a captured step reads anew at every replay; the first
                      step is 1
