@@ -128,7 +128,10 @@ __device__ __forceinline__ int tiles_of(const GradArgs &a, int g, int rows) {
   return rows > 0 || (g < a.E && !a.add) ? a.nb * a.kb : 0;
 }
 
-// Tile t: its group and place in the group's gradient, tiles of n fastest.
+// Tile t: its group and place in the group's gradient, tiles of n fastest within
+// bands of eight, so that what all pairs work on at a time is about as high as it
+// is wide (7168 x 2048, 1024 rows, added to: 994 us for 48 gradients, 1049 with all
+// 28 tiles of n in a row).
 __device__ int4 tile_of(const GradArgs &a, const Shared *sh, int t) {
   int lo = 0, hi = (a.groups + a.per - 1) / a.per - 1;
   while (lo < hi) {
@@ -144,7 +147,8 @@ __device__ int4 tile_of(const GradArgs &a, const Shared *sh, int t) {
       if (rest < n) break;
       rest -= n;
     }
-  const int kt = rest / a.nb, nt = rest - kt * a.nb;
+  const int band = rest / (8 * a.kb), left = rest - band * 8 * a.kb;
+  const int wide = min(8, a.nb - band * 8), kt = left / wide, nt = band * 8 + left - kt * wide;
   const int j = g < a.E ? g / a.L : (g - a.E) / a.B;
   return make_int4(g, nt | kt << 16, j * a.NvS + start, rows);
 }

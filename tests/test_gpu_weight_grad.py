@@ -119,6 +119,12 @@ def test_few_sms(sms):
     _check(buf, cu, 1024, 1032, seed=sms)
 
 
+@pytest.mark.parametrize("N,Kd", [(2056, 264), (4360, 8), (2304, 520)])
+def test_more_tiles_than_a_band(N, Kd):
+    buf = _buffer(1, 3, 0, 200)
+    _check(buf, _cu(1, 3, 0, [70, 0, 33], buf.NvS), N, Kd)
+
+
 def test_long_segment():
     """Twenty thousand rows into one gradient."""
     buf = _buffer(1, 2, 0, 20011)
