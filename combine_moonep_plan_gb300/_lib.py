@@ -40,6 +40,7 @@ EXPORTS = (
     "moonep_dequantize_mx", "moonep_expert_product", "moonep_gated_act",
     "moonep_gated_act_backward", "moonep_grad_norm_workspace", "moonep_grad_norm",
     "moonep_adamw", "moonep_adamw_moments", "moonep_expert_weight_grad",
+    "moonep_expert_weight_grad_workspace",
     "moonep_route_select", "moonep_route_select_backward", "moonep_update_route_bias",
 )
 
@@ -146,7 +147,8 @@ def load(path: str = LIB_PATH):
         "moonep_expert_product": (ci, [vp, vp, vp, i64, vp, i64, vp, vp, ci, ci, ci, vp, vp]),
         "moonep_gated_act": (ci, [vp] * 5 + [ci] + [vp] * 6),
         "moonep_gated_act_backward": (ci, [vp] * 8 + [ci] + [vp] * 4),
-        "moonep_expert_weight_grad": (ci, [vp, vp, vp, i64, vp, i64, ci, ci, ci, vp, vp, vp]),
+        "moonep_expert_weight_grad": (ci, [vp, vp, vp, i64, vp, i64, ci, ci, ci, vp, vp, vp, vp]),
+        "moonep_expert_weight_grad_workspace": (ctypes.c_size_t, [vp, ci, ci]),
         "moonep_grad_norm_workspace": (ctypes.c_size_t, [vp]),
         "moonep_grad_norm": (ci, [vp, ci, vpp, i64p, ci, vp, vp, vp]),
         "moonep_adamw": (ci, [vp, ctypes.POINTER(MoonepAdamwConfig), ci, i64p] + [vpp] * 7 + [vp]),

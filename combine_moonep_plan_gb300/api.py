@@ -781,9 +781,14 @@ class Buffer:
         grad, slots = out
         gp = _check_tensor(grad, "grad", torch.float32, (self.E, N, Kd))
         sp = _check_tensor(slots, "slots", torch.float32, (self.R, self.B, N, Kd))
-        check(_lib.load().moonep_expert_weight_grad(
+        lib, work = _lib.load(), None
+        n = lib.moonep_expert_weight_grad_workspace(self._ctx, N, Kd)
+        if n:
+            work = torch.empty(n // 4, dtype=torch.float32, device=rows.device)
+        check(lib.moonep_expert_weight_grad(
             self._ctx, self._segments(cu_seqlens), xp, ldx, dp, ldd, N, Kd, bool(accumulate), gp,
-            sp, _stream()), "moonep_expert_weight_grad")
+            sp, None if work is None else work.data_ptr(), _stream()),
+            "moonep_expert_weight_grad")
         return grad, slots
 
     def gated_act(self, gate: torch.Tensor, up: torch.Tensor, cu_seqlens: torch.Tensor,

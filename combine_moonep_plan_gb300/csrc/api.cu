@@ -618,15 +618,27 @@ int moonep_expert_product(moonep_ctx *ctx, const int32_t *cu_seqlens, const uint
                         Kd, out, out_fp32 != 0, (cudaStream_t)stream);
 }
 
+// Sizes that a weight gradient's tiles and offsets allow.
+static bool grad_sizes_ok(const moonep_ctx *ctx, int N, int Kd) {
+  const int64_t groups = (int64_t)ctx->cfg.E + (int64_t)ctx->cfg.R * ctx->cfg.B;
+  return N >= 0 && N % 8 == 0 && Kd >= 0 && Kd % 8 == 0 && N <= 1 << 20 && Kd <= 1 << 20 &&
+         groups * ((N + 255) / 256) * ((Kd + 255) / 256) <= INT32_MAX - (1 << 20);
+}
+
+size_t moonep_expert_weight_grad_workspace(const moonep_ctx *ctx, int N, int Kd) {
+  if (check_ctx(ctx) || !grad_sizes_ok(ctx, N, Kd) || N == 0 || Kd == 0 || ctx->NvS == 0) return 0;
+  const int64_t groups = (int64_t)ctx->cfg.E + (int64_t)ctx->cfg.R * ctx->cfg.B;
+  const int shares = wgrad_shares(ctx, N, Kd);
+  return shares > 1 ? (size_t)shares * groups * N * Kd * sizeof(float) : 0;
+}
+
 int moonep_expert_weight_grad(moonep_ctx *ctx, const int32_t *cu_seqlens, const uint16_t *x,
                               int64_t x_row_bytes, const uint16_t *d, int64_t d_row_bytes, int N,
-                              int Kd, int accumulate, float *grad, float *slots, void *stream) {
+                              int Kd, int accumulate, float *grad, float *slots, void *workspace,
+                              void *stream) {
   int st = check_ctx(ctx);
   if (st) return st;
-  const int64_t groups = (int64_t)ctx->cfg.E + (int64_t)ctx->cfg.R * ctx->cfg.B;
-  if (N < 0 || N % 8 != 0 || Kd < 0 || Kd % 8 != 0 || N > 1 << 20 || Kd > 1 << 20 ||
-      groups * ((N + 255) / 256) * ((Kd + 255) / 256) > INT32_MAX - (1 << 20))
-    return MOONEP_ERR_INVALID_ARG;
+  if (!grad_sizes_ok(ctx, N, Kd)) return MOONEP_ERR_INVALID_ARG;
   if (N == 0 || Kd == 0) return MOONEP_OK;
   const bool extra = ctx->cfg.B > 0;
   if (!grad || !aligned16(grad) || (extra && (!slots || !aligned16(slots))))
@@ -642,8 +654,10 @@ int moonep_expert_weight_grad(moonep_ctx *ctx, const int32_t *cu_seqlens, const 
                                                     (cudaStream_t)stream));
   }
   if (!x || !d || !aligned16(x) || !aligned16(d)) return MOONEP_ERR_INVALID_ARG;
+  if (wgrad_shares(ctx, N, Kd) > 1 && (!workspace || !aligned16(workspace)))
+    return MOONEP_ERR_INVALID_ARG;
   return launch_wgrad(ctx, cu_seqlens, x, x_row_bytes, d, d_row_bytes, N, Kd, accumulate != 0,
-                      grad, slots, (cudaStream_t)stream);
+                      grad, slots, (float *)workspace, (cudaStream_t)stream);
 }
 
 int moonep_gated_act(moonep_ctx *ctx, const int32_t *cu_seqlens, const uint16_t *gate,

@@ -187,7 +187,8 @@ int launch_product(moonep_ctx *ctx, const int32_t *cu, const uint8_t *rows, int6
 int wgrad_clusters(int sms);  // CTA pairs resident at once on that many SMs (0: none)
 int launch_wgrad(moonep_ctx *ctx, const int32_t *cu, const uint16_t *x, int64_t x_pitch,
                  const uint16_t *d, int64_t d_pitch, int N, int Kd, int add, float *grad,
-                 float *slots, cudaStream_t st);
+                 float *slots, float *work, cudaStream_t st);
+int wgrad_shares(const moonep_ctx *ctx, int N, int Kd);  // tensors of its workspace (1: none)
 // The experts' gated activation.
 int launch_gated(moonep_ctx *ctx, const int32_t *cu, const uint16_t *gate, const uint16_t *up,
                  const float *w, int F, uint16_t *act, uint8_t *g8, uint8_t *u8, uint8_t *gs,

@@ -27,6 +27,8 @@
 //          order of nothing changes a result).  The tensor cores' own sums drop
 //          bits at every addition, 2e-6 of the result over 2000 rows, so they
 //          end after 512 rows and the epilogue adds the parts up in registers
+// Where the gradients are so few that their tiles leave SMs idle, the segments' rows
+// are split over tiles in a workspace, which join_kernel adds up in order.
 // Home experts without rows get zeros unless gradients are added to; slots
 // without rows are not touched.  Every wait has a limit of one second, after
 // which the kernel latches MOONEP_ERR_TIMEOUT, drains and returns; every warp
@@ -81,6 +83,10 @@ struct __align__(1024) Shared {
 struct GradArgs {
   const int32_t *cu;  // [R, EB]
   int E, B, L, EB, NvS, N, Kd, nb, kb;  // nb, kb: tiles of n and of k
+  // Shares: a segment's rows are split into so many (whole stages each), which
+  // fill tiles of their own in a workspace [shares, E + R*B, N, Kd] where there are
+  // several.  A group below is a share of one: weight row * shares + share.
+  int shares;
   int groups, per;    // groups, groups per table entry
   int add;
   int whole_d, whole_x;  // columns in whole blocks of 64
@@ -111,11 +117,11 @@ __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, bool add
       : "memory");
 }
 
-// Rows [start, start + rows) of group g in its rank's window; offsets outside
-// the window are reported and the segment treated as empty.
-__device__ __forceinline__ bool segment(const GradArgs &a, int g, int *start, int *rows) {
-  const int j = g < a.E ? g / a.L : (g - a.E) / a.B;
-  const int x = g < a.E ? g : a.E + (g - a.E) % a.B;
+// Rows [start, start + rows) of weight row w's segment in its rank's window; offsets
+// outside the window are reported and the segment treated as empty.
+__device__ __forceinline__ bool segment_of(const GradArgs &a, int w, int *start, int *rows) {
+  const int j = w < a.E ? w / a.L : (w - a.E) / a.B;
+  const int x = w < a.E ? w : a.E + (w - a.E) % a.B;
   const int32_t *cu = a.cu + (int64_t)j * a.EB;
   const int lo = x ? cu[x - 1] : 0, hi = cu[x];
   const bool bad = lo < 0 || hi < lo || hi > a.NvS;
@@ -123,9 +129,25 @@ __device__ __forceinline__ bool segment(const GradArgs &a, int g, int *start, in
   *rows = bad ? 0 : hi - lo;
   return !bad;
 }
+// Rows of a share of a segment, the last ones have fewer or none.
+__device__ __forceinline__ int share_rows(int rows, int shares) {
+  return ((rows + shares - 1) / shares + kDeep - 1) / kDeep * kDeep;
+}
+// The same of group g.
+__device__ __forceinline__ bool segment(const GradArgs &a, int g, int *start, int *rows) {
+  const bool ok = segment_of(a, g / a.shares, start, rows);
+  if (a.shares > 1) {
+    const int each = share_rows(*rows, a.shares), from = min(g % a.shares * each, *rows);
+    *start += from;
+    *rows = min(each, *rows - from);
+  }
+  return ok;
+}
 
 __device__ __forceinline__ int tiles_of(const GradArgs &a, int g, int rows) {
-  return rows > 0 || (g < a.E && !a.add) ? a.nb * a.kb : 0;
+  // home experts without rows are zeros, that the kernel after this one writes
+  // where there are shares
+  return rows > 0 || (g < a.E && !a.add && a.shares == 1) ? a.nb * a.kb : 0;
 }
 
 // Tile t: its group and place in the group's gradient, tiles of n fastest within
@@ -149,7 +171,7 @@ __device__ int4 tile_of(const GradArgs &a, const Shared *sh, int t) {
     }
   const int band = rest / (8 * a.kb), left = rest - band * 8 * a.kb;
   const int wide = min(8, a.nb - band * 8), kt = left / wide, nt = band * 8 + left - kt * wide;
-  const int j = g < a.E ? g / a.L : (g - a.E) / a.B;
+  const int w = g / a.shares, j = w < a.E ? w / a.L : (w - a.E) / a.B;
   return make_int4(g, nt | kt << 16, j * a.NvS + start, rows);
 }
 
@@ -412,9 +434,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int parts = (tile.w + kPart * kDeep - 1) / (kPart * kDeep);
       const int n = (tile.y & 0xffff) * kSide + (int)rank * 128 + q * 32;
       const int k0 = (tile.y >> 16) * kSide + half * 128;
-      const bool home = tile.x < a.E;
+      const bool home = tile.x < a.E || a.shares > 1;
       const CUtensorMap *map = home ? &map_home : &map_slots;
-      const int z = home ? tile.x : tile.x - a.E;
+      // the workspace's tensors are share by share
+      const int z = a.shares > 1 ? tile.x % a.shares * (a.groups / a.shares) + tile.x / a.shares
+                                 : home ? tile.x : tile.x - a.E;
       // gradients that are added to, on their way to L2 while the products run
       if (a.add && n < a.N && elect())
 #pragma unroll
@@ -482,6 +506,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
+// Adds up the shares of every gradient, in order.
+__global__ void __launch_bounds__(256)
+    join_kernel(const GradArgs a, const float4 *work, float4 *grad, float4 *slots, int add) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int weights = a.groups / a.shares;
+  const int64_t size = (int64_t)a.N * a.Kd / 4, whole = weights * size;
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < whole;
+       i += (int64_t)gridDim.x * blockDim.x) {
+    const int w = (int)(i / size);
+    int start, rows;
+    segment_of(a, w, &start, &rows);
+    const bool home = w < a.E;
+    if (rows == 0 && (add || !home)) continue;
+    float4 *to = home ? grad + i : slots + (i - (int64_t)a.E * size);
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const int each = share_rows(rows, a.shares);
+    for (int s = 0; s * each < rows; s++) {
+      const float4 p = __ldcs(work + s * whole + i);
+      v.x += p.x;
+      v.y += p.y;
+      v.z += p.z;
+      v.w += p.w;
+    }
+    if (add) {
+      const float4 o = *to;
+      v = make_float4(o.x + v.x, o.y + v.y, o.z + v.z, o.w + v.w);
+    }
+    *to = v;
+  }
+}
+
 constexpr size_t kSmem = sizeof(Shared) + 1024;
 static_assert(kSmem <= 227 * 1024, "shared memory");
 
@@ -535,17 +591,32 @@ int wgrad_clusters(int sms) {
   return n < sms / 2 ? n : (sms / 2 > 0 ? sms / 2 : 1);
 }
 
+// Shares of a segment's rows: as many as the pairs of SMs can take at once beside
+// each other, of 1024 rows or more if each rank's rows are spread evenly over its
+// experts.  (Two experts of 256 x 512, 65536 rows each: 51 us in 19 shares, 69 in
+// 38, 284 in one; eight of 512 x 512 with 8192 rows: 43 us in two, 48 in one; eight
+// of 256 x 256 with 1024 rows: 16 in two, 13 in one.)
+int wgrad_shares(const moonep_ctx *ctx, int N, int Kd) {
+  const int64_t tiles = (int64_t)ctx->cfg.E * ((N + kSide - 1) / kSide) * ((Kd + kSide - 1) / kSide);
+  const int64_t want = (int64_t)ctx->wgrad_clusters / tiles;
+  const int64_t most = (int64_t)ctx->NvS / ctx->L / (2 * kPart * kDeep);
+  const int64_t n = want < most ? want : most;
+  return (int)(n < 1 ? 1 : n > 64 ? 64 : n);
+}
+
 int launch_wgrad(moonep_ctx *ctx, const int32_t *cu, const uint16_t *x, int64_t x_pitch,
                  const uint16_t *d, int64_t d_pitch, int N, int Kd, int add, float *grad,
-                 float *slots, cudaStream_t st) {
+                 float *slots, float *work, cudaStream_t st) {
   const moonep_config &c = ctx->cfg;
   if (ctx->wgrad_clusters <= 0) return MOONEP_ERR_CUDA;
   const int64_t rows = (int64_t)c.R * ctx->NvS, extra = (int64_t)c.R * c.B;
+  const int shares = wgrad_shares(ctx, N, Kd);
   CUtensorMap md, mx, mh, ms;
   if (!rows_map(&md, d, N, rows, d_pitch) || !rows_map(&mx, x, Kd, rows, x_pitch) ||
-      !grad_map(&mh, grad, c.E, N, Kd))
+      !(shares > 1 ? grad_map(&mh, work, shares * (c.E + extra), N, Kd)
+                   : grad_map(&mh, grad, c.E, N, Kd)))
     return MOONEP_ERR_CUDA;
-  if (extra == 0)
+  if (extra == 0 || shares > 1)
     ms = mh;  // no group reads it
   else if (!grad_map(&ms, slots, extra, N, Kd))
     return MOONEP_ERR_CUDA;
@@ -560,14 +631,21 @@ int launch_wgrad(moonep_ctx *ctx, const int32_t *cu, const uint16_t *x, int64_t 
   a.Kd = Kd;
   a.nb = (N + kSide - 1) / kSide;
   a.kb = (Kd + kSide - 1) / kSide;
-  a.groups = (int)(c.E + extra);
+  a.shares = shares;
+  a.groups = (int)(c.E + extra) * shares;
   a.per = (a.groups + kEntries - 1) / kEntries;
-  a.add = add;
+  a.add = add && shares == 1;
   a.whole_d = N % 64 == 0;
   a.whole_x = Kd % 64 == 0;
   a.status = ctx->d_status;
-  return cuda_status(launch_pdl(wgrad_kernel, dim3(2 * ctx->wgrad_clusters), dim3(kThreads), kSmem,
-                                st, false, md, mx, mh, ms, a));
+  cudaError_t e = launch_pdl(wgrad_kernel, dim3(2 * ctx->wgrad_clusters), dim3(kThreads), kSmem, st,
+                             false, md, mx, mh, ms, a);
+  if (e == cudaSuccess && shares > 1) {
+    const int64_t need = ((c.E + extra) * N * Kd / 4 + 255) / 256, most = (int64_t)ctx->sms * 8;
+    e = launch_pdl(join_kernel, dim3((unsigned)(need < most ? need : most)), dim3(256), 0, st,
+                   false, a, (const float4 *)work, (float4 *)grad, (float4 *)slots, add);
+  }
+  return cuda_status(e);
 }
 
 }  // namespace moonep

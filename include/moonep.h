@@ -529,14 +529,19 @@ int moonep_expert_product(moonep_ctx *ctx, const int32_t *cu_seqlens,
  *                without rows
  *   slots        [R, B, N, Kd] fp32 (may be NULL when B = 0): the slots', those
  *                without rows are not touched (moonep_reduce_redundant_grad's Gs)
- * accumulate: both are added to instead (one addition per element).  N % 8 == 0,
- * Kd % 8 == 0, each at most 2^20.  Runs on pairs of SMs: at least one pair,
+ *   workspace    moonep_expert_weight_grad_workspace(ctx, N, Kd) bytes of device
+ *                memory, 16-byte aligned, the call's own until it has run (0: NULL
+ *                will do): few small gradients are computed in shares of their rows
+ * accumulate: both are added to instead (one addition per element).  Sums are in a
+ * fixed order.  N % 8 == 0, Kd % 8 == 0, each at most 2^20.  Runs on pairs of SMs: at least one pair,
  * however few SMs the context may use. */
+size_t moonep_expert_weight_grad_workspace(const moonep_ctx *ctx, int N,
+                                           int Kd);
 int moonep_expert_weight_grad(moonep_ctx *ctx, const int32_t *cu_seqlens,
                               const uint16_t *x, int64_t x_row_bytes,
                               const uint16_t *d, int64_t d_row_bytes, int N,
                               int Kd, int accumulate, float *grad,
-                              float *slots, void *stream);
+                              float *slots, void *workspace, void *stream);
 
 /* The experts' gated activation over the dispatched layout, times the route
  * weight (combine sums unweighted):

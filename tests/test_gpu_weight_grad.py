@@ -125,6 +125,32 @@ def test_more_tiles_than_a_band(N, Kd):
     _check(buf, _cu(1, 3, 0, [70, 0, 33], buf.NvS), N, Kd)
 
 
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("N,Kd", [(264, 72), (8, 8), (256, 512)])
+def test_shares_of_long_segments(N, Kd, accumulate):
+    """Few small gradients over many rows: each is computed in shares of its rows."""
+    from combine_moonep_plan_gb300 import _lib
+    buf = _buffer(2, 4, 1, 6000)
+    n = _lib.load().moonep_expert_weight_grad_workspace(buf._ctx, N, Kd)
+    assert n >= 2 * 6 * N * Kd * 4 and n % (6 * N * Kd * 4) == 0
+    for turn, lengths in enumerate(([2500, 0, 1, 700, 63, 512], [5900, 3, 0, 65, 17, 3001],
+                                    [0], [64, 320, 1900])):
+        _check(buf, _cu(2, 4, 1, lengths, buf.NvS), N, Kd, seed=turn, accumulate=accumulate)
+    # the same twice, and from a capture
+    cu = torch.from_numpy(_cu(2, 4, 1, [2500, 0, 1, 700, 63, 512], buf.NvS)).cuda()
+    x, d = (torch.randn(2 * buf.NvS, c, device="cuda").bfloat16() for c in (Kd, N))
+    first = buf.expert_weight_grad(x, d, cu)
+    out = tuple(torch.zeros_like(t) for t in first)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        buf.expert_weight_grad(x, d, cu, out=out)
+    for _ in range(2):
+        for t in out:
+            t.zero_()
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(first, out))
+
+
 def test_long_segment():
     """Twenty thousand rows into one gradient."""
     buf = _buffer(1, 2, 0, 20011)

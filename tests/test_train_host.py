@@ -22,7 +22,8 @@ def test_null_context_refused(lib):
     assert lib.moonep_route_select(n, n, 0, 0, sel, 0.0, 0, n, n, n, n, n, n, n) == bad
     assert lib.moonep_route_select_backward(n, n, 0, 0, sel, n, n, n, n, n, n, n, n) == bad
     assert lib.moonep_update_route_bias(n, n, n, 0.0, n, n) == bad
-    assert lib.moonep_expert_weight_grad(n, n, n, 16, n, 16, 8, 8, 0, n, n, n) == bad
+    assert lib.moonep_expert_weight_grad(n, n, n, 16, n, 16, 8, 8, 0, n, n, n, n) == bad
+    assert lib.moonep_expert_weight_grad_workspace(n, 8, 8) == 0
     assert lib.moonep_grad_norm_workspace(n) == 0
     assert lib.moonep_grad_norm(n, 0, n, n, 0, n, n, n) == bad
     assert lib.moonep_adamw(n, cfg, 0, n, n, n, n, n, n, n, n, n) == bad
