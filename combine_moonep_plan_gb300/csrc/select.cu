@@ -6,7 +6,8 @@
 //   v_g = the largest c in group g, or the sum of its two largest
 //   picks = the K largest c among the top groups (equal: lowest index)
 //   w_k = scale a_k / sum_picks a, or scale a_k       weighs, without the bias
-// Without a bias the order of c is that of the logits, and these are compared.
+// Without a bias the order of c is that of the logits, and these are compared: expert
+// with expert, and groups by their largest.
 //
 // The order of c is that of its value in 64 bits.  In fp32 two neighbours may
 // come out the wrong way round, so the picks are made in fp32 with a bound on
@@ -54,7 +55,12 @@ __device__ __forceinline__ void select_exact(const SelectArgs &a, const T *z, ui
                                           uint64_t *best, int32_t *index) {
   const int lane = threadIdx.x & 31, E = a.r.E, gs = E / a.groups;
   const bool grouped = a.top_groups < a.groups;
-  if (a.bias || grouped) {
+  // as in select_kernel: without a bias the logits themselves order the experts, and
+  // groups by their largest (two logits may have one score in 64 bits)
+  if (!a.bias && !(grouped && a.sum_two)) {
+    for (int e = lane; e < E; e += 32) row[e] = order_key(to_f(z[e]));
+    __syncwarp();
+  } else {
     float m = -INFINITY;
     double Z = 1.0;
     if (!a.r.sigmoid) {
@@ -102,7 +108,7 @@ __device__ __forceinline__ void select_exact(const SelectArgs &a, const T *z, ui
         before += best[h] > best[g] || (best[h] == best[g] && h < g);
       in = before < a.top_groups;
     }
-    if (!a.bias) row[e] = (uint64_t)order_key(to_f(z[e]));
+    if (!a.bias) row[e] = order_key(to_f(z[e]));
     if (!in) row[e] = 0;
   }
   __syncwarp();

@@ -431,7 +431,8 @@ int moonep_route_backward(moonep_ctx *ctx, const void *logits, int logits_bf16,
  * (MOONEP_GROUP_MAX) or the sum of the two largest (MOONEP_GROUP_TOP2; the one
  * of a group of one), and the picks are the K largest c within the top_groups
  * best groups; equal values by lowest index, a NaN first.  The order is that
- * of c in 64 bits; without a bias that of the logits.
+ * of c in 64 bits; without a bias that of the logits, of experts and of groups by
+ * their largest (sums of two are those of c).
  *   w_sk   scale a of the picks over their sum (renormalize; 0 when that is 0),
  *          or scale a; the bias weighs nothing
  * Everything else as moonep_route.  bias: [E] fp32 in device memory or NULL;
