@@ -152,10 +152,16 @@ __device__ __forceinline__ void write_picks(const SelectArgs &a, bool sigmoid, i
 #pragma unroll
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   }
-  const float v = mine ? score(z, top, sigmoid) : 0.0f;
+  float v = mine ? score(z, top, sigmoid) : 0.0f;
   if (a.renormalize) {
     const float sum = warp_sum(v);
     by = sum == 0.0f ? 0.0f : a.scale * inverse(sum);
+    // scale over a sum below 1 may pass the largest number: the shares first, none
+    // of which is above 1 (softmax scores add up to 1 or more)
+    if (sigmoid && fabsf(by) == INFINITY) {
+      v *= inverse(sum);
+      by = a.scale;
+    }
   } else {
     by = sigmoid ? a.scale : a.scale * inv;
   }

@@ -56,3 +56,42 @@ def test_groups_by_logits(scoring, E, K, groups, top, nan):
                         balance=balance)
         assert np.array_equal(out.topk.cpu().numpy(), want)
     assert buf.get_status() == 0
+
+
+# name: (logits of the picks, scale)
+SMALL = {"one": ([-86.5], 16.0), "two": ([-86.0, -87.0], 16.0),
+         "beside none": ([-86.5, -100.0], 16.0), "many": ([-86.9] * 8, 100.0), "all lost": ([-90.0, -95.0], 16.0),
+         "largest scale": ([-2.0, -3.0, -2.5], 3.4e38), "negative": ([-85.0, -86.5], -1e6),
+         "ordinary": ([1.0, 0.5, -0.25], 2.5)}
+
+
+@pytest.mark.parametrize("E", [32, 700])
+@pytest.mark.parametrize("name", sorted(SMALL))
+def test_weights_of_small_scores(name, E):
+    """Normalised weights are scale times shares, whatever the scores' sum: a score
+    below 2^-126 counts as 0, the others' errors are those of exp(|z|), |z| 2^-24
+    relative, and a few roundings."""
+    picks, scale = SMALL[name]
+    K = len(picks)
+    z = np.full((1, 3, E), -200.0, np.float32)
+    z[..., 3:3 + K] = picks
+    buf = _buffer(1, 3, K, E)
+    t = torch.from_numpy(z).cuda()
+    out = buf.route(t, scoring="sigmoid", scale=scale)
+    zn = z.astype(np.float64)
+    ids = ref.select(zn, K, "sigmoid", None, 1, 1, "max")
+    assert np.array_equal(out.topk.cpu().numpy(), ids)
+    s = base.sigmoid(np.take_along_axis(zn, ids, -1))
+    s[s < 2.0 ** -126] = 0
+    total = s.sum(-1, keepdims=True)
+    w = scale * np.divide(s, total, out=np.zeros_like(s), where=total > 0)
+    tol = (100 + K + 16) * EPS * np.abs(w)
+    assert np.all(np.abs(out.weights.double().cpu().numpy() - w) <= tol)
+    dw = np.linspace(-1, 1, 3 * K).reshape(1, 3, K).astype(np.float32)
+    dz = buf.route_backward(out, t, torch.from_numpy(dw).cuda()).double().cpu().numpy()
+    dw, none = dw.astype(np.float64), np.zeros((1, E))
+    want, _ = ref.select_grad(zn, ids, w, dw, none, 0.0, "sigmoid", [3], True, scale)
+    # the terms' magnitudes are those of |w| and |scale|: with a negative w the
+    # reference's |d_w| + sum w |d_w| / |scale| is a difference, not their sum
+    _, mag = ref.select_grad(zn, ids, np.abs(w), dw, none, 0.0, "sigmoid", [3], True, abs(scale))
+    assert np.all(np.abs(dz - want) <= (3 * 100 + E + K + 48) * EPS * mag + 1e-30)
