@@ -897,6 +897,7 @@ class Buffer:
           lr, step   host numbers, or tensors [1] (fp32, int32) in device memory,
                      which a captured step reads anew at every replay; the first
                      step is 1
+          eps        from 2^-126 to 2^125
           norm       grad_norm's: gradients are scaled by min(1, max_norm/norm),
                      and a norm that is not finite leaves everything as it was
           seed       moments in 8 bits and bf16 parameters are rounded at random,

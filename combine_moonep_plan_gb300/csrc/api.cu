@@ -740,9 +740,9 @@ int moonep_adamw(moonep_ctx *ctx, const moonep_adamw_config *h, int n_tensors,
   if (st) return st;
   if (!h || (h->bits != 32 && h->bits != 8) || !sizes_ok(n_tensors, sizes))
     return MOONEP_ERR_INVALID_ARG;
-  // written so that a NaN is refused
-  if (!(h->beta1 >= 0 && h->beta1 < 1 && h->beta2 >= 0 && h->beta2 < 1 && h->eps > 0 &&
-        h->eps <= FLT_MAX && (float)h->eps > 0 && h->lr - h->lr == 0 &&
+  // written so that a NaN is refused; eps as the update's inverse needs it
+  if (!(h->beta1 >= 0 && h->beta1 < 1 && h->beta2 >= 0 && h->beta2 < 1 && h->eps >= FLT_MIN &&
+        h->eps <= 0x1p125 && h->lr - h->lr == 0 &&
         h->weight_decay - h->weight_decay == 0) ||
       (!h->step_dev && h->step < 1) || (h->norm && !(h->max_norm > 0)) ||
       !aligned4(h->norm) || !aligned4(h->lr_dev) || !aligned4(h->step_dev))

@@ -206,12 +206,12 @@ struct AdamwCall {
   void *const *m, *const *v;
   uint8_t *const *ms, *const *vs;  // 8 bits
   uint16_t *const *w;              // or null
+  bool tiny;                       // a v below 2^-126 counts beside eps
 };
 int norm_blocks(const moonep_ctx *ctx);  // most blocks of the norm's sums
 int launch_grad_norm(moonep_ctx *ctx, const AdamwCall &c, double *part, float *norm,
                      cudaStream_t st);
-int launch_adamw(moonep_ctx *ctx, const AdamwCall &c, const moonep_adamw_config &h,
-                 cudaStream_t st);
+int launch_adamw(moonep_ctx *ctx, AdamwCall c, const moonep_adamw_config &h, cudaStream_t st);
 int launch_adamw_moments(moonep_ctx *ctx, int64_t n, const uint8_t *m8, const uint8_t *ms,
                          const uint8_t *v8, const uint8_t *vs, int fp32, void *m, void *v,
                          cudaStream_t st);

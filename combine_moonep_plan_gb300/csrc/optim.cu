@@ -17,8 +17,8 @@
 // Rounding is to nearest even, or with a seed up with the probability that
 // makes it right on average: b2 = 0.999 moves v by a thousandth per step, and
 // to nearest on a grid of steps of a tenth it would never move.  A v above zero
-// keeps at least the least code, so an update never divides by eps alone for
-// want of range.  The stored values' error does not enter the update of its own
+// keeps at least the least code, so an update never divides by eps alone because
+// of the codes' range.  The stored values' error does not enter the update of its own
 // step: p is computed from m and v before they are rounded.
 //
 // Measured (the kernels alone, 704 million parameters in three tensors): fp32
@@ -171,11 +171,17 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return make_float2(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y));
 }
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+// Square root; a subnormal's is 0 unless it is asked for (TINY).
+template <bool TINY>
 __device__ __forceinline__ float sqrt_fast(float x) {
   float r;
-  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  if (TINY)
+    asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  else
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+// 1 / x for x from 2^-126 to 2^126, which eps and the root's size keep it within.
 __device__ __forceinline__ float inverse(float x) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -286,7 +292,12 @@ __device__ void device_scalars(const StepArgs &a, Scalars *s) {
   s->key = mix(a.seed + mix((uint32_t)t));
 }
 
-template <typename P, typename G, int BITS, int N>
+// TINY: eps is small enough for the root of a v below 2^-126 to count beside it.
+// With 8-bit moments, where instructions count, that root costs 2 to 3 % (704 million
+// values rounded at random, fp32 parameters 1.68 ms for 1.64, bf16 1.95 for 1.89; a
+// branch on eps in one kernel as much), so they take it only then; with 32-bit ones,
+// bound by memory, always.
+template <typename P, typename G, int BITS, bool TINY, int N>
 __global__ void __launch_bounds__(kThreads, BITS == 8 && sizeof(P) == 4 ? 5 : 6)
     adamw_kernel(const __grid_constant__ Table<N> tab, const __grid_constant__ StepArgs a) {
   pdl_wait();
@@ -334,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, BITS == 8 && sizeof(P) == 4 ? 5 : 6)
         const float x = __fmul_rn(g[k], clip);
         f[k] = __fadd_rn(__fmul_rn(s.b1, f[k]), __fmul_rn(s.c1, x));
         h[k] = __fadd_rn(__fmul_rn(s.b2, h[k]), __fmul_rn(__fmul_rn(s.c2, x), x));
-        p[k] = p[k] * s.decay - s.rate * (f[k] * inverse(sqrt_fast(h[k]) * s.root + s.eps));
+        p[k] = p[k] * s.decay - s.rate * (f[k] * inverse(sqrt_fast<TINY>(h[k]) * s.root + s.eps));
       }
       if (live) {
         store8((float *)tab.m[t] + i, f);
@@ -356,8 +367,8 @@ __global__ void __launch_bounds__(kThreads, BITS == 8 && sizeof(P) == 4 ? 5 : 6)
         const float2 x = mul2(make_float2(g[2 * k], g[2 * k + 1]), both(clip));
         m[k] = add2(mul2(both(s.b1), m[k]), mul2(both(s.c1), x));
         v[k] = add2(mul2(both(s.b2), v[k]), mul2(mul2(both(s.c2), x), x));
-        const float2 den = fma2(make_float2(sqrt_fast(v[k].x), sqrt_fast(v[k].y)), both(s.root),
-                                both(s.eps));
+        const float2 den = fma2(make_float2(sqrt_fast<TINY>(v[k].x), sqrt_fast<TINY>(v[k].y)),
+                                both(s.root), both(s.eps));
         const float2 q = mul2(m[k], make_float2(inverse(den.x), inverse(den.y)));
         const float2 y = fma2(both(-s.rate), q, mul2(make_float2(p[2 * k], p[2 * k + 1]),
                                                      both(s.decay)));
@@ -478,8 +489,9 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 template <typename P, typename G, int N>
-auto adamw_kernel_of(int bits) {
-  return bits == 32 ? adamw_kernel<P, G, 32, N> : adamw_kernel<P, G, 8, N>;
+auto adamw_kernel_of(int bits, bool tiny) {
+  return bits == 32 ? adamw_kernel<P, G, 32, true, N>
+         : tiny     ? adamw_kernel<P, G, 8, true, N> : adamw_kernel<P, G, 8, false, N>;
 }
 
 // Blocks: as many as are resident at once on the SMs that the context may use.
@@ -554,7 +566,7 @@ int adamw_run(moonep_ctx *ctx, const AdamwCall &c, StepArgs a, cudaStream_t st) 
     from += fill(&tab, c, from, true);
     const int chunks = tab.first[tab.count];
     if (chunks == 0) continue;
-    auto kern = adamw_kernel_of<P, G, N>(c.bits);
+    auto kern = adamw_kernel_of<P, G, N>(c.bits, c.tiny);
     const cudaError_t e = launch_pdl(kern, dim3((unsigned)step_blocks(ctx, c, kern, chunks)),
                                      dim3(kThreads), 0, st, false, tab, a);
     if (e != cudaSuccess) return cuda_status(e);
@@ -601,9 +613,11 @@ int launch_grad_norm(moonep_ctx *ctx, const AdamwCall &c, double *part, float *n
              : norm_run<float, kManyTensors>(ctx, c, part, norm, st);
 }
 
-int launch_adamw(moonep_ctx *ctx, const AdamwCall &c, const moonep_adamw_config &h,
-                 cudaStream_t st) {
+int launch_adamw(moonep_ctx *ctx, AdamwCall c, const moonep_adamw_config &h, cudaStream_t st) {
   StepArgs a{};
+  // v below 2^-126: sqrt(v) / sqrt(1 - b2^t) is below 2^-63 / sqrt(1 - b2), which is
+  // half an ulp of any other eps or less
+  c.tiny = !(h.eps * sqrt(1.0 - h.beta2) >= 0x1p-39);
   a.norm = h.norm;
   a.max_norm = h.max_norm;
   a.lr_dev = h.lr_dev;

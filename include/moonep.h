@@ -588,8 +588,8 @@ int moonep_grad_norm(moonep_ctx *ctx, int n_tensors, const void *const *g,
  *   m = beta1 m + (1 - beta1) g'    v = beta2 v + (1 - beta2) g'^2
  *   p = p (1 - lr wd) - lr / (1 - beta1^step) m /
  *                       (sqrt(v) / sqrt(1 - beta2^step) + eps)
- * in fp32 (a v below 2^-126 counts as 0 beside eps).  When norm[0] is not finite
- * the call changes nothing.  No two tensors overlap.
+ * in fp32, subnormals kept (a g'^2 (1 - beta2) below 2^-150 is 0).  When norm[0] is
+ * not finite the call changes nothing.  No two tensors overlap.
  *   p, g     n_tensors host arrays of device pointers, fp32 or bf16 (one type
  *            per call each), any element alignment; sizes: elements, >= 0
  *   m, v     bits 32: fp32; bits 8: codes, uint8, with ms, vs their scales;
@@ -608,7 +608,7 @@ int moonep_grad_norm(moonep_ctx *ctx, int n_tensors, const void *const *g,
  *   lr_dev, step_dev   device scalars used in place of lr and step when given
  *            (a captured step then goes on from replay to replay); a step below
  *            1 there counts as 1
- * 0 <= beta < 1, eps > 0, step >= 1, and max_norm > 0 with a norm. */
+ * 0 <= beta < 1, 2^-126 <= eps <= 2^125, step >= 1, and max_norm > 0 with a norm. */
 typedef struct moonep_adamw_config {
   double lr, beta1, beta2, eps, weight_decay;
   const float *lr_dev;
