@@ -249,11 +249,12 @@ class AdamWState:
     One allocation per kind, every tensor's part starting on a multiple of 32
     elements; `tensors` is (m, v) in fp32, or with bits=8 (m codes, m scales,
     v codes, v scales) in uint8, a scale for every 32 codes.  All zero is the
-    state before the first step.  `sizes` are the tensors' elements and
-    `offsets` the places of their first ones."""
+    state before the first step.  Other tensors of the same type, size and device
+    may take their place.  `sizes` are the tensors' elements and `offsets` the
+    places of their first ones."""
 
     __slots__ = ("tensors", "bits", "sizes", "offsets", "total", "_buffer", "_c_sizes", "_c_ptrs",
-                 "_base")
+                 "_base", "_layout")
 
     def __init__(self, buffer: "Buffer", sizes, bits: int, device):
         self.bits, self.sizes, self._buffer = bits, tuple(sizes), buffer
@@ -269,10 +270,21 @@ class AdamWState:
                                  for d in (1, 32, 1, 32))
         self._c_sizes = (ctypes.c_int64 * len(self.sizes))(*self.sizes)
         self._base = None
+        self._layout = [(t.dtype, t.device, t.shape) for t in self.tensors]
+
+    def _checked(self):
+        """The moments' tensors, which may have been replaced."""
+        if [(t.dtype, t.device, t.shape) for t in self.tensors] != self._layout:
+            raise ValueError("state: tensors have to be of " + ", ".join(
+                f"{n[0]} {k} on {d}" for k, d, n in self._layout) + "; got " + ", ".join(
+                f"{tuple(t.shape)} {t.dtype} on {t.device}" for t in self.tensors))
+        if not all(t.is_contiguous() for t in self.tensors):
+            raise ValueError("state: tensors must be contiguous")
+        return self.tensors
 
     def _pointers(self):
         """The C arrays of every tensor's moments: m, v, m scales, v scales."""
-        base = tuple(t.data_ptr() for t in self.tensors)
+        base = tuple(t.data_ptr() for t in self._checked())
         if base != self._base:
             if self.bits == 32:
                 m, v = (_lib.ptr_array([b + 4 * o for o in self.offsets]) for b in base)
@@ -288,10 +300,10 @@ class AdamWState:
         """(m, v), flat: the fp32 moments themselves, or in `dtype` (bf16 or
         fp32) the values that the 8-bit ones stand for."""
         if self.bits == 32:
-            return self.tensors
+            return self._checked()
         if dtype not in _FLOATS:
             raise TypeError(f"dtype: expected one of {_FLOATS}, got {dtype}")
-        m8, ms, v8, vs = self.tensors
+        m8, ms, v8, vs = self._checked()
         m, v = (torch.empty(self.total, dtype=dtype, device=m8.device) for _ in range(2))
         check(_lib.load().moonep_adamw_moments(
             self._buffer._ctx, self.total, m8.data_ptr(), ms.data_ptr(), v8.data_ptr(),
