@@ -80,14 +80,21 @@ def _one_of(t, name, dtypes):
 
 
 _kind, _place = operator.attrgetter("dtype"), torch.Tensor.get_device
+_shape, _dims = operator.attrgetter("shape"), torch.Tensor.dim
+_look = operator.attrgetter("dtype", "device", "shape")
 _ptr, _numel, _whole = torch.Tensor.data_ptr, torch.Tensor.numel, torch.Tensor.is_contiguous
 
 
 def _check_list(tensors, name, dtypes, sizes):
     """Contiguous CUDA tensors of one type out of `dtypes`, of `sizes` elements
-    where given: (type, addresses, sizes).  Every look at a tensor costs a
-    twentieth of a microsecond and there may be hundreds, so each property is
-    asked of all of them at a time."""
+    where given: (type, addresses, sizes)."""
+    return _look_over(tensors, name, dtypes, sizes)[:3]
+
+
+def _look_over(tensors, name, dtypes, sizes):
+    """_check_list, and the device's number (None: no tensors).  Every look at a
+    tensor costs a twentieth of a microsecond and there may be hundreds, so each
+    property is asked of all of them at a time."""
     count = list(map(_numel, tensors))
     if sizes is not None and (len(count) != len(sizes) or count != list(sizes)):
         raise ValueError(f"{name}: expected tensors of {list(sizes)[:8]}... elements, got "
@@ -103,7 +110,26 @@ def _check_list(tensors, name, dtypes, sizes):
         raise ValueError(f"{name}: must be CUDA tensors of one device")
     if not all(map(_whole, tensors)):
         raise ValueError(f"{name}: must be contiguous")
-    return dtype, list(map(_ptr, tensors)), count
+    return dtype, list(map(_ptr, tensors)), count, places.pop() if places else None
+
+
+def _check_shapes(tensors, name, params):
+    """Tensors of the shapes of `params`, or of the same elements in another number
+    of dimensions (views of a flat buffer, say): equal counts alone would let a
+    transposed one pass.  Flat parameters match any."""
+    if not params or max(map(_dims, params)) < 2:
+        return
+    have, want = list(map(_shape, tensors)), list(map(_shape, params))
+    if have != want:
+        for k, (h, s) in enumerate(zip(have, want)):
+            if h != s and len(h) == len(s):
+                raise ValueError(f"{name}: expected the parameters' shapes, got {tuple(h)} for "
+                                 f"{tuple(s)} at {k}")
+
+
+def _check_one_device(places):
+    if len(places - {None}) > 1:
+        raise ValueError("params, grads, state, weights and device scalars must be on one device")
 
 
 def _check_rows(t, name, rows, cols):
@@ -254,7 +280,7 @@ class AdamWState:
     places of their first ones."""
 
     __slots__ = ("tensors", "bits", "sizes", "offsets", "total", "_buffer", "_c_sizes", "_c_ptrs",
-                 "_base", "_layout")
+                 "_base", "_layout", "_known")
 
     def __init__(self, buffer: "Buffer", sizes, bits: int, device):
         self.bits, self.sizes, self._buffer = bits, tuple(sizes), buffer
@@ -269,22 +295,28 @@ class AdamWState:
             self.tensors = tuple(torch.zeros(at // d, dtype=torch.uint8, device=device)
                                  for d in (1, 32, 1, 32))
         self._c_sizes = (ctypes.c_int64 * len(self.sizes))(*self.sizes)
-        self._base = None
-        self._layout = [(t.dtype, t.device, t.shape) for t in self.tensors]
+        self._base = self._known = None
+        self._layout = list(map(_look, self.tensors))
 
     def _checked(self):
         """The moments' tensors, which may have been replaced."""
-        if [(t.dtype, t.device, t.shape) for t in self.tensors] != self._layout:
-            raise ValueError("state: tensors have to be of " + ", ".join(
-                f"{n[0]} {k} on {d}" for k, d, n in self._layout) + "; got " + ", ".join(
-                f"{tuple(t.shape)} {t.dtype} on {t.device}" for t in self.tensors))
-        if not all(t.is_contiguous() for t in self.tensors):
+        tensors = self.tensors
+        if list(map(_look, tensors)) != self._layout:
+            raise ValueError(f"state: expected tensors of (type, device, shape) {self._layout}, "
+                             f"got {list(map(_look, tensors))}")
+        if not all(map(_whole, tensors)):
             raise ValueError("state: tensors must be contiguous")
-        return self.tensors
+        return tensors
 
     def _pointers(self):
         """The C arrays of every tensor's moments: m, v, m scales, v scales."""
-        base = tuple(t.data_ptr() for t in self._checked())
+        tensors = self.tensors
+        base = tuple(map(_ptr, tensors))
+        # the same tuple of tensors at the same places has been looked at before (a
+        # tensor keeps its storage, or its place changes)
+        if tensors is not self._known or base != self._base:
+            self._checked()
+            self._known = tensors if type(tensors) is tuple else None
         if base != self._base:
             if self.bits == 32:
                 m, v = (_lib.ptr_array([b + 4 * o for o in self.offsets]) for b in base)
@@ -904,8 +936,9 @@ class Buffer:
               eps: float = 1e-8, weight_decay: float = 0.01, norm: torch.Tensor | None = None,
               max_norm: float | None = None, seed: int | None = None, weights=None) -> None:
         """One AdamW step, in place on `params` (all fp32 or all bf16) and on
-        their `state`; grads: matching tensors (all fp32 or all bf16).  Autograd
-        is not told: a graph that saved a parameter sees its new values.
+        their `state`; grads: matching tensors (all fp32 or all bf16; of the same
+        shapes, or flat).  Autograd is not told: a graph that saved a parameter
+        sees its new values.
           lr, step   host numbers, or tensors [1] (fp32, int32) in device memory,
                      which a captured step reads anew at every replay; the first
                      step is 1
@@ -917,18 +950,23 @@ class Buffer:
           weights    for fp32 params: bf16 tensors (or None) that receive the
                      rounded parameters, e.g. the experts' rows W[:E]"""
         params, grads = list(params), list(grads)
-        pt, pp, _ = _check_list(params, "params", _FLOATS, state.sizes)
-        gt, gp, _ = _check_list(grads, "grads", _FLOATS, state.sizes)
-        wp = None
+        pt, pp, _, on = _look_over(params, "params", _FLOATS, state.sizes)
+        gt, gp, _, g_on = _look_over(grads, "grads", _FLOATS, state.sizes)
+        _check_shapes(grads, "grads", params)
+        m, v, ms, vs = state._pointers()
+        places, wp = {on, g_on, state.tensors[0].get_device()}, None
         if weights is not None:
             if pt != torch.float32:
                 raise TypeError("weights: only beside fp32 params")
             weights = list(weights)
             if len(weights) != len(params):
                 raise ValueError(f"weights: expected {len(params)} tensors")
-            given = [(t, n) for t, n in zip(weights, state.sizes) if t is not None]
-            _, to, _ = _check_list([t for t, _ in given], "weights", (torch.bfloat16,),
-                                   [n for _, n in given])
+            of = [k for k, t in enumerate(weights) if t is not None]
+            given = [weights[k] for k in of]
+            _, to, _, on = _look_over(given, "weights", (torch.bfloat16,),
+                                      [state.sizes[k] for k in of])
+            places.add(on)
+            _check_shapes(given, "weights", [params[k] for k in of])
             to = iter(to)
             wp = _words(ctypes.c_void_p, [0 if t is None else next(to) for t in weights])
         if len(set(pp)) < len(pp):
@@ -941,20 +979,23 @@ class Buffer:
             beta1=betas[0], beta2=betas[1], eps=eps, weight_decay=weight_decay, bits=state.bits,
             p_bf16=pt == torch.bfloat16, g_bf16=gt == torch.bfloat16, seeded=seed is not None,
             seed=0 if seed is None else seed & 0xffffffff)
-        if torch.is_tensor(lr):
+        if isinstance(lr, torch.Tensor):
+            places.add(lr.get_device())
             cfg.lr_dev = _check_tensor(lr, "lr", torch.float32, (1,))
         else:
             cfg.lr = lr
-        if torch.is_tensor(step):
+        if isinstance(step, torch.Tensor):
+            places.add(step.get_device())
             cfg.step_dev = _check_tensor(step, "step", torch.int32, (1,))
         else:
             if not 1 <= step < 1 << 31:
                 raise ValueError(f"step: expected 1 or more, got {step}")
             cfg.step = step
         if norm is not None:
+            places.add(norm.get_device())
             cfg.norm = _check_tensor(norm, "norm", torch.float32, (1,))
             cfg.max_norm = max_norm
-        m, v, ms, vs = state._pointers()
+        _check_one_device(places)
         check(_lib.load().moonep_adamw(
             self._ctx, ctypes.byref(cfg), len(params), state._c_sizes,
             _words(ctypes.c_void_p, pp), _words(ctypes.c_void_p, gp), m, v, ms, vs, wp, _stream()),

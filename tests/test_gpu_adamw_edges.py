@@ -74,3 +74,21 @@ def test_eps_out_of_range(buf, eps, bits):
     with pytest.raises(MoonepError):
         buf.adamw([p], [g], state, lr=1.0, step=1, eps=eps, weight_decay=0.0)
     assert p.eq(1).all()
+
+
+def test_transposed_gradients_and_copies(buf):
+    """Refused, where views of the elements in order are taken."""
+    p = [torch.ones(8, 16, device="cuda"), torch.ones(5, device="cuda")]
+    g = [torch.ones(16, 8, device="cuda"), torch.ones(5, device="cuda")]
+    w = [torch.zeros(16, 8, device="cuda").bfloat16(), None]
+    state = buf.adamw_state(p)
+    kw = dict(lr=0.5, step=1, weight_decay=0.0)
+    with pytest.raises(ValueError):
+        buf.adamw(p, g, state, **kw)
+    flat = [t.view(-1) for t in g]
+    with pytest.raises(ValueError):
+        buf.adamw(p, flat, state, weights=w, **kw)
+    assert p[0].eq(1).all() and not state.tensors[0].any()
+    buf.adamw(p, flat, state, weights=[w[0].view(-1), None], **kw)
+    assert (p[0] - 0.5).abs().max().item() < 1e-5 and torch.equal(w[0].view(8, 16), p[0].bfloat16())
+    assert (p[1] - 0.5).abs().max().item() < 1e-5
