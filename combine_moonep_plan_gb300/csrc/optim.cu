@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, BITS == 8 && sizeof(P) == 4 ? 5 : 6)
   __shared__ Scalars sh;
   float clip = 1.0f;
   if (a.norm) {
-    const float norm = __ldg(a.norm);
+    const float norm = *a.norm;
     if (!(fabsf(norm) < INFINITY)) return;  // no step on gradients that are not finite
     clip = fminf(1.0f, __fdiv_rn(a.max_norm, norm));
   }

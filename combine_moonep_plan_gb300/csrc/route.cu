@@ -349,7 +349,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_backward_kernel(RouteBwdArg
 #pragma unroll
   for (int i = 0; i < V; i++) {
     cf[i] = a.coef && col + i < a.E
-                ? __ldg(a.coef + (int64_t)r * a.E + col + i) * kCoefScale : 0.0f;
+                ? a.coef[(int64_t)r * a.E + col + i] * kCoefScale : 0.0f;
     row[col + i] = 0.0f;
   }
   __syncwarp();
@@ -375,9 +375,9 @@ __global__ void __launch_bounds__(kWarps * 32) route_backward_kernel(RouteBwdArg
     for (int i = 0; i < kPicks; i++) {
       const int k = i * LP + lane % LP;
       if (k < a.K) {
-        pid[i] = __ldg(a.topk + t * a.K + k);
-        pw[i] = __ldg(a.w + t * a.K + k);
-        pd[i] = __ldg(a.dw + t * a.K + k);
+        pid[i] = a.topk[t * a.K + k];
+        pw[i] = a.w[t * a.K + k];
+        pd[i] = a.dw[t * a.K + k];
       }
     }
   };

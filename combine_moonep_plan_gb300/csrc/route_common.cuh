@@ -80,7 +80,7 @@ __device__ __forceinline__ void load_row(const float *z, int c, int E, bool vec,
   if (V % 4 == 0 && vec) {
 #pragma unroll
     for (int i = 0; i < V; i += 4) {
-      const float4 v = c + i < E ? __ldg((const float4 *)(z + c + i))
+      const float4 v = c + i < E ? *(const float4 *)(z + c + i)
                                  : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
       f[i] = v.x;
       f[i + 1] = v.y;
@@ -90,13 +90,13 @@ __device__ __forceinline__ void load_row(const float *z, int c, int E, bool vec,
     return;
   }
   if (V == 2 && vec) {
-    const float2 v = c < E ? __ldg((const float2 *)(z + c)) : make_float2(-INFINITY, -INFINITY);
+    const float2 v = c < E ? *(const float2 *)(z + c) : make_float2(-INFINITY, -INFINITY);
     f[0] = v.x;
     f[V - 1] = v.y;
     return;
   }
 #pragma unroll
-  for (int i = 0; i < V; i++) f[i] = c + i < E ? __ldg(z + c + i) : -INFINITY;
+  for (int i = 0; i < V; i++) f[i] = c + i < E ? z[c + i] : -INFINITY;
 }
 template <int V>
 __device__ __forceinline__ void load_row(const __nv_bfloat16 *z, int c, int E, bool vec,
@@ -105,7 +105,7 @@ __device__ __forceinline__ void load_row(const __nv_bfloat16 *z, int c, int E, b
 #pragma unroll
     for (int i = 0; i < V; i += 8) {
       if (c + i < E) {
-        bf16x8(__ldg((const uint4 *)(z + c + i)), f + i);
+        bf16x8(*(const uint4 *)(z + c + i), f + i);
       } else {
 #pragma unroll
         for (int j = 0; j < 8; j++) f[i + j] = -INFINITY;
@@ -116,7 +116,7 @@ __device__ __forceinline__ void load_row(const __nv_bfloat16 *z, int c, int E, b
   if (V % 4 == 0 && vec) {
 #pragma unroll
     for (int i = 0; i < V; i += 4) {
-      const uint2 v = c + i < E ? __ldg((const uint2 *)(z + c + i))
+      const uint2 v = c + i < E ? *(const uint2 *)(z + c + i)
                                 : make_uint2(0xff80ff80u, 0xff80ff80u);
       f[i] = __uint_as_float(v.x << 16);
       f[i + 1] = __uint_as_float(v.x & 0xffff0000u);
@@ -126,7 +126,7 @@ __device__ __forceinline__ void load_row(const __nv_bfloat16 *z, int c, int E, b
     return;
   }
   if (V == 2 && vec) {
-    const uint32_t v = c < E ? __ldg((const uint32_t *)(z + c)) : 0xff80ff80u;
+    const uint32_t v = c < E ? *(const uint32_t *)(z + c) : 0xff80ff80u;
     f[0] = __uint_as_float(v << 16);
     f[V - 1] = __uint_as_float(v & 0xffff0000u);
     return;

@@ -77,7 +77,7 @@ __device__ __forceinline__ void select_exact(const SelectArgs &a, const T *z, ui
       const double x = to_f(z[e]);
       double c = a.r.sigmoid ? 1.0 / (1.0 + exp(-x))
                              : (m == -INFINITY && x == x ? 0.0 : exp(x - (double)m) / Z);
-      if (a.bias) c += (double)__ldg(a.bias + e);
+      if (a.bias) c += (double)a.bias[e];
       row[e] = order_key64(c);
     }
     __syncwarp();
@@ -385,7 +385,7 @@ __global__ void __launch_bounds__(kWarps * 32, V <= 12 ? 4 : 2)
   const int gs = a.size;
   const float none = __uint_as_float(0x7fffffffu);  // left out: no comparison holds
   for (int e = threadIdx.x; e < 32 * V; e += blockDim.x)
-    bias[e] = a.bias && e < E ? __ldg(a.bias + e) : 0.0f;
+    bias[e] = a.bias && e < E ? a.bias[e] : 0.0f;
   for (int e = threadIdx.x; e < E; e += blockDim.x) cnt[e] = 0;
   __syncthreads();
   float sum[V];

@@ -1,0 +1,18 @@
+"""Every kernel may start while the kernel before it on the stream still writes
+(programmatic dependent launch), and the read-only path is defined for memory that
+nothing writes while the kernel runs: what was loaded through it before the wait, or
+lies in its cache, need not be what the kernel before wrote."""
+import os
+import re
+
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                    "combine_moonep_plan_gb300", "csrc")
+
+
+@pytest.mark.parametrize("name", ["optim.cu", "route.cu", "route_common.cuh", "select.cu", "wgrad.cu"])
+def test_no_load_through_the_read_only_path(name):
+    with open(os.path.join(CSRC, name)) as f:
+        code = re.sub(r"//[^\n]*|/\*.*?\*/", "", f.read(), flags=re.S)
+    assert not re.search(r"__ldg\b|ld\.global(\.\w+)*\.nc\b|__restrict__", code)
