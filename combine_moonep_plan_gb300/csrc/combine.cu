@@ -124,12 +124,12 @@ __global__ void __launch_bounds__(BT) combine_kernel(Args a, Rows rows) {
   // The next unit's dst entries are loaded one unit ahead, so their latency
   // overlaps the current unit's row loads.
   int32_t d_next = 0;
-  if (wid < units && lane < K) d_next = __ldg(a.dst + (wid / a.nchunk) * K + lane);
+  if (wid < units && lane < K) d_next = a.dst[(wid / a.nchunk) * K + lane];
   for (int64_t u = wid; u < units; u += nw) {
     const int64_t t = u / a.nchunk;
     const int c = (int)(u - t * a.nchunk);
     const int32_t d_cur = d_next;
-    if (u + nw < units && lane < K) d_next = __ldg(a.dst + ((u + nw) / a.nchunk) * K + lane);
+    if (u + nw < units && lane < K) d_next = a.dst[((u + nw) / a.nchunk) * K + lane];
     int64_t g = 0;
     // duplicate routes that the prologue folded into their primaries (the
     // same for every lane: route k's sign, broadcast)
@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(BT) combine_kernel(Args a, Rows rows) {
         set_status(a.status, MOONEP_ERR_PLAN);
         g = 0;
       }
-      if (c == 0 && a.w_out) a.w_out[t * K + lane] = __ldg(rows.weight(g, a.NvS));
+      if (c == 0 && a.w_out) a.w_out[t * K + lane] = *rows.weight(g, a.NvS);
     }
     const int v0 = c * 32 * U + lane;
     float acc[U][8];
@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(32) combine_staged_kernel(Args a, Rows rows) {
 
   // this lane's dst entry of unit u (route k = lane)
   auto dst_of = [&](int64_t u) -> int32_t {
-    return (u < units && lane < K) ? __ldg(a.dst + (u / nchunk) * K + lane) : 0;
+    return (u < units && lane < K) ? a.dst[(u / nchunk) * K + lane] : 0;
   };
   // issue unit u's K chunk copies into stage q (d: this lane's dst entry)
   auto issue = [&](int64_t u, int q, int32_t d) {
@@ -323,9 +323,9 @@ __global__ void __launch_bounds__(32) combine_staged_kernel(Args a, Rows rows) {
     const int64_t t = u / nchunk;
     const int c = (int)(u - t * nchunk);
     if (c == 0 && a.w_out && lane < K) {
-      int64_t g = decode_row(__ldg(a.dst + t * K + lane));
+      int64_t g = decode_row(a.dst[t * K + lane]);
       if (g >= a.total_rows) g = 0;
-      a.w_out[t * K + lane] = __ldg(rows.weight(g, a.NvS));
+      a.w_out[t * K + lane] = *rows.weight(g, a.NvS);
     }
     // this lane's 16-byte vectors of the chunk: lane + 32 * i
     const uint8_t *stage = stage_mem + q * stage_bytes;

@@ -9,13 +9,13 @@ namespace moonep {
 // Streaming read: every byte is read once, keep it out of L1.
 __device__ __forceinline__ uint4 ld_stream(const uint4 *p) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "l"(p));
   return v;
 }
 
-// Read once through L2 from memory this kernel also writes (no .nc path).
+// Read once through L2, as memory that this kernel also writes.
 __device__ __forceinline__ float4 ld_once_f4(const float4 *p) {
   float4 v;
   asm volatile("ld.global.L1::no_allocate.v4.f32 {%0, %1, %2, %3}, [%4];"

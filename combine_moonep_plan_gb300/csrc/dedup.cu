@@ -90,7 +90,7 @@ struct Group {
 __device__ __forceinline__ bool load_group(const Args &a, int j, int i, Group &g) {
   const int lane = threadIdx.x & 31;
   const int32_t *rec = a.groups + ((int64_t)j * a.NvS + i) * 3;
-  const int v = lane < 3 ? __ldg(rec + lane) : 0;
+  const int v = lane < 3 ? rec[lane] : 0;
   g.base = (int64_t)j * a.NvS;
   g.prim = __shfl_sync(0xffffffffu, v, 0);
   const int first = __shfl_sync(0xffffffffu, v, 1);
@@ -99,7 +99,7 @@ __device__ __forceinline__ bool load_group(const Args &a, int j, int i, Group &g
             first <= a.NvS - g.cnt;
   g.dup = 0;
   if (ok && lane < g.cnt) {
-    g.dup = __ldg(a.loffs + g.base + first + lane);
+    g.dup = a.loffs[g.base + first + lane];
     if (g.dup < 0 || g.dup >= a.NvS) ok = false;
   }
   ok = __all_sync(0xffffffffu, ok);
@@ -118,8 +118,8 @@ dedup_kernel(Args a) {
   const int64_t nw = ((int64_t)gridDim.x * kThreads) >> 5;
   // groups per rank (R <= 64: two ranks per lane), inclusive prefix p0 for
   // rank lane, p1 for rank lane + 32
-  int c0 = lane < a.R ? __ldg(a.dup_counts + 2 * lane + 1) : 0;
-  int c1 = lane + 32 < a.R ? __ldg(a.dup_counts + 2 * (lane + 32) + 1) : 0;
+  int c0 = lane < a.R ? a.dup_counts[2 * lane + 1] : 0;
+  int c1 = lane + 32 < a.R ? a.dup_counts[2 * (lane + 32) + 1] : 0;
   if (c0 < 0 || c0 > a.NvS || c1 < 0 || c1 > a.NvS) {
     set_status(a.status, MOONEP_ERR_PLAN);
     c0 = c1 = 0;

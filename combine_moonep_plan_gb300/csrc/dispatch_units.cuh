@@ -63,11 +63,10 @@ DispatchArgs dispatch_args(const moonep_ctx *ctx, const moonep_comm_plan *plan,
                            const uint16_t *hidden, const float *w_sk, int64_t ntok, int r0,
                            int seg_lo, int seg_hi, int U);
 
-// A word of the plan: through the read-only path when an earlier kernel
-// wrote it, through L2 when another block of the same launch did.
+// A word of the plan: through L2 when another block of the same launch wrote it.
 template <bool kSameLaunch>
 __device__ __forceinline__ int32_t plan_word(const int32_t *p) {
-  return kSameLaunch ? __ldcg(p) : __ldg(p);
+  return kSameLaunch ? __ldcg(p) : *p;
 }
 
 // Units wid, wid + nw, ... of the launch (wid: this warp, nw: warps of the
@@ -110,7 +109,7 @@ __device__ __forceinline__ void dispatch_units(const DispatchArgs &a, const Rows
         if (v < a.H8) x[i] = ld_stream(src + v);
       }
       float wv = 0.0f;
-      if (c == 0 && lane < K && wts) wv = __ldg(a.w_sk + t * K + lane);
+      if (c == 0 && lane < K && wts) wv = a.w_sk[t * K + lane];
       int64_t g = -1;
       if (lane < K) {
         const int64_t gg = decode_row(d_cur);

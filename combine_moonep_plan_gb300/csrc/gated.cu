@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(kThreads) gated_kernel(GatedArgs a) {
   const int used = used_rows(a.cu, blockIdx.y, a.EB, a.NvS);
   for (int64_t r = (int64_t)blockIdx.x * kRows + sub; r < used; r += (int64_t)gridDim.x * kRows) {
     const int64_t row = (int64_t)blockIdx.y * a.NvS + r;
-    const float w = a.w ? __ldg(a.w + row) : 1.0f;
+    const float w = a.w ? a.w[row] : 1.0f;
     for (int c0 = 0; c0 < a.F8; c0 += kLanes * 2) {
       uint4 gv[2] = {}, uv[2] = {};
 #pragma unroll
@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(kThreads) gated_backward_kernel(GatedArgs a) {
   const int used = used_rows(a.cu, blockIdx.y, a.EB, a.NvS);
   for (int64_t r = (int64_t)blockIdx.x * kRows + sub; r < used; r += (int64_t)gridDim.x * kRows) {
     const int64_t row = (int64_t)blockIdx.y * a.NvS + r;
-    const float w = a.w ? __ldg(a.w + row) : 1.0f;
+    const float w = a.w ? a.w[row] : 1.0f;
     float sum = 0.0f;
     for (int c0 = 0; c0 < a.F8; c0 += kLanes * 2) {
       uint4 dv[2];
@@ -132,10 +132,10 @@ __global__ void __launch_bounds__(kThreads) gated_backward_kernel(GatedArgs a) {
         if (c < a.F8) {
           const int64_t u = row * a.F8 + c;
           dv[b] = ld_stream((const uint4 *)a.d_act + u);
-          gv[b] = __ldg((const uint2 *)a.g8 + u);
-          uv[b] = __ldg((const uint2 *)a.u8 + u);
-          gs[b] = __ldg(a.gs + (u >> 2));
-          us[b] = __ldg(a.us + (u >> 2));
+          gv[b] = ((const uint2 *)a.g8)[u];
+          uv[b] = ((const uint2 *)a.u8)[u];
+          gs[b] = a.gs[u >> 2];
+          us[b] = a.us[u >> 2];
         }
       }
 #pragma unroll

@@ -250,7 +250,10 @@ int occupancy_dedup(bool fold);
 // that kernel has completed and its memory is visible, before touching any
 // memory; then pdl_launch_dependents() lets the next kernel be scheduled.
 // Back-to-back launches (the decode path's plan -> dispatch -> combine) then
-// overlap one kernel's launch latency with the previous one's tail.
+// overlap one kernel's launch latency with the previous one's tail.  So they
+// read nothing through the read-only path (__ldg, ld.global.nc, const pointers that
+// are __restrict__): it is defined for memory that no one writes while the kernel
+// runs, and the kernel may have started while the one before still wrote.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 __device__ __forceinline__ void pdl_launch_dependents() {

@@ -100,8 +100,8 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(const uint8_t *pac
 #pragma unroll
     for (int b = 0; b < kBatch; b++)
       if (u0 + b * kThreads < units) {
-        w[b] = __ldg((const uint32_t *)packed + u0 + b * kThreads);
-        s[b] = __ldg(scales + ((u0 + b * kThreads) >> 2));
+        w[b] = ((const uint32_t *)packed)[u0 + b * kThreads];
+        s[b] = scales[(u0 + b * kThreads) >> 2];
       }
 #pragma unroll
     for (int b = 0; b < kBatch; b++) {

@@ -931,7 +931,7 @@ __global__ void __launch_bounds__(kFusedThreads, 1) plan_fused_kernel(FusedArgs 
 #pragma unroll
     for (int c = 0; c < items; c++) {
       const int i = wbase + c * lpc + lane;
-      e_reg[c] = lane < lpc && i < C ? __ldg(src + i) : -1;
+      e_reg[c] = lane < lpc && i < C ? src[i] : -1;
     }
     for (int i = tid; i < kFusedWarps * E; i += kFusedThreads) h[i] = 0;
     __syncthreads();
@@ -983,7 +983,7 @@ __global__ void __launch_bounds__(kFusedThreads, 1) plan_fused_kernel(FusedArgs 
   // this block's first tokens_per_expert word to check, loaded now so that
   // its latency overlaps the meeting
   const int i_tpe = g * kFusedThreads + tid;
-  const int tpe0 = (a.tpe != nullptr && !local && i_tpe < R * E) ? __ldg(a.tpe + i_tpe) : 0;
+  const int tpe0 = (a.tpe != nullptr && !local && i_tpe < R * E) ? a.tpe[i_tpe] : 0;
 
   // 3. all blocks arrive; each waits for the rest
   if (tid == 0 && dsm) s_ok = 1;
@@ -1020,9 +1020,9 @@ __global__ void __launch_bounds__(kFusedThreads, 1) plan_fused_kernel(FusedArgs 
       // the gathered histograms are the totals; this rank's recount checks
       // its own row, a slice per block (a mismatch latches its error; the
       // tables stay those of the gathered counts, which every rank shares)
-      for (int i = tid; i < R * E; i += kFusedThreads) sCnt[i] = __ldg(a.hist_all + i);
+      for (int i = tid; i < R * E; i += kFusedThreads) sCnt[i] = a.hist_all[i];
       for (int e = g * kFusedThreads + tid; e < E; e += nblk * kFusedThreads)
-        if (__ldcg(tot_in + e) != __ldg(a.hist_all + (int64_t)r * E + e))
+        if (__ldcg(tot_in + e) != a.hist_all[(int64_t)r * E + e])
           set_status(a.status, MOONEP_ERR_HIST_MISMATCH);
     } else if (dsm) {
       // rank j's totals: the sum of its tiles' counts (blocks j*tpr ...)
@@ -1050,7 +1050,7 @@ __global__ void __launch_bounds__(kFusedThreads, 1) plan_fused_kernel(FusedArgs 
     // latches its error but the plan stands (it is built from the recount)
     if (a.tpe != nullptr && !local)
       for (int i = i_tpe; i < R * E; i += nblk * kFusedThreads)
-        if (sCnt[i] != (i == i_tpe ? tpe0 : __ldg(a.tpe + i)))
+        if (sCnt[i] != (i == i_tpe ? tpe0 : a.tpe[i]))
           set_status(a.status, MOONEP_ERR_HIST_MISMATCH);
     __syncthreads();
   }
@@ -1157,8 +1157,8 @@ constexpr int kDupThreads = kDupTile;
 
 // The group of row w of rank j: has = 1 when w is a primary row with
 // duplicates on its rank (dupflag names its route), cnt = their number.
-__device__ __forceinline__ void dup_row(const PlanDims &d, const int32_t *__restrict__ dst,
-                                        const int32_t *__restrict__ dupflag, int j, int w,
+__device__ __forceinline__ void dup_row(const PlanDims &d, const int32_t *dst,
+                                        const int32_t *dupflag, int j, int w,
                                         int &has, int &cnt, int64_t &tb, int &k) {
   has = cnt = 0;
   tb = 0;
@@ -1200,8 +1200,8 @@ __device__ __forceinline__ void dup_block_scan(int has, int cnt, int &hx, int &c
 
 // Pass 1: per (tile, rank) block, the tile's group and duplicate counts.
 __global__ void __launch_bounds__(kDupThreads)
-plan_dup_count_kernel(PlanDims d, const int32_t *__restrict__ dst,
-                      const int32_t *__restrict__ dupflag, int32_t *__restrict__ tiles) {
+plan_dup_count_kernel(PlanDims d, const int32_t *dst,
+                      const int32_t *dupflag, int32_t *tiles) {
   pdl_wait();
   pdl_launch_dependents();
   const int t = blockIdx.x, j = blockIdx.y, T = gridDim.x;
@@ -1219,9 +1219,9 @@ plan_dup_count_kernel(PlanDims d, const int32_t *__restrict__ dst,
 // Pass 2: every block adds up the counts of the rank's earlier tiles, then
 // writes its groups (ascending primary row) and their duplicate rows (k order).
 __global__ void __launch_bounds__(kDupThreads)
-plan_dup_write_kernel(PlanDims d, const int32_t *__restrict__ dst,
-                      const int32_t *__restrict__ dupflag, const int32_t *__restrict__ tiles,
-                      int32_t *__restrict__ dup_groups, int32_t *__restrict__ dup_loffs) {
+plan_dup_write_kernel(PlanDims d, const int32_t *dst,
+                      const int32_t *dupflag, const int32_t *tiles,
+                      int32_t *dup_groups, int32_t *dup_loffs) {
   pdl_wait();
   pdl_launch_dependents();
   __shared__ int base[2][32];

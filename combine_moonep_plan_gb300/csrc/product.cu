@@ -238,14 +238,14 @@ __device__ __noinline__ uint4 load_bytes(const uint8_t *base, const uint8_t *end
   for (int i = 0; i < 5; i++) {
     const uint8_t *q = w0 + 4 * i;
     w[i] = 0;
-    if (q < p + need && q >= base && q + 4 <= end) w[i] = __ldg((const uint32_t *)q);
+    if (q < p + need && q >= base && q + 4 <= end) w[i] = *(const uint32_t *)q;
   }
   if (w0 < base || w0 + 20 > end) {
     // the tensor's first or last word: what of it lies inside
     for (int i = 0; i < 20; i++) {
       const uint8_t *q = w0 + i, *v = w0 + (i & ~3);
       if (q >= base && q < end && !(v >= base && v + 4 <= end)) {
-        const uint32_t x = (uint32_t)__ldg(q) << (8 * (i & 3));
+        const uint32_t x = (uint32_t)*q << (8 * (i & 3));
 #pragma unroll
         for (int j = 0; j < 5; j++)
           if (j == i >> 2) w[j] |= x;
@@ -269,7 +269,7 @@ __device__ __forceinline__ uint4 load_scales(const uint8_t *base, int64_t total,
   const uint32_t one = 0x7f7f7f7fu;
   if (!there || c >= n) return make_uint4(one, one, one, one);
   const uint8_t *p = base + row * pitch + c;
-  if (vec) return __ldg((const uint4 *)p);
+  if (vec) return *(const uint4 *)p;
   return load_bytes(base, base + total, p, min(16, n - c));
 }
 
