@@ -68,15 +68,18 @@ __device__ __forceinline__ void select_exact(const SelectArgs &a, const T *z, ui
 #pragma unroll
       for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
       Z = 0.0;
-      if (m > -INFINITY)
-        for (int e = lane; e < E; e += 32) Z += exp((double)to_f(z[e]) - (double)m);
+      for (int e = lane; e < E; e += 32) {
+        const double x = to_f(z[e]);
+        Z += m > -INFINITY ? exp(x - (double)m) : x == x ? 0.0 : x;
+      }
 #pragma unroll
       for (int o = 16; o; o >>= 1) Z += __shfl_xor_sync(0xffffffffu, Z, o);
     }
     for (int e = lane; e < E; e += 32) {
       const double x = to_f(z[e]);
+      // no share where every logit is -inf, none that is a number beside a NaN
       double c = a.r.sigmoid ? 1.0 / (1.0 + exp(-x))
-                             : (m == -INFINITY && x == x ? 0.0 : exp(x - (double)m) / Z);
+                             : (m > -INFINITY || Z != Z ? exp(x - (double)m) / Z : 0.0);
       if (a.bias) c += (double)a.bias[e];
       row[e] = order_key64(c);
     }
@@ -433,6 +436,9 @@ __global__ void __launch_bounds__(kWarps * 32, V <= 12 ? 4 : 2)
         Z += p[i];
       }
       nan = Z != Z || odd;  // a NaN among the lane's scores, or its biases
+      if (!sigmoid && m == -INFINITY)  // scores of 0, whatever the logits
+#pragma unroll
+        for (int i = 0; i < V; i++) nan |= c[i] != c[i];
       if (a.r.part_p || !sigmoid) {
         Z = warp_sum(Z);
         inv = Z == 0.0f ? 0.0f : 1.0f / Z;

@@ -46,7 +46,8 @@ def test_shapes_of_gradients_and_copies():
     for good in ([view(4, 6), view(24), view(2, 3, 4), one[0]], [view(24)] * 3 + [one],
                  [view(2, 3, 4), view(4, 6), view(4, 6), one]):
         _check_shapes(good, "grads", p)
-    for bad in ([view(6, 4), view(24), view(2, 3, 4), one], [view(4, 6), view(24), view(2, 4, 3), one],
+    for bad in ([view(6, 4), view(24), view(2, 3, 4), one],
+                [view(4, 6), view(24), view(2, 4, 3), one],
                 [view(1, 24), view(24), view(2, 3, 4), one]):
         with pytest.raises(ValueError):
             _check_shapes(bad, "grads", p)
