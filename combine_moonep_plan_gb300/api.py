@@ -620,8 +620,9 @@ class Buffer:
         With bias [E] fp32 the picks are those of the largest score + bias
         (softmax: share + bias), with groups > 1 among the top_groups groups
         (default: all) of neighbouring experts whose largest such value ("max")
-        or sum of the two largest ("top2") is best.  Weights are made of the
-        scores alone and times `scale`: normalised over the picks, or with
+        or sum of the two largest ("top2") is best.  A bias of -inf shuts an
+        expert out (a finite one of -10^5 or so does as well, but every row
+        then takes the slow way).  Weights are made of the scores alone and times `scale`: normalised over the picks, or with
         renormalize=False as they are (softmax: the shares among all
         experts)."""
         R, S, K, E = dims = self._dims

@@ -31,7 +31,9 @@
 // eight values of a thread share took 8-bit moments from 2.44 to 1.86 ms; five
 // blocks per SM in place of four (a few registers spilled) to 1.81, bf16
 // parameters with six from 2.10 to 1.87.  The norm reads at 7.3 TB/s (fp32) and
-// 6.3 (bf16).
+// 6.3 (bf16).  Tensors that do not start on 16 bytes go element by element: without
+// copies 2.97 for 2.80 ms (fp32, 32 bits), 2.20 for 1.64 (fp32, 8 bits at random),
+// 2.37 for 1.89 (bf16, 8 bits at random).
 #include <cuda_bf16.h>
 #include <math.h>
 

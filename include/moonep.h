@@ -435,7 +435,8 @@ int moonep_route_backward(moonep_ctx *ctx, const void *logits, int logits_bf16,
  * their largest (sums of two are those of c).
  *   w_sk   scale a of the picks over their sum (renormalize; 0 when that is 0),
  *          or scale a; the bias weighs nothing
- * Everything else as moonep_route.  bias: [E] fp32 in device memory or NULL;
+ * Everything else as moonep_route.  bias: [E] fp32 in device memory or NULL; -inf
+ * shuts an expert out (a large finite one does too, at the cost of the fast way);
  * E % groups == 0, 1 <= top_groups <= groups, K <= top_groups * (E / groups). */
 #define MOONEP_GROUP_MAX 0
 #define MOONEP_GROUP_TOP2 1
